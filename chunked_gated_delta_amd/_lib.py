@@ -41,6 +41,32 @@ class KdaOpts(ctypes.Structure):
                 ("ev_begin", ctypes.c_void_p), ("ev_end", ctypes.c_void_p)]
 
 
+class KdaStride(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class KdaGdr(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "Hk", "Hv", "T", "dk", "dv", "n_seq")] + \
+        [("dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("g_min", ctypes.c_float), ("scale", ctypes.c_float)] + \
+        [(n, KdaStride) for n in ("q", "k", "v", "w", "beta")]
+
+
+class KdaGdrGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dq", "dk", "dv", "dw", "dbeta", "dS0")] + \
+        [(n, KdaStride) for n in ("sq", "sk", "sv", "sw", "sbeta")]
+
+
+class KdaNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "H", "T", "D")] + \
+        [("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32), ("act", ctypes.c_int32), ("alpha", ctypes.c_float),
+         ("eps", ctypes.c_float)] + [(n, KdaStride) for n in ("x", "z", "residual")]
+
+
+class KdaNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dz", "dresidual", "dweight", "dnext_weight")] + \
+        [(n, KdaStride) for n in ("sx", "sz", "sresidual")]
+
+
 class KdaError(RuntimeError):
     def __init__(self, code: int, where: str, hip_text: str = ""):
         self.code = code
@@ -87,6 +113,21 @@ def load():
     lib.kda_workspace_bytes.restype = sz
     lib.kda_workspace_bytes_ex.argtypes = [ctypes.POINTER(KdaShape), i32, ctypes.POINTER(KdaOpts)]
     lib.kda_workspace_bytes_ex.restype = sz
+    i64, gdr, norm, st = ctypes.c_int64, ctypes.POINTER(KdaGdr), ctypes.POINTER(KdaNorm), ctypes.POINTER(KdaStride)
+    lib.kda_gdr_chunk_fwd.argtypes = [vp] * 7 + [gdr, vp, st, vp, vp, sz, vp]
+    lib.kda_gdr_chunk_fwd.restype = i32
+    lib.kda_gdr_chunk_bwd.argtypes = [vp] * 7 + [gdr, vp, st, vp, ctypes.POINTER(KdaGdrGrads), vp, sz, vp]
+    lib.kda_gdr_chunk_bwd.restype = i32
+    lib.kda_gdr_workspace_bytes.argtypes = [gdr, i32]
+    lib.kda_gdr_workspace_bytes.restype = sz
+    lib.kda_gdr_decode.argtypes = [vp] * 6 + [i64, vp, gdr, vp, st, vp]
+    lib.kda_gdr_decode.restype = i32
+    lib.kda_norm_fwd.argtypes = [vp] * 5 + [norm, vp, st, vp, st, vp]
+    lib.kda_norm_fwd.restype = i32
+    lib.kda_norm_bwd.argtypes = [vp] * 5 + [norm, vp, st, vp, st, ctypes.POINTER(KdaNormGrads), vp, sz, vp]
+    lib.kda_norm_bwd.restype = i32
+    lib.kda_norm_bwd_workspace_bytes.argtypes = [norm]
+    lib.kda_norm_bwd_workspace_bytes.restype = sz
     lib.kda_strerror.argtypes = [i32]
     lib.kda_strerror.restype = ctypes.c_char_p
     lib.kda_last_hip_error.argtypes = []

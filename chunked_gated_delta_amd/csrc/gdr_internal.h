@@ -1,0 +1,272 @@
+// Internal declarations of the head-gated delta rule (one log-decay per token and head) and of the
+// norms around a block: parameters, launchers and the operand fragments of the matrix-core kernels.
+//
+// Chunk form (C = 64 tokens; per sequence and value head, S entering the chunk, G the chunk's inclusive
+// prefix of the log-decay, D_rj = e^{G_r - G_j}, gam = e^G, eta = e^{G_last - G}):
+//   A = strict_lower(K K^T . D)      P = scale lower(Q K^T . D)      T' = (I + A diag(beta))^{-1}
+//   E = V - gam K S     F = T' E     U = beta F
+//   O = scale gam Q S + P U          S <- e^{G_last} S + K^T (eta U)
+// One decay per head keeps it out of the operands: K K^T and Q K^T are products of the inputs as they
+// are (bf16 products are exact), and every decay factor is at most 1 and multiplies an fp32 result.
+#pragma once
+
+#include "kda_mfma_util.h"
+
+namespace kda {
+
+constexpr int kGdrChunk = 64;
+
+struct GdrParams {
+  const void *q, *k, *v, *w, *beta;
+  kda_stride_t sq, sk, sv, sw, sb;
+  const float* S0;              // nullable
+  const int32_t* seq_start;     // packed sequences: n_seq + 1 offsets; null: every batch row is a sequence
+  int64_t B, T, n_seq;          // n_seq = B when not packed
+  int Hk, Hv, dk, dv;
+  int dtype, gate;
+  float g_min, scale;
+  void* o;
+  kda_stride_t so;
+  float* S_final;               // nullable
+  // backward
+  const void* dO;
+  kda_stride_t sdo;
+  const float* dSf;             // nullable
+  void *dq, *dk_, *dv_, *dw, *dbeta;
+  kda_stride_t sdq, sdk, sdv, sdw, sdb;
+  float* dS0;                   // nullable
+  // workspace sections, one block per (chunk slot, head); see gdr_layout
+  char *ws_gate, *ws_ti, *ws_tt, *ws_p, *ws_kt, *ws_qt, *ws_s, *ws_ds, *ws_f, *ws_db;
+};
+
+struct GdrStepParams {
+  const void *q, *k, *v, *w, *beta;
+  kda_stride_t sq, sk, sv, sw, sb, so;
+  const int32_t* slots;         // null: row b uses state b
+  float* S;
+  void* o;
+  int64_t B, T, n_slots;
+  int Hk, Hv, dk, dv;
+  int dtype, gate;
+  float g_min, scale;
+};
+
+struct NormParams {
+  const void *x, *z, *res, *weight, *weight2;
+  kda_stride_t sx, sz, sr, ss, sy;
+  void *s, *y;
+  // backward: cotangents and gradients
+  const void *ds, *dy;
+  void *dx, *dz, *dres, *dweight, *dweight2;
+  kda_stride_t sds, sdy, sdx, sdz, sdr;
+  float* partial;               // workspace: per-workgroup sums of the weights' gradients
+  int64_t B, H, T, D;
+  int dtype, wdtype, act;
+  float alpha, eps;
+};
+
+int64_t gdr_slots(int64_t B, int64_t T, int64_t n_seq, bool packed);
+// sets the workspace sections of p from base (may be null) and returns the bytes needed
+size_t gdr_layout(GdrParams& p, void* base, bool bwd);
+hipError_t launch_gdr_fwd(const GdrParams& p, hipStream_t s);
+hipError_t launch_gdr_bwd(const GdrParams& p, hipStream_t s);
+hipError_t launch_gdr_prep(const GdrParams& p, hipStream_t s, bool bwd);
+hipError_t launch_gdr_scan(const GdrParams& p, hipStream_t s, bool states);
+hipError_t launch_gdr_rscan(const GdrParams& p, hipStream_t s);
+hipError_t launch_gdr_grad(const GdrParams& p, hipStream_t s);
+hipError_t launch_gdr_step(const GdrStepParams& p, hipStream_t s);
+size_t norm_bwd_workspace_bytes(const NormParams& p);
+hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s);
+
+// ---------------------------------------------------------------- workspace blocks
+
+// per (slot, value head), fp32: gam, eta, beta, and G as a sum of two floats (64 each), then e^{G_last}
+constexpr int kGateGam = 0, kGateEta = 64, kGateBeta = 128, kGateHi = 192, kGateLo = 256, kGateLast = 320;
+constexpr int kGateFloats = 336;
+// a 64 x 64 triangular matrix as A operands: 16 x 32 fragments of the row tiles that hold any of it
+constexpr int kTriFrags = 6;
+__host__ __device__ constexpr int lower_frag(int tile, int ks) { return tile < 2 ? tile : 2 + 2 * (tile - 2) + ks; }
+__host__ __device__ constexpr int upper_frag(int tile, int ks) { return tile < 2 ? 2 * tile + ks : 4 + (tile - 2); }
+
+// ---------------------------------------------------------------- sequences and chunk slots
+
+// A packed batch keeps its chunks at slot floor(start / 64) + sequence, which leaves room for every
+// sequence's partly filled chunk without a prefix sum over the lengths.  Offsets are clamped into
+// [0, T], so that offsets out of order cannot address anything out of range.
+struct GdrSeq {
+  int64_t row, t0, len, slot0, n_chunks;   // batch row, first token, tokens, first chunk slot, chunks
+};
+
+__device__ __forceinline__ int64_t clamp_off(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+__device__ __forceinline__ GdrSeq gdr_seq(const GdrParams& p, int64_t s) {
+  GdrSeq q;
+  if (!p.seq_start) {
+    q.row = s;
+    q.t0 = 0;
+    q.len = p.T;
+    q.n_chunks = (p.T + kGdrChunk - 1) / kGdrChunk;
+    q.slot0 = s * q.n_chunks;
+  } else {
+    const int64_t a = clamp_off(p.seq_start[s], 0, p.T), e = clamp_off(p.seq_start[s + 1], a, p.T);
+    q.row = 0;
+    q.t0 = a;
+    q.len = e - a;
+    q.n_chunks = (q.len + kGdrChunk - 1) / kGdrChunk;
+    q.slot0 = a / kGdrChunk + s;
+  }
+  return q;
+}
+
+// the sequence whose chunks hold this slot, the chunk in *chunk; false where the slot holds none
+__device__ __forceinline__ bool gdr_find(const GdrParams& p, int64_t slot, GdrSeq* seq, int64_t* chunk) {
+  int64_t lo = 0;
+  if (!p.seq_start) {
+    lo = slot / ((p.T + kGdrChunk - 1) / kGdrChunk);
+  } else {
+    int64_t hi = p.n_seq - 1;   // the last sequence whose first slot is not behind this one
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) / 2;
+      if (clamp_off(p.seq_start[mid], 0, p.T) / kGdrChunk + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+  }
+  *seq = gdr_seq(p, lo);
+  *chunk = slot - seq->slot0;
+  return *chunk >= 0 && *chunk < seq->n_chunks;
+}
+
+// log-decay of one gate value.  Below -1e4 it is held there (e^-1e4 is 0 already), so that a decay
+// of -infinity, a reset of the state, leaves differences of prefixes defined; NaN stays.
+__device__ __forceinline__ float gdr_gate(float w, int gate, float g_min) {
+  float g = w;
+  if (gate == KDA_GATE_BOUNDED) g = gate_f32(w, g_min, 0);
+  if (gate == KDA_GATE_SOFTPLUS) g = gate_f32(w, 0.f, 1);
+  return g < -1e4f ? -1e4f : g;
+}
+// its derivative by w
+__device__ __forceinline__ float gdr_gate_grad(float w, int gate, float g_min) {
+  if (gate == KDA_GATE_LOG) return 1.f;
+  const float s = 1.f / (1.f + expf(-w));
+  return gate == KDA_GATE_BOUNDED ? g_min * s * (1.f / (1.f + expf(w))) : -s;
+}
+
+// ---------------------------------------------------------------- operand fragments
+
+// A fragment is 8 values a lane: of the A operand row li, of the B operand column li, at contraction
+// places 8g .. 8g + 7 (lane = 16 g + li) of a step of 32.  bf16 inputs are one register group, exact.
+// Values that the kernel computes (E, U, the state, the triangular factors) are carried as the sum of
+// two bf16 (hi + lo: 16 bits of fraction, relative error at most 2^-17), so products with an input
+// take two matrix instructions and keep the fp32 state and its adjoint to fp32-like accuracy.
+// fp32 inputs use v_mfma_f32_16x16x4_f32 on the same 8 values, one place of each lane group at a time.
+template <typename T> struct Frags;
+struct OpBf16 {
+  bf16x8 hi, lo;
+};
+template <> struct Frags<uint16_t> {
+  using In = bf16x8;
+  using Op = OpBf16;
+  static constexpr int kInPlanes = 1;
+};
+template <> struct Frags<float> {
+  using In = float8v;
+  using Op = float8v;
+  static constexpr int kInPlanes = 2;
+};
+constexpr int kPlane = 64 * 16;   // 16 bytes a lane; an Op fragment is two planes (hi and lo, or fp32 halves)
+
+__device__ __forceinline__ floatx4 mma(bf16x8 a, bf16x8 b, floatx4 c) { return mfma(a, b, c); }
+__device__ __forceinline__ floatx4 mma(bf16x8 a, const OpBf16& b, floatx4 c) { return mfma(a, b.lo, mfma(a, b.hi, c)); }
+__device__ __forceinline__ floatx4 mma(const OpBf16& a, bf16x8 b, floatx4 c) { return mfma(a.lo, b, mfma(a.hi, b, c)); }
+__device__ __forceinline__ floatx4 mma(const OpBf16& a, const OpBf16& b, floatx4 c) {
+  return mfma(a.hi, b.lo, mfma(a.lo, b.hi, mfma(a.hi, b.hi, c)));   // lo lo is below the splits' own error
+}
+__device__ __forceinline__ floatx4 mma(const float8v& a, const float8v& b, floatx4 c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ void zero_frag(bf16x8& f) { f = bf16x8{}; }
+__device__ __forceinline__ void zero_frag(float8v& f) { f = float8v{}; }
+
+// 8 consecutive values of a row in memory (16-byte aligned)
+__device__ __forceinline__ bf16x8 load_row8(const uint16_t* p) { return ld8(p); }
+__device__ __forceinline__ float8v load_row8(const float* p) {
+  const floatx4 a = *reinterpret_cast<const floatx4*>(p), b = *reinterpret_cast<const floatx4*>(p + 4);
+  return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// fragments stored plane by plane (LDS or workspace)
+template <typename F> __device__ __forceinline__ F load_frag(const char* base, int lane);
+template <> __device__ __forceinline__ bf16x8 load_frag<bf16x8>(const char* base, int lane) { return ld8(base + lane * 16); }
+template <> __device__ __forceinline__ OpBf16 load_frag<OpBf16>(const char* base, int lane) {
+  return OpBf16{ld8(base + lane * 16), ld8(base + kPlane + lane * 16)};
+}
+template <> __device__ __forceinline__ float8v load_frag<float8v>(const char* base, int lane) {
+  const floatx4 a = *reinterpret_cast<const floatx4*>(base + lane * 16);
+  const floatx4 b = *reinterpret_cast<const floatx4*>(base + kPlane + lane * 16);
+  return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+__device__ __forceinline__ OpBf16 make_op(const float8v& f, uint16_t) {
+  OpBf16 r;
+  const bf16x8v hi = __builtin_convertvector(f, bf16x8v);
+  r.hi = __builtin_bit_cast(bf16x8, hi);
+  r.lo = __builtin_bit_cast(bf16x8, __builtin_convertvector(f - __builtin_convertvector(hi, float8v), bf16x8v));
+  return r;
+}
+__device__ __forceinline__ float8v make_op(const float8v& f, float) { return f; }
+
+__device__ __forceinline__ void store_frag(char* base, int lane, const bf16x8& f) { *reinterpret_cast<bf16x8*>(base + lane * 16) = f; }
+__device__ __forceinline__ void store_frag(char* base, int lane, const OpBf16& f) {
+  store_frag(base, lane, f.hi);
+  store_frag(base + kPlane, lane, f.lo);
+}
+__device__ __forceinline__ void store_frag(char* base, int lane, const float8v& f) {
+  *reinterpret_cast<floatx4*>(base + lane * 16) = floatx4{f[0], f[1], f[2], f[3]};
+  *reinterpret_cast<floatx4*>(base + kPlane + lane * 16) = floatx4{f[4], f[5], f[6], f[7]};
+}
+
+// A result tile (lane (li, g): rows 4g .. 4g + 3 of column li) as the half `half` (rows 0-15 or 16-31)
+// of a fragment's contraction places: 4 consecutive places of one lane, one 8- or 16-byte write a plane
+__device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, uint16_t) {
+  char* at = frag + (li + 16 * (2 * half + (g >> 1))) * 16 + (g & 1) * 8;
+  const uint32_t h0 = pk_bf16(x[0], x[1]), h1 = pk_bf16(x[2], x[3]);
+  *reinterpret_cast<u32x2v*>(at) = u32x2v{h0, h1};
+  const uint32_t l0 = pk_bf16(x[0] - lo_bf16(h0), x[1] - hi_bf16(h0)), l1 = pk_bf16(x[2] - lo_bf16(h1), x[3] - hi_bf16(h1));
+  *reinterpret_cast<u32x2v*>(at + kPlane) = u32x2v{l0, l1};
+}
+__device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, float) {
+  *reinterpret_cast<floatx4*>(frag + (g & 1) * kPlane + (li + 16 * (2 * half + (g >> 1))) * 16) = x;
+}
+// the same for values that are inputs (one bf16 plane, exact)
+__device__ __forceinline__ void put_in(char* frag, int half, int li, int g, floatx4 x, uint16_t) {
+  *reinterpret_cast<u32x2v*>(frag + (li + 16 * (2 * half + (g >> 1))) * 16 + (g & 1) * 8) = u32x2v{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+}
+__device__ __forceinline__ void put_in(char* frag, int half, int li, int g, floatx4 x, float t) { put_op(frag, half, li, g, x, t); }
+
+__device__ __forceinline__ floatx4 ld4f(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
+
+// 4 consecutive values of a row in memory (8-byte aligned bf16, 16-byte aligned fp32)
+__device__ __forceinline__ floatx4 load_row4(const uint16_t* p) {
+  const u32x2v x = *reinterpret_cast<const u32x2v*>(p);
+  return floatx4{lo_bf16(x[0]), hi_bf16(x[0]), lo_bf16(x[1]), hi_bf16(x[1])};
+}
+__device__ __forceinline__ floatx4 load_row4(const float* p) { return ld4f(p); }
+__device__ __forceinline__ void store_row4(uint16_t* p, floatx4 x) {
+  *reinterpret_cast<u32x2v*>(p) = u32x2v{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+}
+__device__ __forceinline__ void store_row4(float* p, floatx4 x) { *reinterpret_cast<floatx4*>(p) = x; }
+
+// Workgroups of one (sequence, head) read the same operands: they get blocks of one XCD (block b runs
+// on XCD b mod 8), so that its L2 serves all but the first.  Returns false for a block without work.
+__device__ __forceinline__ bool gdr_block(int64_t block, int64_t units, int parts, int64_t* unit, int* part) {
+  const int64_t j = block >> 3;
+  *unit = (block & 7) + 8 * (j / parts);
+  *part = (int)(j % parts);
+  return *unit < units;
+}
+inline int64_t gdr_blocks(int64_t units, int parts) { return (units + 7) / 8 * 8 * parts; }
+
+}  // namespace kda

@@ -255,6 +255,117 @@ KDA_API size_t kda_workspace_bytes(const kda_shape_t* shape, int chunk);
  * returns (size_t)-1). */
 KDA_API size_t kda_workspace_bytes_ex(const kda_shape_t* shape, int chunk, const kda_opts_t* opts);
 
+/* ------------------------------------------------------------------------------------------------
+ * The gated delta rule with ONE log-decay per token and head ("head-gated"), the sibling of the
+ * per-channel rule above, for query/key heads shared by several value heads, packed sequences and
+ * strided tensors.  Per sequence and value head h, with query/key head h / (Hv / Hk):
+ *
+ *     S <- e^{g_t} S;   f_t = v_t - S^T k_t;   S <- S + beta_t k_t f_t^T;   o_t = scale S^T q_t
+ *
+ *   g_t = g_min sigmoid(w_t)  (KDA_GATE_BOUNDED, g_min finite and <= 0),
+ *         -softplus(w_t)      (KDA_GATE_SOFTPLUS), or
+ *         w_t                 (KDA_GATE_LOG: w is the log-decay itself, <= 0; -infinity resets the state).
+ *
+ * Tensors (all of dtype, element strides given, the last dimension contiguous):
+ *   q, k [B,Hk,T,dk];  v, o [B,Hv,T,dv];  w, beta [B,Hv,T];  states [n,Hv,dk,dv], dense, fp32.
+ * Rows of q, k, v, o (and of their gradients) lie on 16-byte places.  Input strides may be 0 (a
+ * broadcast dimension); gradients are those of every element as if it were its own.  An output may
+ * not hold one place twice, nor reach into the span of an input or another output.
+ * Packed sequences: B = 1, seq_start (device, int32) holds n_seq + 1 offsets into T, not decreasing;
+ * sequence i is tokens seq_start[i] .. seq_start[i + 1] - 1 (it may be empty) with state i.  Tokens of
+ * no sequence are neither read nor written.  Offsets out of order or range give undefined values,
+ * never an access out of range.
+ * Evaluated in chunks of 64 tokens: a NaN or infinity in a token may reach the other tokens of its
+ * chunk and every later one, never another sequence.  bf16: inputs are exact operands; what is
+ * computed is carried as a sum of two bf16, so o is off by its own rounding and states stay near fp32. */
+typedef struct {
+  int64_t b, h, t;         /* elements between batch rows, heads and tokens */
+} kda_stride_t;
+
+typedef enum { KDA_GATE_BOUNDED = 0, KDA_GATE_SOFTPLUS = 1, KDA_GATE_LOG = 2 } kda_gate_t;
+
+typedef struct {
+  int64_t B, Hk, Hv, T, dk, dv; /* Hk divides Hv; dk, dv in {32, 64, 128}; 0 <= T < 2^31 */
+  int64_t n_seq;                /* packed sequences (0 without seq_start) */
+  int32_t dtype;                /* a kda_dtype_t */
+  int32_t gate;                 /* a kda_gate_t */
+  float g_min;                  /* KDA_GATE_BOUNDED only */
+  float scale;                  /* of the outputs, finite */
+  kda_stride_t q, k, v, w, beta;
+} kda_gdr_t;
+
+/* Gradients, in the inputs' type; dS0 fp32 or NULL (not wanted). */
+typedef struct {
+  void *dq, *dk, *dv, *dw, *dbeta;
+  float* dS0;
+  kda_stride_t sq, sk, sv, sw, sbeta;
+} kda_gdr_grads_t;
+
+/* Chunked forward: o, and S_final unless it is NULL (which may be S0, in place).  S0 NULL: zero states. */
+KDA_API int kda_gdr_chunk_fwd(const void* q, const void* k, const void* v, const void* w, const void* beta,
+                              const float* S0, const int32_t* seq_start, const kda_gdr_t* desc, void* o,
+                              const kda_stride_t* o_stride, float* S_final, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Its gradients, given dO = dL/do and dS_final = dL/dS_final (NULL: zero).  Value heads that share a
+ * query/key head add up in dq and dk. */
+KDA_API int kda_gdr_chunk_bwd(const void* q, const void* k, const void* v, const void* w, const void* beta,
+                              const float* S0, const int32_t* seq_start, const kda_gdr_t* desc, const void* dO,
+                              const kda_stride_t* dO_stride, const float* dS_final, const kda_gdr_grads_t* grads,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch of the two (backward != 0: of kda_gdr_chunk_bwd); (size_t)-1 for an invalid descriptor. */
+KDA_API size_t kda_gdr_workspace_bytes(const kda_gdr_t* desc, int backward);
+
+/* Recurrent step: advances states of the pool S [n_slots,Hv,dk,dv] (fp32) by the T tokens of each of B
+ * rows, in place.  slots (device, int32, B) names each row's state; NULL: row b has state b.  A row whose
+ * slot is outside [0, n_slots) is padding: its outputs are zeros and no state is touched.  Rows that
+ * name the same slot are successive tokens of that state, in row order. */
+KDA_API int kda_gdr_decode(const void* q, const void* k, const void* v, const void* w, const void* beta, float* S,
+                           int64_t n_slots, const int32_t* slots, const kda_gdr_t* desc, void* o,
+                           const kda_stride_t* o_stride, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * The norms around a block, with its gate and its residual's scale, per row of D values:
+ *     n = x / rms(x) * weight       (weight NULL: n = x)
+ *     h = n * act(z)                (z NULL: h = n)
+ *     s = residual + alpha h        (residual NULL: s = alpha h)
+ *     y = s / rms(s) * next_weight  (next_weight NULL: no y)      rms(t) = sqrt(mean(t^2) + eps)
+ * at least one of the two norms being there.  The gated norm of a delta rule's heads is (weight, z); a
+ * residual add with the next block's norm is (residual, next_weight); a block normed on both sides has
+ * all.  Rows are [B,H,T] places of strided tensors of dtype, any strides and alignment of the type;
+ * weights are dense, of wdtype.  Sums and norms in fp32; y is taken from s before its rounding. */
+#define KDA_NORM_MAX_D 16384
+
+typedef enum { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_act_t;
+
+typedef struct {
+  int64_t B, H, T, D;
+  int32_t dtype, wdtype;   /* kda_dtype_t of the rows and of the weights */
+  int32_t act;             /* a kda_act_t */
+  float alpha, eps;        /* finite, eps >= 0 */
+  kda_stride_t x, z, residual;
+} kda_norm_t;
+
+typedef struct {
+  void *dx, *dz, *dresidual;        /* of dtype; dz, dresidual where z, residual are given */
+  void *dweight, *dnext_weight;     /* [D], of wdtype, where the weights are given */
+  kda_stride_t sx, sz, sresidual;
+} kda_norm_grads_t;
+
+KDA_API int kda_norm_fwd(const void* x, const void* weight, const void* z, const void* residual, const void* next_weight,
+                         const kda_norm_t* desc, void* s, const kda_stride_t* s_stride, void* y,
+                         const kda_stride_t* y_stride, void* stream);
+
+/* Gradients given ds = dL/ds (NULL: zero, with next_weight) and dy = dL/dy (with next_weight).  The
+ * weights' gradients are sums over the rows in a fixed order. */
+KDA_API int kda_norm_bwd(const void* x, const void* weight, const void* z, const void* residual, const void* next_weight,
+                         const kda_norm_t* desc, const void* ds, const kda_stride_t* ds_stride, const void* dy,
+                         const kda_stride_t* dy_stride, const kda_norm_grads_t* grads, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+KDA_API size_t kda_norm_bwd_workspace_bytes(const kda_norm_t* desc);
+
 /* Static description of an error code. Host-only. */
 KDA_API const char* kda_strerror(int code);
 
