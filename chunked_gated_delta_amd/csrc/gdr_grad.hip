@@ -12,7 +12,7 @@
 //   dg_t  = sum_{r >= t} dG_r
 // The second identity gives the log-decay's gradient from the accumulators that are there anyway.  S,
 // dS, F and dE are held in the inputs' type here (their rounding is one of the gradients' own size, half a
-// step of that type); dP and dA are hi + lo, which keeps the error below 1.5 times the final rounding's.
+// step of that type); dP and dA take two planes, which keeps the error below 1.5 times the final rounding's.
 #include "gdr_internal.h"
 
 namespace kda {
@@ -22,9 +22,9 @@ namespace {
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
-  using Op = typename Frags<T>::Op;
+  using Op = typename Frags<T>::template Op<2>;
   constexpr int KV = DV / 32, MT = DK / 16;
-  constexpr int kInFrag = Frags<T>::kInPlanes * kPlane, kOpFrag = 2 * kPlane;
+  constexpr int kInFrag = in_frag<T>(), kOpFrag = op_frag<T, 2>();
   __shared__ __attribute__((aligned(16))) char tri[4][4 * kOpFrag];   // a wavefront's dP and dA, two steps each
   __shared__ float ghi[64], glo[64], bet[64];
   __shared__ double dG[64];
@@ -104,8 +104,8 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
           b[r] = tok > j ? -d * b[r] : 0.f;
         }
       }
-      put_op(dp_f + (m >> 1) * kOpFrag, m & 1, li, g, a, T{});
-      put_op(da_f + (m >> 1) * kOpFrag, m & 1, li, g, b, T{});
+      put_op<2>(dp_f + (m >> 1) * kOpFrag, m & 1, li, g, a, T{});
+      put_op<2>(da_f + (m >> 1) * kOpFrag, m & 1, li, g, b, T{});
     }
     compiler_fence();
     double dg = 0.0, write = 0.0, hold = 0.0;
@@ -163,8 +163,8 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
           b[r] = i > tok ? -d * b[r] : 0.f;
         }
       }
-      put_op(dp_f + (m >> 1) * kOpFrag, m & 1, li, g, a, T{});
-      put_op(da_f + (m >> 1) * kOpFrag, m & 1, li, g, b, T{});
+      put_op<2>(dp_f + (m >> 1) * kOpFrag, m & 1, li, g, a, T{});
+      put_op<2>(da_f + (m >> 1) * kOpFrag, m & 1, li, g, b, T{});
     }
     compiler_fence();
 #pragma unroll

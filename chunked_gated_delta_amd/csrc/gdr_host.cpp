@@ -135,7 +135,7 @@ int64_t gdr_slots(int64_t B, int64_t T, int64_t n_seq, bool packed) {
 
 size_t gdr_layout(GdrParams& p, void* base, bool bwd) {
   const size_t slots = (size_t)gdr_slots(p.B, p.T, p.n_seq, p.seq_start != nullptr);
-  const size_t e = p.dtype == KDA_DTYPE_BF16 ? 2 : 4, op = 2 * kPlane, in = e == 2 ? kPlane : 2 * kPlane;
+  const size_t e = p.dtype == KDA_DTYPE_BF16 ? 2 : 4, op = (e == 2 ? 3 : 2) * kPlane, in = (e == 2 ? 1 : 2) * kPlane;
   const size_t vh = slots * p.Hv, kh = slots * p.Hk;
   size_t off = 0;
   auto take = [&](char*& at, size_t bytes) {

@@ -155,31 +155,50 @@ __device__ __forceinline__ float gdr_gate_grad(float w, int gate, float g_min) {
 
 // A fragment is 8 values a lane: of the A operand row li, of the B operand column li, at contraction
 // places 8g .. 8g + 7 (lane = 16 g + li) of a step of 32.  bf16 inputs are one register group, exact.
-// Values that the kernel computes (E, U, the state, the triangular factors) are carried as the sum of
-// two bf16 (hi + lo: 16 bits of fraction, relative error at most 2^-17), so products with an input
-// take two matrix instructions and keep the fp32 state and its adjoint to fp32-like accuracy.
+// Values that the kernels compute are carried as sums of bf16 planes, each the rounding of what the planes
+// before it leave: three planes hold an fp32 value whole, two are off by at most 2^-17 of it.  The state,
+// its adjoint and everything between them (E, T', U) take three: with two, S_final was off by 4e-6 where
+// fp32 arithmetic is off by 5e-8, with three it keeps fp32's accuracy for 1.5 times the matrix
+// instructions.  What enters only results of the inputs' type takes one or two.
 // fp32 inputs use v_mfma_f32_16x16x4_f32 on the same 8 values, one place of each lane group at a time.
-template <typename T> struct Frags;
-struct OpBf16 {
-  bf16x8 hi, lo;
+template <int N> struct Planes {
+  bf16x8 p[N];
 };
+template <typename T> struct Frags;
 template <> struct Frags<uint16_t> {
   using In = bf16x8;
-  using Op = OpBf16;
-  static constexpr int kInPlanes = 1;
+  template <int N> using Op = Planes<N>;
+  static constexpr int in_planes = 1;
+  static constexpr int planes(int n) { return n; }
 };
 template <> struct Frags<float> {
   using In = float8v;
-  using Op = float8v;
-  static constexpr int kInPlanes = 2;
+  template <int N> using Op = float8v;
+  static constexpr int in_planes = 2;
+  static constexpr int planes(int) { return 2; }
 };
-constexpr int kPlane = 64 * 16;   // 16 bytes a lane; an Op fragment is two planes (hi and lo, or fp32 halves)
+constexpr int kPlane = 64 * 16;   // 16 bytes a lane; an fp32 fragment is two planes (places 0-3 and 4-7)
+template <typename T> constexpr int in_frag() { return Frags<T>::in_planes * kPlane; }
+template <typename T, int N> constexpr int op_frag() { return Frags<T>::planes(N) * kPlane; }
 
 __device__ __forceinline__ floatx4 mma(bf16x8 a, bf16x8 b, floatx4 c) { return mfma(a, b, c); }
-__device__ __forceinline__ floatx4 mma(bf16x8 a, const OpBf16& b, floatx4 c) { return mfma(a, b.lo, mfma(a, b.hi, c)); }
-__device__ __forceinline__ floatx4 mma(const OpBf16& a, bf16x8 b, floatx4 c) { return mfma(a.lo, b, mfma(a.hi, b, c)); }
-__device__ __forceinline__ floatx4 mma(const OpBf16& a, const OpBf16& b, floatx4 c) {
-  return mfma(a.hi, b.lo, mfma(a.lo, b.hi, mfma(a.hi, b.hi, c)));   // lo lo is below the splits' own error
+template <int N> __device__ __forceinline__ floatx4 mma(bf16x8 a, const Planes<N>& b, floatx4 c) {
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) c = mfma(a, b.p[i], c);
+  return c;
+}
+template <int N> __device__ __forceinline__ floatx4 mma(const Planes<N>& a, bf16x8 b, floatx4 c) {
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) c = mfma(a.p[i], b, c);
+  return c;
+}
+// both in planes: the products that lie above the last plane's size
+template <int N> __device__ __forceinline__ floatx4 mma(const Planes<N>& a, const Planes<N>& b, floatx4 c) {
+#pragma unroll
+  for (int s = N - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i) c = mfma(a.p[i], b.p[s - i], c);
+  return c;
 }
 __device__ __forceinline__ floatx4 mma(const float8v& a, const float8v& b, floatx4 c) {
 #pragma unroll
@@ -198,53 +217,69 @@ __device__ __forceinline__ float8v load_row8(const float* p) {
 }
 
 // fragments stored plane by plane (LDS or workspace)
-template <typename F> __device__ __forceinline__ F load_frag(const char* base, int lane);
-template <> __device__ __forceinline__ bf16x8 load_frag<bf16x8>(const char* base, int lane) { return ld8(base + lane * 16); }
-template <> __device__ __forceinline__ OpBf16 load_frag<OpBf16>(const char* base, int lane) {
-  return OpBf16{ld8(base + lane * 16), ld8(base + kPlane + lane * 16)};
-}
-template <> __device__ __forceinline__ float8v load_frag<float8v>(const char* base, int lane) {
-  const floatx4 a = *reinterpret_cast<const floatx4*>(base + lane * 16);
-  const floatx4 b = *reinterpret_cast<const floatx4*>(base + kPlane + lane * 16);
-  return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
+template <typename F> struct FragIo;
+template <> struct FragIo<bf16x8> {
+  static __device__ __forceinline__ bf16x8 load(const char* at, int lane) { return ld8(at + lane * 16); }
+  static __device__ __forceinline__ void store(char* at, int lane, bf16x8 f) { *reinterpret_cast<bf16x8*>(at + lane * 16) = f; }
+};
+template <int N> struct FragIo<Planes<N>> {
+  static __device__ __forceinline__ Planes<N> load(const char* at, int lane) {
+    Planes<N> f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f.p[i] = ld8(at + i * kPlane + lane * 16);
+    return f;
+  }
+  static __device__ __forceinline__ void store(char* at, int lane, const Planes<N>& f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8*>(at + i * kPlane + lane * 16) = f.p[i];
+  }
+};
+template <> struct FragIo<float8v> {
+  static __device__ __forceinline__ float8v load(const char* at, int lane) {
+    const floatx4 a = *reinterpret_cast<const floatx4*>(at + lane * 16);
+    const floatx4 b = *reinterpret_cast<const floatx4*>(at + kPlane + lane * 16);
+    return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  }
+  static __device__ __forceinline__ void store(char* at, int lane, const float8v& f) {
+    *reinterpret_cast<floatx4*>(at + lane * 16) = floatx4{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<floatx4*>(at + kPlane + lane * 16) = floatx4{f[4], f[5], f[6], f[7]};
+  }
+};
+template <typename F> __device__ __forceinline__ F load_frag(const char* at, int lane) { return FragIo<F>::load(at, lane); }
+template <typename F> __device__ __forceinline__ void store_frag(char* at, int lane, const F& f) { FragIo<F>::store(at, lane, f); }
 
-__device__ __forceinline__ OpBf16 make_op(const float8v& f, uint16_t) {
-  OpBf16 r;
-  const bf16x8v hi = __builtin_convertvector(f, bf16x8v);
-  r.hi = __builtin_bit_cast(bf16x8, hi);
-  r.lo = __builtin_bit_cast(bf16x8, __builtin_convertvector(f - __builtin_convertvector(hi, float8v), bf16x8v));
+template <int N> __device__ __forceinline__ Planes<N> make_op(float8v f, uint16_t) {
+  Planes<N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bf16x8v h = __builtin_convertvector(f, bf16x8v);
+    r.p[i] = __builtin_bit_cast(bf16x8, h);
+    f -= __builtin_convertvector(h, float8v);
+  }
   return r;
 }
-__device__ __forceinline__ float8v make_op(const float8v& f, float) { return f; }
-
-__device__ __forceinline__ void store_frag(char* base, int lane, const bf16x8& f) { *reinterpret_cast<bf16x8*>(base + lane * 16) = f; }
-__device__ __forceinline__ void store_frag(char* base, int lane, const OpBf16& f) {
-  store_frag(base, lane, f.hi);
-  store_frag(base + kPlane, lane, f.lo);
-}
-__device__ __forceinline__ void store_frag(char* base, int lane, const float8v& f) {
-  *reinterpret_cast<floatx4*>(base + lane * 16) = floatx4{f[0], f[1], f[2], f[3]};
-  *reinterpret_cast<floatx4*>(base + kPlane + lane * 16) = floatx4{f[4], f[5], f[6], f[7]};
-}
+template <int N> __device__ __forceinline__ float8v make_op(const float8v& f, float) { return f; }
 
 // A result tile (lane (li, g): rows 4g .. 4g + 3 of column li) as the half `half` (rows 0-15 or 16-31)
 // of a fragment's contraction places: 4 consecutive places of one lane, one 8- or 16-byte write a plane
-__device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, uint16_t) {
+template <int N> __device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, uint16_t) {
   char* at = frag + (li + 16 * (2 * half + (g >> 1))) * 16 + (g & 1) * 8;
-  const uint32_t h0 = pk_bf16(x[0], x[1]), h1 = pk_bf16(x[2], x[3]);
-  *reinterpret_cast<u32x2v*>(at) = u32x2v{h0, h1};
-  const uint32_t l0 = pk_bf16(x[0] - lo_bf16(h0), x[1] - hi_bf16(h0)), l1 = pk_bf16(x[2] - lo_bf16(h1), x[3] - hi_bf16(h1));
-  *reinterpret_cast<u32x2v*>(at + kPlane) = u32x2v{l0, l1};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t h0 = pk_bf16(x[0], x[1]), h1 = pk_bf16(x[2], x[3]);
+    *reinterpret_cast<u32x2v*>(at + i * kPlane) = u32x2v{h0, h1};
+    if (i + 1 < N) x -= floatx4{lo_bf16(h0), hi_bf16(h0), lo_bf16(h1), hi_bf16(h1)};
+  }
 }
-__device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, float) {
+template <int N> __device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, float) {
   *reinterpret_cast<floatx4*>(frag + (g & 1) * kPlane + (li + 16 * (2 * half + (g >> 1))) * 16) = x;
 }
-// the same for values that are inputs (one bf16 plane, exact)
-__device__ __forceinline__ void put_in(char* frag, int half, int li, int g, floatx4 x, uint16_t) {
-  *reinterpret_cast<u32x2v*>(frag + (li + 16 * (2 * half + (g >> 1))) * 16 + (g & 1) * 8) = u32x2v{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+// one value of a fragment of the inputs' type (its first plane): contraction place `k` of column `col`
+template <typename T> __device__ __forceinline__ T frag_at(const char* frag, int k, int col) {
+  const int ln = col + 16 * (k >> 3);
+  if constexpr (sizeof(T) == 2) return *reinterpret_cast<const T*>(frag + ln * 16 + (k & 7) * 2);
+  else return *reinterpret_cast<const T*>(frag + ((k >> 2) & 1) * kPlane + ln * 16 + (k & 3) * 4);
 }
-__device__ __forceinline__ void put_in(char* frag, int half, int li, int g, floatx4 x, float t) { put_op(frag, half, li, g, x, t); }
 
 __device__ __forceinline__ floatx4 ld4f(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
 

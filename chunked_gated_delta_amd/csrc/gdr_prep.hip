@@ -62,27 +62,22 @@ __device__ __forceinline__ void solve_columns(float* mat, float* diag, int wave,
 }
 
 // fragments of a matrix in LDS as an A operand: lane holds 8 consecutive columns of row li of the tile
-template <typename T>
-__device__ __forceinline__ typename Frags<T>::Op rows_frag(const float* mat, int tile, int ks, int li, int g) {
-  return make_op(load_row8(mat + (16 * tile + li) * kLd + 32 * ks + 8 * g), T{});
+__device__ __forceinline__ float8v rows_frag(const float* mat, int tile, int ks, int li, int g) {
+  return load_row8(mat + (16 * tile + li) * kLd + 32 * ks + 8 * g);
 }
 // the same of its transpose
-template <typename T>
-__device__ __forceinline__ typename Frags<T>::Op cols_frag(const float* mat, int tile, int ks, int li, int g) {
+__device__ __forceinline__ float8v cols_frag(const float* mat, int tile, int ks, int li, int g) {
   float8v f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = mat[(32 * ks + 8 * g + e) * kLd + 16 * tile + li];
-  return make_op(f, T{});
+  return f;
 }
-
-__device__ __forceinline__ void store_hi(char* at, int lane, const OpBf16& f) { store_frag(at, lane, f.hi); }
-__device__ __forceinline__ void store_hi(char* at, int lane, const float8v& f) { store_frag(at, lane, f); }
 
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
   constexpr int KS = DK / 32;
-  constexpr int kInFrag = Frags<T>::kInPlanes * kPlane;
+  constexpr int kInFrag = in_frag<T>(), kOpFrag = op_frag<T, 3>();
   __shared__ __attribute__((aligned(16))) char kf[4 * KS * kInFrag];   // a row operand's fragments [tile][step]
   __shared__ __attribute__((aligned(16))) float mat[64 * kLd];
   __shared__ __attribute__((aligned(16))) float diag[4 * 320];
@@ -222,15 +217,15 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
         for (int r = 0; r < 4; ++r) mat[(16 * i + 4 * g + r) * kLd + 16 * wave + li] = X[i][r];
       __syncthreads();
       if (variant == 0) {
-        char* out = p.ws_ti + blk * kTriFrags * 2 * kPlane;
+        char* out = p.ws_ti + blk * kTriFrags * kOpFrag;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * 2 * kPlane, lane, rows_frag<T>(mat, wave, ks, li, g));
+          if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * kOpFrag, lane, make_op<3>(rows_frag(mat, wave, ks, li, g), T{}));
       } else {
-        char* out = p.ws_tt + blk * kTriFrags * 2 * kPlane;
+        char* out = p.ws_tt + blk * kTriFrags * kOpFrag;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * 2 * kPlane, lane, cols_frag<T>(mat, wave, ks, li, g));
+          if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * kOpFrag, lane, make_op<3>(cols_frag(mat, wave, ks, li, g), T{}));
       }
       __syncthreads();
     }
@@ -243,16 +238,16 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
       }
     __syncthreads();
     if constexpr (BWD) {
-      char* out = p.ws_p + blk * kTriFrags * 2 * kPlane;
+      char* out = p.ws_p + blk * kTriFrags * kOpFrag;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * 2 * kPlane, lane, cols_frag<T>(mat, wave, ks, li, g));
+        if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * kOpFrag, lane, make_op<3>(cols_frag(mat, wave, ks, li, g), T{}));
     } else {
       // the outputs' own factor, rounded to the inputs' type: it enters o alone, which is rounded to that type
-      char* out = p.ws_p + blk * kTriFrags * kInFrag;
+      char* out = p.ws_p + blk * kTriFrags * op_frag<T, 1>();
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks <= wave / 2) store_hi(out + lower_frag(wave, ks) * kInFrag, lane, rows_frag<T>(mat, wave, ks, li, g));
+        if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * op_frag<T, 1>(), lane, make_op<1>(rows_frag(mat, wave, ks, li, g), T{}));
     }
     __syncthreads();
   }

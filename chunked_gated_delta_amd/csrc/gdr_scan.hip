@@ -1,31 +1,56 @@
 // The sequential part of the head-gated delta rule: the state from chunk to chunk, and the outputs.
 //
-// Value columns are independent, so a workgroup of 4 wavefronts owns one (sequence, value head) and 16
-// of its columns and walks the chunks.  Inside a chunk wavefront i owns token rows 16i .. 16i + 15 and
-// the state's rows dk/4 i .. dk/4 (i + 1) - 1, in registers (fp32 matrix-core results).  Every A operand
-// (K, Q, K^T, T', P) is used by exactly one wavefront and is loaded straight into its registers;
-// what wavefronts exchange (the state, E, U: 16 columns each) goes through LDS as ready B operands:
-//   E = V - gam K S  |  U = beta T' E  |  O = scale gam Q S + P U,  S <- e^{G_last} S + K^T (eta U)
-// with one barrier at each bar.  The state is an fp32 sum; as an operand it is hi + lo.
-// The backward runs the same kernel without outputs: it leaves each chunk's entering state and F, which
-// the gradient kernel reads (rounded to the inputs' type there: they enter gradients of that type).
+// Value columns are independent, so a workgroup owns one (sequence, value head) and 16 of its columns and
+// walks the chunks:
+//   E = V - gam K S  |  U = beta T' E  |  S <- e^{G_last} S + K^T (eta U)         O = scale gam Q S + P U
+// with a barrier at each bar.  What bounds it is that chain: three products of 16 columns, each waiting
+// for the one before, so everything else is kept off it.
+//  - Wavefronts 0-3 walk the chain.  Wavefront i owns token rows 16i .. 16i + 15 and a quarter of the
+//    state's rows, in registers (fp32 matrix-core results).  Wavefronts 4-7, one more on each SIMD, form the
+//    outputs (or, in the backward's run, write out the entering states and F) in the chain's shadow.
+//  - Every A operand (K, Q, K^T, T', P) has exactly one reader in the workgroup and is loaded straight into its
+//    registers, for the chunk after the next as soon as this chunk's is used: two register buffers, the
+//    loop unrolled by two.  Loads past the last chunk are clamped to it.
+//  - What the wavefronts exchange (the state, E, U: 16 columns each) goes through LDS as ready B operands.
+// Rows behind the sequence's end read its last row; their E is set to zero, so nothing of them reaches
+// the state, and their outputs are not written.
 #include "gdr_internal.h"
 
 namespace kda {
 
 namespace {
 
+__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// Writes `rows` contraction places x 16 columns of a B-operand array (first planes) to row-major memory:
+// a lane takes 8 columns of one place.
+template <typename T>
+__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, T* out, int64_t ld, int tid) {
+  for (int i = tid; i < rows * 2; i += 256) {
+    const int r = i >> 1, c0 = (i & 1) * 8;
+    const char* fr = frags + (r >> 5) * frag_bytes;
+    T x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(fr, r & 31, c0 + e);
+    typename Frags<T>::In v;
+    __builtin_memcpy(&v, x, sizeof(v));
+    *reinterpret_cast<typename Frags<T>::In*>(out + (int64_t)r * ld + c0) = v;
+  }
+}
+
 template <typename T, int DK, bool STATES>
-__global__ __launch_bounds__(256) void gdr_scan_kernel(GdrParams p) {
+__global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
-  using Op = typename Frags<T>::Op;
+  using Op3 = typename Frags<T>::template Op<3>;
+  using Op2 = typename Frags<T>::template Op<2>;
+  using Op1 = typename Frags<T>::template Op<1>;
   constexpr int KS = DK / 32;
   constexpr int RT = DK >= 64 ? DK / 64 : 1;      // state row tiles of a wavefront
-  constexpr int kInFrag = Frags<T>::kInPlanes * kPlane, kOpFrag = 2 * kPlane;
-  __shared__ __attribute__((aligned(16))) char sf[KS * kOpFrag];   // the state, as B operands
-  __shared__ __attribute__((aligned(16))) char ef[2 * kOpFrag];    // E
-  __shared__ __attribute__((aligned(16))) char uf[2 * kOpFrag];    // U
-  __shared__ __attribute__((aligned(16))) char wf[2 * kOpFrag];    // eta U
+  constexpr int kIn = in_frag<T>(), kOp1 = op_frag<T, 1>(), kOp2 = op_frag<T, 2>(), kOp3 = op_frag<T, 3>();
+  __shared__ __attribute__((aligned(16))) char sf[KS * kOp3];              // the state, as B operands
+  __shared__ __attribute__((aligned(16))) char ef[2 * kOp3];               // E
+  __shared__ __attribute__((aligned(16))) char wf[2 * kOp3];               // eta U
+  __shared__ __attribute__((aligned(16))) char uf[2 * kOp2];               // U (F where states are written)
 
   int64_t unit;
   int part;
@@ -33,121 +58,211 @@ __global__ __launch_bounds__(256) void gdr_scan_kernel(GdrParams p) {
   const int64_t s = unit / p.Hv;
   const int h = (int)(unit % p.Hv), kh = h / (p.Hv / p.Hk);
   const GdrSeq seq = gdr_seq(p, s);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+  const int64_t nc = seq.n_chunks;
+  const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+  const bool chain = threadIdx.x < 256;
+  const int wave = (threadIdx.x >> 6) & 3;
   const int col = 16 * part + li;
-  const bool owner = wave * RT < DK / 16;
   const int r0 = 16 * wave + 4 * g;               // first of this lane's 4 token rows in result tiles
+  const int64_t blk0 = seq.slot0 * p.Hv + h;      // workspace block of chunk 0; the next is Hv further
+  const float* gates = (const float*)p.ws_gate + blk0 * kGateFloats;
+  auto clamp_chunk = [&](int64_t c) { return min64(c, nc - 1); };
+  auto row_of = [&](int64_t c) { return seq.t0 + min64(c * kGdrChunk + 16 * wave + li, seq.len - 1); };
 
-  floatx4 S[RT];
-#pragma unroll
-  for (int m = 0; m < RT; ++m) {
-    S[m] = floatx4{};
-    if (owner && p.S0) {
-      const float* at = p.S0 + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
-    }
-  }
-  auto put_state = [&]() {
+  if (chain) {
+    const bool owner = wave * RT < DK / 16;
+    floatx4 S[RT];
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
-      const int t = wave * RT + m;
-      if (owner) put_op(sf + (t >> 1) * kOpFrag, t & 1, li, g, S[m], T{});
+      S[m] = floatx4{};
+      if (owner && p.S0) {
+        const float* at = p.S0 + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
+      }
     }
-  };
-  put_state();
-  block_barrier();
+    auto put_state = [&]() {
+#pragma unroll
+      for (int m = 0; m < RT; ++m) {
+        const int t = wave * RT + m;
+        if (owner) put_op<3>(sf + (t >> 1) * kOp3, t & 1, li, g, S[m], T{});
+      }
+    };
+    put_state();
+    block_barrier();
 
-  const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + (seq.t0 + 16 * wave + li) * p.sk.t + 8 * g;
-  const T* qp = (const T*)p.q + seq.row * p.sq.b + kh * p.sq.h + (seq.t0 + 16 * wave + li) * p.sq.t + 8 * g;
-  const T* vp = (const T*)p.v + seq.row * p.sv.b + h * p.sv.h + (seq.t0 + r0) * p.sv.t + col;
-  T* op = STATES ? nullptr : (T*)p.o + seq.row * p.so.b + h * p.so.h + (seq.t0 + r0) * p.so.t + col;
+    const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + 8 * g;
+    const T* vp = (const T*)p.v + seq.row * p.sv.b + h * p.sv.h + col;
+    struct Buf {
+      In k[KS];
+      Op3 ti[2];
+      In kt[RT][2];
+      float v[4];
+      floatx4 gam, eta, beta;
+      float last;
+    };
+    auto load_k = [&](Buf& b, int64_t c) {
+      const T* at = kp + row_of(c) * p.sk.t;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(at + 32 * ks);
+    };
+    auto load_v = [&](Buf& b, int64_t c) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b.v[r] = load_f32(vp, (seq.t0 + min64(c * kGdrChunk + r0 + r, seq.len - 1)) * p.sv.t);
+      b.gam = ld4f(gates + c * p.Hv * kGateFloats + kGateGam + r0);
+    };
+    auto load_ti = [&](Buf& b, int64_t c) {
+      const char* at = p.ws_ti + (blk0 + c * p.Hv) * kTriFrags * kOp3;
+      b.ti[0] = load_frag<Op3>(at + lower_frag(wave, 0) * kOp3, lane);
+      if (wave >= 2) b.ti[1] = load_frag<Op3>(at + lower_frag(wave, 1) * kOp3, lane);
+      const float* gt = gates + c * p.Hv * kGateFloats;
+      b.eta = ld4f(gt + kGateEta + r0);
+      b.beta = ld4f(gt + kGateBeta + r0);
+      b.last = gt[kGateLast];
+    };
+    auto load_kt = [&](Buf& b, int64_t c) {
+      if (!owner) return;
+      const char* at = p.ws_kt + ((seq.slot0 + c) * p.Hk + kh) * (int64_t)(DK / 8) * kIn;
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) b.kt[m][ks] = load_frag<In>(at + (2 * (wave * RT + m) + ks) * kIn, lane);
+    };
+    auto step = [&](Buf& b, int64_t c) {
+      const int64_t left = seq.len - c * kGdrChunk, ahead = clamp_chunk(c + 2);
+      const int n = left < kGdrChunk ? (int)left : kGdrChunk;
+      floatx4 E = {};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) E = mma(b.k[ks], load_frag<Op3>(sf + ks * kOp3, lane), E);
+      load_k(b, ahead);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) E[r] = r0 + r < n ? b.v[r] - b.gam[r] * E[r] : 0.f;
+      load_v(b, ahead);
+      put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, E, T{});
+      block_barrier();
 
-  for (int64_t c = 0; c < seq.n_chunks; ++c) {
-    const int64_t slot = seq.slot0 + c, blk = slot * p.Hv + h;
-    const int64_t left = seq.len - c * kGdrChunk;
-    const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-    const float* gate = (const float*)p.ws_gate + blk * kGateFloats;
-    const floatx4 gam = ld4f(gate + kGateGam + r0), eta = ld4f(gate + kGateEta + r0), beta = ld4f(gate + kGateBeta + r0);
-    const float last = gate[kGateLast];
+      floatx4 F = mma(b.ti[0], load_frag<Op3>(ef, lane), floatx4{});
+      if (wave >= 2) F = mma(b.ti[1], load_frag<Op3>(ef + kOp3, lane), F);
+      const floatx4 U = b.beta * F, W = b.eta * U;
+      const float last = b.last;
+      load_ti(b, ahead);
+      put_op<3>(wf + (wave >> 1) * kOp3, wave & 1, li, g, W, T{});
+      block_barrier();
 
-    if constexpr (STATES) {   // the state entering the chunk
+      put_op<2>(uf + (wave >> 1) * kOp2, wave & 1, li, g, STATES ? F : U, T{});
       if (owner) {
-        T* at = (T*)p.ws_s + blk * p.dk * p.dv + (int64_t)(16 * wave * RT + 4 * g) * p.dv + col;
+        const Op3 w0 = load_frag<Op3>(wf, lane), w1 = load_frag<Op3>(wf + kOp3, lane);
 #pragma unroll
-        for (int m = 0; m < RT; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) store_f32(at, (int64_t)(16 * m + r) * p.dv, S[m][r]);
+        for (int m = 0; m < RT; ++m) S[m] = mma(b.kt[m][1], w1, mma(b.kt[m][0], w0, S[m] * last));
+      }
+      load_kt(b, ahead);
+      put_state();
+      block_barrier();
+    };
+    if (nc > 0) {
+      Buf b0, b1;
+      const int64_t second = clamp_chunk(1);
+      load_k(b0, 0);
+      load_v(b0, 0);
+      load_ti(b0, 0);
+      load_kt(b0, 0);
+      load_k(b1, second);
+      load_v(b1, second);
+      load_ti(b1, second);
+      load_kt(b1, second);
+      for (int64_t c = 0; c < nc; c += 2) {
+        step(b0, c);
+        if (c + 1 < nc) step(b1, c + 1);
       }
     }
-    floatx4 E = {}, O = {};
+    if (p.S_final && owner) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      In kf, qf;
-      zero_frag(kf);
-      zero_frag(qf);
-      if (16 * wave + li < n) {
-        kf = load_row8(kp + c * kGdrChunk * p.sk.t + 32 * ks);
-        if constexpr (!STATES) qf = load_row8(qp + c * kGdrChunk * p.sq.t + 32 * ks);
+      for (int m = 0; m < RT; ++m) {
+        float* at = p.S_final + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
       }
-      const Op b = load_frag<Op>(sf + ks * kOpFrag, lane);
-      E = mma(kf, b, E);
-      if constexpr (!STATES) O = mma(qf, b, O);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float v = r0 + r < n ? load_f32(vp, (c * kGdrChunk + r) * p.sv.t) : 0.f;
-      E[r] = v - gam[r] * E[r];
-    }
-    put_op(ef + (wave >> 1) * kOpFrag, wave & 1, li, g, E, T{});
-    block_barrier();
+    return;
+  }
 
-    floatx4 F = {};
-    const char* ti = p.ws_ti + blk * kTriFrags * kOpFrag;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-      if (ks <= wave / 2) F = mma(load_frag<Op>(ti + lower_frag(wave, ks) * kOpFrag, lane), load_frag<Op>(ef + ks * kOpFrag, lane), F);
-    if constexpr (STATES) {
-      T* at = (T*)p.ws_f + blk * kGdrChunk * p.dv + (int64_t)r0 * p.dv + col;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) store_f32(at, (int64_t)r * p.dv, F[r]);
+  block_barrier();   // the first state
+  if constexpr (STATES) {
+    const int tid = threadIdx.x & 255;
+    T* sp = (T*)p.ws_s + blk0 * p.dk * p.dv + 16 * part;
+    T* fp = (T*)p.ws_f + blk0 * kGdrChunk * p.dv + 16 * part;
+    for (int64_t c = 0; c < nc; ++c) {
+      // the state that enters this chunk, F of the one before
+      write_rows<T>(sf, kOp3, DK, sp + c * p.Hv * p.dk * p.dv, p.dv, tid);
+      if (c > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp + (c - 1) * p.Hv * kGdrChunk * p.dv, p.dv, tid);
+      block_barrier();
+      block_barrier();
+      block_barrier();
     }
-    const floatx4 U = beta * F;
-    if constexpr (!STATES) put_op(uf + (wave >> 1) * kOpFrag, wave & 1, li, g, U, T{});
-    put_op(wf + (wave >> 1) * kOpFrag, wave & 1, li, g, eta * U, T{});
-    block_barrier();
-
-    if constexpr (!STATES) {
+    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp + (nc - 1) * p.Hv * kGdrChunk * p.dv, p.dv, tid);
+  } else {
+    const T* qp = (const T*)p.q + seq.row * p.sq.b + kh * p.sq.h + 8 * g;
+    T* op = (T*)p.o + seq.row * p.so.b + h * p.so.h + (seq.t0 + r0) * p.so.t + col;
+    struct Buf {
+      In q[KS];
+      Op1 pm[2];
+      floatx4 gam;
+    };
+    auto load_q = [&](Buf& b, int64_t c) {
+      const T* at = qp + row_of(c) * p.sq.t;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) O[r] *= p.scale * gam[r];
-      const char* pm = p.ws_p + blk * kTriFrags * kInFrag;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        if (ks <= wave / 2) O = mma(load_frag<In>(pm + lower_frag(wave, ks) * kInFrag, lane), load_frag<Op>(uf + ks * kOpFrag, lane), O);
+      for (int ks = 0; ks < KS; ++ks) b.q[ks] = load_row8(at + 32 * ks);
+      b.gam = ld4f(gates + c * p.Hv * kGateFloats + kGateGam + r0);
+    };
+    auto load_p = [&](Buf& b, int64_t c) {
+      const char* at = p.ws_p + (blk0 + c * p.Hv) * kTriFrags * kOp1;
+      b.pm[0] = load_frag<Op1>(at + lower_frag(wave, 0) * kOp1, lane);
+      if (wave >= 2) b.pm[1] = load_frag<Op1>(at + lower_frag(wave, 1) * kOp1, lane);
+    };
+    floatx4 O = {};
+    // the outputs of chunk c, whose U the chain has left
+    auto finish = [&](Buf& b, int64_t c) {
+      const int64_t left = seq.len - c * kGdrChunk;
+      const int n = left < kGdrChunk ? (int)left : kGdrChunk;
+      const Op2 u0 = load_frag<Op2>(uf, lane);
+      if constexpr (sizeof(T) == 2) {
+        O = mma(b.pm[0].p[0], u0, O);
+        if (wave >= 2) O = mma(b.pm[1].p[0], load_frag<Op2>(uf + kOp2, lane), O);
+      } else {
+        O = mma(b.pm[0], u0, O);
+        if (wave >= 2) O = mma(b.pm[1], load_frag<Op2>(uf + kOp2, lane), O);
+      }
+      load_p(b, clamp_chunk(c + 2));
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (r0 + r < n) store_f32(op, (c * kGdrChunk + r) * p.so.t, O[r]);
-    }
-    if (owner) {
-      const char* kt = p.ws_kt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
+    };
+    auto step = [&](Buf& b, Buf& before, int64_t c) {
+      if (c > 0) finish(before, c - 1);
+      O = floatx4{};
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        S[m] = S[m] * last;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-          S[m] = mma(load_frag<In>(kt + (2 * (wave * RT + m) + ks) * kInFrag, lane), load_frag<Op>(wf + ks * kOpFrag, lane), S[m]);
+      for (int ks = 0; ks < KS; ++ks) {
+        // two planes: o is rounded to the inputs' type
+        O = mma(b.q[ks], load_frag<Op2>(sf + ks * kOp3, lane), O);
       }
-    }
-    put_state();
-    block_barrier();
-  }
-
-  if (p.S_final && owner) {
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      float* at = p.S_final + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
+      O *= p.scale * b.gam;
+      load_q(b, clamp_chunk(c + 2));
+      block_barrier();
+      block_barrier();
+      block_barrier();
+    };
+    if (nc > 0) {
+      Buf b0, b1;
+      load_q(b0, 0);
+      load_p(b0, 0);
+      load_q(b1, clamp_chunk(1));
+      load_p(b1, clamp_chunk(1));
+      for (int64_t c = 0; c < nc; c += 2) {
+        step(b0, b1, c);
+        if (c + 1 < nc) step(b1, b0, c + 1);
+      }
+      if (nc & 1) finish(b0, nc - 1);
+      else finish(b1, nc - 1);
     }
   }
 }
@@ -155,20 +270,23 @@ __global__ __launch_bounds__(256) void gdr_scan_kernel(GdrParams p) {
 // The adjoint's sequential part, from the last chunk to the first, in the same division of work:
 //   X = P^T dO + eta K dS  |  dU = T^T X, dE = beta dU (the gradient of v)
 //   |  dS <- e^{G_last} dS + Q^T (scale gam dO) - K^T (gam dE)
-// It leaves dS of each chunk's end for the gradient kernel and, per 16 columns, the sums of dU F that
-// make beta's gradient.
+// Wavefronts 0-3 walk the chain; wavefronts 4-7 form P^T dO and Q^T (scale gam dO) of the chunk that comes
+// next, which do not depend on it, and write out dS of each chunk's end for the gradient kernel.  The
+// chain leaves, per 16 columns, the sums of dU F that make beta's gradient.
 template <typename T, int DK>
-__global__ __launch_bounds__(256) void gdr_rscan_kernel(GdrParams p) {
+__global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
-  using Op = typename Frags<T>::Op;
+  using Op3 = typename Frags<T>::template Op<3>;
   constexpr int KS = DK / 32;
   constexpr int RT = DK >= 64 ? DK / 64 : 1;
-  constexpr int kInFrag = Frags<T>::kInPlanes * kPlane, kOpFrag = 2 * kPlane;
-  __shared__ __attribute__((aligned(16))) char sf[KS * kOpFrag];   // dS
-  __shared__ __attribute__((aligned(16))) char of[2 * kInFrag];    // dO
-  __shared__ __attribute__((aligned(16))) char gf[2 * kOpFrag];    // scale gam dO
-  __shared__ __attribute__((aligned(16))) char xf[2 * kOpFrag];    // X
-  __shared__ __attribute__((aligned(16))) char ef[2 * kOpFrag];    // -gam dE
+  constexpr int kIn = in_frag<T>(), kOp3 = op_frag<T, 3>();
+  __shared__ __attribute__((aligned(16))) char sf[KS * kOp3];              // dS
+  __shared__ __attribute__((aligned(16))) char xf[2 * kOp3];               // X
+  __shared__ __attribute__((aligned(16))) char ef[2 * kOp3];               // -gam dE
+  __shared__ __attribute__((aligned(16))) char of[2 * kIn];                // dO
+  __shared__ __attribute__((aligned(16))) char gf[2 * kOp3];               // scale gam dO
+  __shared__ __attribute__((aligned(16))) float x0[2][4 * 256];            // P^T dO, result tiles [wave][lane][4]
+  __shared__ __attribute__((aligned(16))) float d0[2][DK / 16 * 256];      // Q^T (scale gam dO)
 
   int64_t unit;
   int part;
@@ -176,118 +294,213 @@ __global__ __launch_bounds__(256) void gdr_rscan_kernel(GdrParams p) {
   const int64_t s = unit / p.Hv;
   const int h = (int)(unit % p.Hv), kh = h / (p.Hv / p.Hk);
   const GdrSeq seq = gdr_seq(p, s);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+  const int64_t nc = seq.n_chunks;
+  const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+  const bool chain = threadIdx.x < 256;
+  const int wave = (threadIdx.x >> 6) & 3;
   const int col = 16 * part + li;
-  const bool owner = wave * RT < DK / 16;
   const int r0 = 16 * wave + 4 * g;
+  const bool owner = wave * RT < DK / 16;
+  const int64_t blk0 = seq.slot0 * p.Hv + h;
+  const float* gates = (const float*)p.ws_gate + blk0 * kGateFloats;
+  auto clamp_chunk = [&](int64_t c) { return c < 0 ? 0 : c; };
 
-  floatx4 S[RT];
+  if (chain) {
+    floatx4 S[RT];
 #pragma unroll
-  for (int m = 0; m < RT; ++m) {
-    S[m] = floatx4{};
-    if (owner && p.dSf) {
-      const float* at = p.dSf + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+    for (int m = 0; m < RT; ++m) {
+      S[m] = floatx4{};
+      if (owner && p.dSf) {
+        const float* at = p.dSf + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
+        for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
+      }
     }
-  }
-  const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + (seq.t0 + 16 * wave + li) * p.sk.t + 8 * g;
-  const T* dop = (const T*)p.dO + seq.row * p.sdo.b + h * p.sdo.h + (seq.t0 + r0) * p.sdo.t + col;
-  T* dvp = (T*)p.dv_ + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + r0) * p.sdv.t + col;
-
-  for (int64_t c = seq.n_chunks - 1; c >= 0; --c) {
-    const int64_t slot = seq.slot0 + c, blk = slot * p.Hv + h;
-    const int64_t left = seq.len - c * kGdrChunk;
-    const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-    const float* gate = (const float*)p.ws_gate + blk * kGateFloats;
-    const floatx4 gam = ld4f(gate + kGateGam + r0), eta = ld4f(gate + kGateEta + r0), beta = ld4f(gate + kGateBeta + r0);
-    const float last = gate[kGateLast];
-
-    if (owner) {
-      T* at = (T*)p.ws_ds + blk * p.dk * p.dv + (int64_t)(16 * wave * RT + 4 * g) * p.dv + col;
+    auto put_state = [&]() {
 #pragma unroll
       for (int m = 0; m < RT; ++m) {
         const int t = wave * RT + m;
-        put_op(sf + (t >> 1) * kOpFrag, t & 1, li, g, S[m], T{});
-#pragma unroll
-        for (int r = 0; r < 4; ++r) store_f32(at, (int64_t)(16 * m + r) * p.dv, S[m][r]);
+        if (owner) put_op<3>(sf + (t >> 1) * kOp3, t & 1, li, g, S[m], T{});
       }
-    }
-    floatx4 dO;
+    };
+    put_state();
+    const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + 8 * g;
+    T* dvp = (T*)p.dv_ + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + r0) * p.sdv.t + col;
+    struct Buf {
+      In k[KS];
+      Op3 tt[2];
+      In kt[RT][2];
+      float f[4];
+      floatx4 gam, eta, beta;
+      float last;
+    };
+    auto load_k = [&](Buf& b, int64_t c) {
+      const T* at = kp + (seq.t0 + min64(c * kGdrChunk + 16 * wave + li, seq.len - 1)) * p.sk.t;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) dO[r] = r0 + r < n ? load_f32(dop, (c * kGdrChunk + r) * p.sdo.t) : 0.f;
-    put_in(of + (wave >> 1) * kInFrag, wave & 1, li, g, dO, T{});
-    put_op(gf + (wave >> 1) * kOpFrag, wave & 1, li, g, p.scale * (gam * dO), T{});
-    block_barrier();
+      for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(at + 32 * ks);
+      b.eta = ld4f(gates + c * p.Hv * kGateFloats + kGateEta + r0);
+    };
+    auto load_tt = [&](Buf& b, int64_t c) {
+      const char* at = p.ws_tt + (blk0 + c * p.Hv) * kTriFrags * kOp3;
+      if (wave < 2) b.tt[0] = load_frag<Op3>(at + upper_frag(wave, 0) * kOp3, lane);
+      b.tt[1] = load_frag<Op3>(at + upper_frag(wave, 1) * kOp3, lane);
+      const float* gt = gates + c * p.Hv * kGateFloats;
+      b.gam = ld4f(gt + kGateGam + r0);
+      b.beta = ld4f(gt + kGateBeta + r0);
+      b.last = gt[kGateLast];
+    };
+    auto load_kt = [&](Buf& b, int64_t c) {
+      const T* fp = (const T*)p.ws_f + (blk0 + c * p.Hv) * kGdrChunk * p.dv + (int64_t)r0 * p.dv + col;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b.f[r] = load_f32(fp, (int64_t)r * p.dv);
+      if (!owner) return;
+      const char* at = p.ws_kt + ((seq.slot0 + c) * p.Hk + kh) * (int64_t)(DK / 8) * kIn;
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) b.kt[m][ks] = load_frag<In>(at + (2 * (wave * RT + m) + ks) * kIn, lane);
+    };
+    auto step = [&](Buf& b, int64_t c) {
+      const int64_t left = seq.len - c * kGdrChunk, ahead = clamp_chunk(c - 2);
+      const int n = left < kGdrChunk ? (int)left : kGdrChunk;
+      floatx4 X = {};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) X = mma(b.k[ks], load_frag<Op3>(sf + ks * kOp3, lane), X);
+      const floatx4 first = ld4f(&x0[c & 1][(wave * 64 + lane) * 4]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) X[r] = r0 + r < n ? b.eta[r] * X[r] + first[r] : 0.f;
+      load_k(b, ahead);
+      put_op<3>(xf + (wave >> 1) * kOp3, wave & 1, li, g, X, T{});
+      block_barrier();
 
-    floatx4 X = {};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      In kf;
-      zero_frag(kf);
-      if (16 * wave + li < n) kf = load_row8(kp + c * kGdrChunk * p.sk.t + 32 * ks);
-      X = mma(kf, load_frag<Op>(sf + ks * kOpFrag, lane), X);
-    }
-    X = X * eta;
-    const char* pm = p.ws_p + blk * kTriFrags * kOpFrag;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-      if (ks >= wave / 2) X = mma(load_frag<Op>(pm + upper_frag(wave, ks) * kOpFrag, lane), load_frag<In>(of + ks * kInFrag, lane), X);
-    put_op(xf + (wave >> 1) * kOpFrag, wave & 1, li, g, X, T{});
-    block_barrier();
+      floatx4 dU = mma(b.tt[1], load_frag<Op3>(xf + kOp3, lane), floatx4{});
+      if (wave < 2) dU = mma(b.tt[0], load_frag<Op3>(xf, lane), dU);
+      const floatx4 dE = b.beta * dU, G = -(b.gam * dE);
+      const float last = b.last;
+      load_tt(b, ahead);
+      put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, G, T{});
+      block_barrier();
 
-    floatx4 dU = {};
-    const char* tt = p.ws_tt + blk * kTriFrags * kOpFrag;
+      if (owner) {
+        const Op3 e0 = load_frag<Op3>(ef, lane), e1 = load_frag<Op3>(ef + kOp3, lane);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-      if (ks >= wave / 2) dU = mma(load_frag<Op>(tt + upper_frag(wave, ks) * kOpFrag, lane), load_frag<Op>(xf + ks * kOpFrag, lane), dU);
-    const floatx4 dE = beta * dU;
-    put_op(ef + (wave >> 1) * kOpFrag, wave & 1, li, g, -(gam * dE), T{});
-    const T* fp = (const T*)p.ws_f + blk * kGdrChunk * p.dv + (int64_t)r0 * p.dv + col;
-    float* db = (float*)p.ws_db + (blk * (p.dv / 16) + part) * kGdrChunk + r0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (r0 + r < n) store_f32(dvp, (c * kGdrChunk + r) * p.sdv.t, dE[r]);
-      float x = dU[r] * load_f32(fp, (int64_t)r * p.dv);
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d);
-      if (li == 0) db[r] = x;
-    }
-    block_barrier();
-
-    if (owner) {
-      const char* kt = p.ws_kt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
-      const char* qt = p.ws_qt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        S[m] = S[m] * last;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const int f = (2 * (wave * RT + m) + ks) * kInFrag;
-          S[m] = mma(load_frag<In>(qt + f, lane), load_frag<Op>(gf + ks * kOpFrag, lane), S[m]);
-          S[m] = mma(load_frag<In>(kt + f, lane), load_frag<Op>(ef + ks * kOpFrag, lane), S[m]);
+        for (int m = 0; m < RT; ++m) {
+          const floatx4 add = ld4f(&d0[c & 1][((wave * RT + m) * 64 + lane) * 4]);
+          S[m] = mma(b.kt[m][1], e1, mma(b.kt[m][0], e0, S[m] * last + add));
         }
       }
+      float* db = (float*)p.ws_db + ((blk0 + c * p.Hv) * (p.dv / 16) + part) * kGdrChunk + r0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r0 + r < n) store_f32(dvp, (c * kGdrChunk + r) * p.sdv.t, dE[r]);
+        float x = dU[r] * b.f[r];
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d);
+        if (li == 0) db[r] = x;
+      }
+      load_kt(b, ahead);
+      put_state();
+      block_barrier();
+    };
+    block_barrier();
+    block_barrier();
+    if (nc > 0) {
+      Buf b0, b1;
+      const int64_t second = clamp_chunk(nc - 2);
+      load_k(b0, nc - 1);
+      load_tt(b0, nc - 1);
+      load_kt(b0, nc - 1);
+      load_k(b1, second);
+      load_tt(b1, second);
+      load_kt(b1, second);
+      for (int64_t c = nc - 1; c >= 0; c -= 2) {
+        step(b0, c);
+        if (c > 0) step(b1, c - 1);
+      }
     }
-    block_barrier();   // gf and ef are read before the next chunk's writes
+    if (p.dS0 && owner) {
+#pragma unroll
+      for (int m = 0; m < RT; ++m) {
+        float* at = p.dS0 + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
+      }
+    }
+    return;
   }
 
-  if (p.dS0 && owner) {
+  const int tid = threadIdx.x & 255;
+  const T* dop = (const T*)p.dO + seq.row * p.sdo.b + h * p.sdo.h + col;
+  T* sp = (T*)p.ws_ds + blk0 * p.dk * p.dv + 16 * part;
+  struct Buf {
+    float o[4];
+    floatx4 gam;
+    Op3 pm[2];
+    In qt[RT][2];
+  };
+  auto load_o = [&](Buf& b, int64_t c) {
 #pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      float* at = p.dS0 + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+    for (int r = 0; r < 4; ++r) b.o[r] = load_f32(dop, (seq.t0 + min64(c * kGdrChunk + r0 + r, seq.len - 1)) * p.sdo.t);
+    b.gam = ld4f(gates + c * p.Hv * kGateFloats + kGateGam + r0);
+  };
+  auto load_pq = [&](Buf& b, int64_t c) {
+    const char* at = p.ws_p + (blk0 + c * p.Hv) * kTriFrags * kOp3;
+    if (wave < 2) b.pm[0] = load_frag<Op3>(at + upper_frag(wave, 0) * kOp3, lane);
+    b.pm[1] = load_frag<Op3>(at + upper_frag(wave, 1) * kOp3, lane);
+    if (!owner) return;
+    const char* qt = p.ws_qt + ((seq.slot0 + c) * p.Hk + kh) * (int64_t)(DK / 8) * kIn;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) b.qt[m][ks] = load_frag<In>(qt + (2 * (wave * RT + m) + ks) * kIn, lane);
+  };
+  auto spread = [&](Buf& b, int64_t c) {       // dO of chunk c as operands
+    const int64_t left = seq.len - c * kGdrChunk;
+    floatx4 o;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = r0 + r < left ? b.o[r] : 0.f;
+    put_op<1>(of + (wave >> 1) * kIn, wave & 1, li, g, o, T{});
+    put_op<3>(gf + (wave >> 1) * kOp3, wave & 1, li, g, p.scale * (b.gam * o), T{});
+    load_o(b, clamp_chunk(c - 1));
+  };
+  auto products = [&](Buf& b, int64_t c) {
+    floatx4 X = mma(b.pm[1], load_frag<In>(of + kIn, lane), floatx4{});
+    if (wave < 2) X = mma(b.pm[0], load_frag<In>(of, lane), X);
+    *reinterpret_cast<floatx4*>(&x0[c & 1][(wave * 64 + lane) * 4]) = X;
+    if (owner) {
+      const Op3 g0 = load_frag<Op3>(gf, lane), g1 = load_frag<Op3>(gf + kOp3, lane);
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+        *reinterpret_cast<floatx4*>(&d0[c & 1][((wave * RT + m) * 64 + lane) * 4]) = mma(b.qt[m][1], g1, mma(b.qt[m][0], g0, floatx4{}));
     }
+    load_pq(b, clamp_chunk(c - 1));
+  };
+  Buf b;
+  if (nc > 0) {
+    load_o(b, nc - 1);
+    load_pq(b, nc - 1);
+    spread(b, nc - 1);
+  }
+  block_barrier();
+  if (nc > 0) products(b, nc - 1);
+  block_barrier();
+  for (int64_t c = nc - 1; c >= 0; --c) {
+    // dS at this chunk's end; what the next one needs
+    write_rows<T>(sf, kOp3, DK, sp + c * p.Hv * p.dk * p.dv, p.dv, tid);
+    if (c > 0) spread(b, c - 1);
+    block_barrier();
+    if (c > 0) products(b, c - 1);
+    block_barrier();
+    block_barrier();
   }
 }
 
 template <typename T, int DK>
 hipError_t launch_scan(const GdrParams& p, hipStream_t s, int kind) {
   const dim3 grid((unsigned)gdr_blocks(p.n_seq * p.Hv, p.dv / 16));
-  if (kind == 0) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, false>), grid, dim3(256), 0, s, p);
-  else if (kind == 1) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, true>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((gdr_rscan_kernel<T, DK>), grid, dim3(256), 0, s, p);
+  if (kind == 0) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, false>), grid, dim3(512), 0, s, p);
+  else if (kind == 1) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, true>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((gdr_rscan_kernel<T, DK>), grid, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
