@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
   const int64_t slot = blockIdx.x;
   if (!gdr_find(p, slot, &seq, &chunk)) return;
   const int kh = blockIdx.y, grp = p.Hv / p.Hk;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = wave_id(), li = lane & 15, g = lane >> 4;
   const int64_t t0 = seq.t0 + chunk * kGdrChunk, left = seq.len - chunk * kGdrChunk;
   const int n = left < kGdrChunk ? (int)left : kGdrChunk;
   const int tok = 16 * wave + li;                 // this lane's token
@@ -43,10 +43,10 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
   char* dp_f = tri[wave];                         // dP (transposed, then as it is)
   char* da_f = tri[wave] + 2 * kOpFrag;
 
-  const T* qrow = (const T*)p.q + seq.row * p.sq.b + kh * p.sq.h + (t0 + tok) * p.sq.t + 4 * g;
-  const T* krow = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + (t0 + tok) * p.sk.t + 4 * g;
-  const char* kt = p.ws_kt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
-  const char* qt = p.ws_qt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
+  const auto qrow = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + tok) * p.sq.t + 4 * g;
+  const auto krow = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + tok) * p.sk.t + 4 * g;
+  const auto kt = as_global((const char*)p.ws_kt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
+  const auto qt = as_global((const char*)p.ws_qt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
 
   floatx4 dq[MT], dk[MT];
 #pragma unroll
@@ -55,20 +55,20 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
   for (int hg = 0; hg < grp; ++hg) {
     const int h = kh * grp + hg;
     const int64_t blk = slot * p.Hv + h;
-    const float* gate = (const float*)p.ws_gate + blk * kGateFloats;
+    const auto gate = global_in<float>(p.ws_gate) + blk * kGateFloats;
     if (wave == 0) {
       ghi[lane] = gate[kGateHi + lane];
       glo[lane] = gate[kGateLo + lane];
       bet[lane] = gate[kGateBeta + lane];
     }
     const float gam = gate[kGateGam + tok], eta = gate[kGateEta + tok], last = gate[kGateLast];
-    const T* F = (const T*)p.ws_f + blk * kGdrChunk * DV + 8 * g;
-    const T* St = (const T*)p.ws_s + blk * DK * DV + 8 * g;
-    const T* dSt = (const T*)p.ws_ds + blk * DK * DV + 8 * g;
-    const T* dO = (const T*)p.dO + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t + 8 * g;
-    const T* dE = (const T*)p.dv_ + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t + 8 * g;
+    const auto F = global_in<T>(p.ws_f) + blk * kGdrChunk * DV + 8 * g;
+    const auto St = global_in<T>(p.ws_s) + blk * DK * DV + 8 * g;
+    const auto dSt = global_in<T>(p.ws_ds) + blk * DK * DV + 8 * g;
+    const auto dO = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t + 8 * g;
+    const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t + 8 * g;
     auto f_frag = [&](int tile, int kv) { return load_row8(F + (int64_t)(16 * tile + li) * DV + 32 * kv); };
-    auto rows_of = [&](const T* base, int64_t st, int tile, int kv) {
+    auto rows_of = [&](GlobalPtr<const T> base, int64_t st, int tile, int kv) {
       In x;
       zero_frag(x);
       if (16 * tile + li < n) x = load_row8(base + (int64_t)(16 * tile + li) * st + 32 * kv);
@@ -205,22 +205,22 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
         if (lane + d < 64) x += dn;
       }
       if (lane < n) {
-        const float w = load_f32((const T*)p.w, seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
-        store_f32((T*)p.dw, seq.row * p.sdw.b + h * p.sdw.h + (t0 + lane) * p.sdw.t,
-                  (float)(x * (double)gdr_gate_grad(w, p.gate, p.g_min)));
-        const float* db = (const float*)p.ws_db + blk * (DV / 16) * kGdrChunk + lane;
+        const float w = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
+        put(global_out<T>(p.dw) + seq.row * p.sdw.b + h * p.sdw.h + (t0 + lane) * p.sdw.t,
+            (float)(x * (double)gdr_gate_grad(w, p.gate, p.g_min)));
+        const auto db = global_in<float>(p.ws_db) + blk * (DV / 16) * kGdrChunk + lane;
         float sum = 0.f;
 #pragma unroll
         for (int c = 0; c < DV / 16; ++c) sum += db[c * kGdrChunk];
-        store_f32((T*)p.dbeta, seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, sum);
+        put(global_out<T>(p.dbeta) + seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, sum);
       }
     }
     __syncthreads();
   }
 
   if (live) {
-    T* dqp = (T*)p.dq + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + tok) * p.sdq.t + 4 * g;
-    T* dkp = (T*)p.dk_ + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + tok) * p.sdk.t + 4 * g;
+    const auto dqp = global_out<T>(p.dq) + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + tok) * p.sdq.t + 4 * g;
+    const auto dkp = global_out<T>(p.dk_) + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + tok) * p.sdk.t + 4 * g;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       store_row4(dqp + 16 * m, dq[m]);

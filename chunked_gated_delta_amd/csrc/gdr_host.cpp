@@ -21,7 +21,8 @@ Span dense(const void* p, double bytes) {
   return Span{lo, lo + (uintptr_t)bytes};
 }
 
-constexpr int64_t kMaxExtent = (int64_t)1 << 46;   // bytes
+constexpr int64_t kMaxExtent = (int64_t)1 << 46;        // bytes
+constexpr int64_t kMaxTokenStride = (int64_t)1 << 25;   // bytes: the 64 rows of a chunk within 32 bits
 
 // the span of a [B, H, T, D] view, D contiguous (strides already checked)
 Span view(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_t D, int64_t esz) {
@@ -43,6 +44,7 @@ int check_strides(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T
     if (st[i] < 0 || st[i] > kMaxExtent || (st[i] * esz) % align != 0) return KDA_ERR_ARG;
     reach += (double)(n[i] - 1) * (double)st[i];
   }
+  if (T > 1 && s.t * esz > kMaxTokenStride) return KDA_ERR_ARG;
   return reach * esz > (double)kMaxExtent ? KDA_ERR_SHAPE : KDA_OK;
 }
 

@@ -151,6 +151,40 @@ __device__ __forceinline__ float gdr_gate_grad(float w, int gate, float g_min) {
   return gate == KDA_GATE_BOUNDED ? g_min * s * (1.f / (1.f + expf(w))) : -s;
 }
 
+// ---------------------------------------------------------------- memory accesses
+
+// Pointers taken from the parameter block are global memory; said in their type, so that their accesses
+// are global instructions wherever the pointer went (a flat one would also count as an LDS access, and
+// every barrier's wait for LDS would wait for it).
+#define KDA_GLOBAL __attribute__((address_space(1)))
+template <typename T> using GlobalPtr = KDA_GLOBAL T*;
+template <typename T> __device__ __forceinline__ GlobalPtr<T> as_global(T* p) { return (GlobalPtr<T>)p; }
+template <typename T> __device__ __forceinline__ GlobalPtr<const T> global_in(const void* p) { return (GlobalPtr<const T>)p; }
+template <typename T> __device__ __forceinline__ GlobalPtr<T> global_out(void* p) { return (GlobalPtr<T>)p; }
+template <typename To, typename From> __device__ __forceinline__ const To* repoint(const From* p) { return reinterpret_cast<const To*>(p); }
+template <typename To, typename From> __device__ __forceinline__ const KDA_GLOBAL To* repoint(const KDA_GLOBAL From* p) {
+  return reinterpret_cast<const KDA_GLOBAL To*>(p);
+}
+template <typename To, typename From> __device__ __forceinline__ To* repoint(From* p) { return reinterpret_cast<To*>(p); }
+template <typename To, typename From> __device__ __forceinline__ KDA_GLOBAL To* repoint(KDA_GLOBAL From* p) {
+  return reinterpret_cast<KDA_GLOBAL To*>(p);
+}
+__device__ __forceinline__ float get(const KDA_GLOBAL uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float get(const KDA_GLOBAL float* p) { return *p; }
+__device__ __forceinline__ void put(KDA_GLOBAL uint16_t* p, float x) { *p = (uint16_t)pk_bf16(x, x); }
+__device__ __forceinline__ void put(KDA_GLOBAL float* p, float x) { *p = x; }
+// element `off` (of lanes) behind `base` (of the wavefront): the address needs no vector arithmetic
+template <typename T> __device__ __forceinline__ const KDA_GLOBAL T* lane_at(const KDA_GLOBAL T* base, uint32_t bytes) {
+  return (const KDA_GLOBAL T*)((const KDA_GLOBAL char*)base + bytes);
+}
+template <typename T> __device__ __forceinline__ KDA_GLOBAL T* lane_at(KDA_GLOBAL T* base, uint32_t bytes) {
+  return (KDA_GLOBAL T*)((KDA_GLOBAL char*)base + bytes);
+}
+template <typename P> __device__ __forceinline__ floatx4 ld4f(P p) { return *repoint<floatx4>(p); }
+
+// the wavefront's number in its workgroup, known to be the same in all lanes
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // ---------------------------------------------------------------- operand fragments
 
 // A fragment is 8 values a lane: of the A operand row li, of the B operand column li, at contraction
@@ -206,47 +240,87 @@ __device__ __forceinline__ floatx4 mma(const float8v& a, const float8v& b, float
   return c;
 }
 
+// acc + sum over steps of a[i] b[i], as chains of their own added at the end: one dependent matrix
+// instruction takes 32 cycles, an independent one 16
+template <int K, int N> __device__ __forceinline__ floatx4 mma_steps(const bf16x8 (&a)[K], const Planes<N> (&b)[K], floatx4 acc) {
+  floatx4 c[N];
+#pragma unroll
+  for (int n = 1; n < N; ++n) c[n] = floatx4{};
+  c[0] = acc;
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) c[n] = mfma(a[i], b[i].p[n], c[n]);
+#pragma unroll
+  for (int n = N - 1; n > 0; --n) c[n - 1] += c[n];
+  return c[0];
+}
+template <int K> __device__ __forceinline__ floatx4 mma_steps(const float8v (&a)[K], const float8v (&b)[K], floatx4 acc) {
+  floatx4 c[2] = {acc, floatx4{}};
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[i][e], c[e & 1], 0, 0, 0);
+  return c[0] + c[1];
+}
+// both sides in three planes: the six products above the last plane's size
+template <int K> __device__ __forceinline__ floatx4 mma_steps(const Planes<3> (&a)[K], const Planes<3> (&b)[K], floatx4 acc) {
+  floatx4 c[3] = {acc, floatx4{}, floatx4{}};
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    c[2] = mfma(a[i].p[1], b[i].p[1], c[2]);
+    c[1] = mfma(a[i].p[1], b[i].p[0], c[1]);
+    c[0] = mfma(a[i].p[0], b[i].p[0], c[0]);
+    c[2] = mfma(a[i].p[2], b[i].p[0], c[2]);
+    c[1] = mfma(a[i].p[0], b[i].p[1], c[1]);
+    c[2] = mfma(a[i].p[0], b[i].p[2], c[2]);
+  }
+  return c[0] + (c[1] + c[2]);
+}
+
 __device__ __forceinline__ void zero_frag(bf16x8& f) { f = bf16x8{}; }
 __device__ __forceinline__ void zero_frag(float8v& f) { f = float8v{}; }
 
 // 8 consecutive values of a row in memory (16-byte aligned)
-__device__ __forceinline__ bf16x8 load_row8(const uint16_t* p) { return ld8(p); }
-__device__ __forceinline__ float8v load_row8(const float* p) {
-  const floatx4 a = *reinterpret_cast<const floatx4*>(p), b = *reinterpret_cast<const floatx4*>(p + 4);
+__device__ __forceinline__ bf16x8 load_row8(const KDA_GLOBAL uint16_t* p) { return *repoint<bf16x8>(p); }
+__device__ __forceinline__ bf16x8 load_row8(const uint16_t* p) { return *repoint<bf16x8>(p); }
+template <typename P> __device__ __forceinline__ float8v load_two4(P p) {
+  const floatx4 a = ld4f(p), b = ld4f(p + 4);
   return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
+__device__ __forceinline__ float8v load_row8(const KDA_GLOBAL float* p) { return load_two4(p); }
+__device__ __forceinline__ float8v load_row8(const float* p) { return load_two4(p); }
 
 // fragments stored plane by plane (LDS or workspace)
 template <typename F> struct FragIo;
 template <> struct FragIo<bf16x8> {
-  static __device__ __forceinline__ bf16x8 load(const char* at, int lane) { return ld8(at + lane * 16); }
-  static __device__ __forceinline__ void store(char* at, int lane, bf16x8 f) { *reinterpret_cast<bf16x8*>(at + lane * 16) = f; }
+  template <typename P> static __device__ __forceinline__ bf16x8 load(P at, int lane) { return *repoint<bf16x8>(at + lane * 16); }
+  template <typename P> static __device__ __forceinline__ void store(P at, int lane, bf16x8 f) { *repoint<bf16x8>(at + lane * 16) = f; }
 };
 template <int N> struct FragIo<Planes<N>> {
-  static __device__ __forceinline__ Planes<N> load(const char* at, int lane) {
+  template <typename P> static __device__ __forceinline__ Planes<N> load(P at, int lane) {
     Planes<N> f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) f.p[i] = ld8(at + i * kPlane + lane * 16);
+    for (int i = 0; i < N; ++i) f.p[i] = *repoint<bf16x8>(at + i * kPlane + lane * 16);
     return f;
   }
-  static __device__ __forceinline__ void store(char* at, int lane, const Planes<N>& f) {
+  template <typename P> static __device__ __forceinline__ void store(P at, int lane, const Planes<N>& f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8*>(at + i * kPlane + lane * 16) = f.p[i];
+    for (int i = 0; i < N; ++i) *repoint<bf16x8>(at + i * kPlane + lane * 16) = f.p[i];
   }
 };
 template <> struct FragIo<float8v> {
-  static __device__ __forceinline__ float8v load(const char* at, int lane) {
-    const floatx4 a = *reinterpret_cast<const floatx4*>(at + lane * 16);
-    const floatx4 b = *reinterpret_cast<const floatx4*>(at + kPlane + lane * 16);
+  template <typename P> static __device__ __forceinline__ float8v load(P at, int lane) {
+    const floatx4 a = *repoint<floatx4>(at + lane * 16), b = *repoint<floatx4>(at + kPlane + lane * 16);
     return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
-  static __device__ __forceinline__ void store(char* at, int lane, const float8v& f) {
-    *reinterpret_cast<floatx4*>(at + lane * 16) = floatx4{f[0], f[1], f[2], f[3]};
-    *reinterpret_cast<floatx4*>(at + kPlane + lane * 16) = floatx4{f[4], f[5], f[6], f[7]};
+  template <typename P> static __device__ __forceinline__ void store(P at, int lane, const float8v& f) {
+    *repoint<floatx4>(at + lane * 16) = floatx4{f[0], f[1], f[2], f[3]};
+    *repoint<floatx4>(at + kPlane + lane * 16) = floatx4{f[4], f[5], f[6], f[7]};
   }
 };
-template <typename F> __device__ __forceinline__ F load_frag(const char* at, int lane) { return FragIo<F>::load(at, lane); }
-template <typename F> __device__ __forceinline__ void store_frag(char* at, int lane, const F& f) { FragIo<F>::store(at, lane, f); }
+template <typename F, typename P> __device__ __forceinline__ F load_frag(P at, int lane) { return FragIo<F>::load(at, lane); }
+template <typename P, typename F> __device__ __forceinline__ void store_frag(P at, int lane, const F& f) { FragIo<F>::store(at, lane, f); }
 
 template <int N> __device__ __forceinline__ Planes<N> make_op(float8v f, uint16_t) {
   Planes<N> r;
@@ -281,18 +355,16 @@ template <typename T> __device__ __forceinline__ T frag_at(const char* frag, int
   else return *reinterpret_cast<const T*>(frag + ((k >> 2) & 1) * kPlane + ln * 16 + (k & 3) * 4);
 }
 
-__device__ __forceinline__ floatx4 ld4f(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
-
 // 4 consecutive values of a row in memory (8-byte aligned bf16, 16-byte aligned fp32)
-__device__ __forceinline__ floatx4 load_row4(const uint16_t* p) {
-  const u32x2v x = *reinterpret_cast<const u32x2v*>(p);
+__device__ __forceinline__ floatx4 load_row4(const KDA_GLOBAL uint16_t* p) {
+  const u32x2v x = *repoint<u32x2v>(p);
   return floatx4{lo_bf16(x[0]), hi_bf16(x[0]), lo_bf16(x[1]), hi_bf16(x[1])};
 }
-__device__ __forceinline__ floatx4 load_row4(const float* p) { return ld4f(p); }
-__device__ __forceinline__ void store_row4(uint16_t* p, floatx4 x) {
-  *reinterpret_cast<u32x2v*>(p) = u32x2v{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+__device__ __forceinline__ floatx4 load_row4(const KDA_GLOBAL float* p) { return ld4f(p); }
+__device__ __forceinline__ void store_row4(KDA_GLOBAL uint16_t* p, floatx4 x) {
+  *repoint<u32x2v>(p) = u32x2v{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
 }
-__device__ __forceinline__ void store_row4(float* p, floatx4 x) { *reinterpret_cast<floatx4*>(p) = x; }
+__device__ __forceinline__ void store_row4(KDA_GLOBAL float* p, floatx4 x) { *repoint<floatx4>(p) = x; }
 
 // Workgroups of one (sequence, head) read the same operands: they get blocks of one XCD (block b runs
 // on XCD b mod 8), so that its L2 serves all but the first.  Returns false for a block without work.

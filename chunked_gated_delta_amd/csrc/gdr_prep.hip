@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
   GdrSeq seq;
   int64_t chunk;
   if (!gdr_find(p, slot, &seq, &chunk)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = wave_id(), li = lane & 15, g = lane >> 4;
   const int64_t t0 = seq.t0 + chunk * kGdrChunk;
   const int64_t left = seq.len - chunk * kGdrChunk;
   const int n = left < kGdrChunk ? (int)left : kGdrChunk;   // tokens of this chunk
@@ -97,8 +97,8 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
   In kr[KS], qr[KS];
   {
     const int row = 16 * wave + li;
-    const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + (t0 + row) * p.sk.t + 8 * g;
-    const T* qp = (const T*)p.q + seq.row * p.sq.b + kh * p.sq.h + (t0 + row) * p.sq.t + 8 * g;
+    const auto kp = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + row) * p.sk.t + 8 * g;
+    const auto qp = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + row) * p.sq.t + 8 * g;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       zero_frag(kr[ks]);
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
     }
   }
   // channel-major fragments of an operand in kf: the A operand of products over the chunk's tokens
-  auto transpose_out = [&](char* out) {
+  auto transpose_out = [&](GlobalPtr<char> out) {
 #pragma unroll
     for (int f = 0; f < DK / 32; ++f) {   // DK / 16 row tiles x 2 steps over 4 wavefronts
       const int id = wave + 4 * f, m = id >> 1, ks = id & 1;
@@ -133,13 +133,13 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) store_frag(kf + (wave * KS + ks) * kInFrag, lane, qr[ks]);
     __syncthreads();
-    transpose_out(p.ws_qt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag);
+    transpose_out(as_global(p.ws_qt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag);
     __syncthreads();
   }
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) store_frag(kf + (wave * KS + ks) * kInFrag, lane, kr[ks]);
   __syncthreads();
-  transpose_out(p.ws_kt + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag);
+  transpose_out(as_global(p.ws_kt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag);
 
   floatx4 kk[4], qk[4];
 #pragma unroll
@@ -159,13 +159,13 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
   for (int hg = 0; hg < grp; ++hg) {
     const int h = kh * grp + hg;
     const int64_t blk = slot * p.Hv + h;
-    float* gate = (float*)p.ws_gate + blk * kGateFloats;
+    const auto gate = global_out<float>(p.ws_gate) + blk * kGateFloats;
     if (wave == 0) {   // one token a lane
       double G = 0.0;
       float b = 0.f;
       if (lane < n) {
-        G = (double)gdr_gate(load_f32((const T*)p.w, seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t), p.gate, p.g_min);
-        b = load_f32((const T*)p.beta, seq.row * p.sb.b + h * p.sb.h + (t0 + lane) * p.sb.t);
+        G = (double)gdr_gate(get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t), p.gate, p.g_min);
+        b = get(global_in<T>(p.beta) + seq.row * p.sb.b + h * p.sb.h + (t0 + lane) * p.sb.t);
       }
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -217,12 +217,12 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
         for (int r = 0; r < 4; ++r) mat[(16 * i + 4 * g + r) * kLd + 16 * wave + li] = X[i][r];
       __syncthreads();
       if (variant == 0) {
-        char* out = p.ws_ti + blk * kTriFrags * kOpFrag;
+        const auto out = as_global(p.ws_ti) + blk * kTriFrags * kOpFrag;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * kOpFrag, lane, make_op<3>(rows_frag(mat, wave, ks, li, g), T{}));
       } else {
-        char* out = p.ws_tt + blk * kTriFrags * kOpFrag;
+        const auto out = as_global(p.ws_tt) + blk * kTriFrags * kOpFrag;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * kOpFrag, lane, make_op<3>(cols_frag(mat, wave, ks, li, g), T{}));
@@ -238,13 +238,13 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
       }
     __syncthreads();
     if constexpr (BWD) {
-      char* out = p.ws_p + blk * kTriFrags * kOpFrag;
+      const auto out = as_global(p.ws_p) + blk * kTriFrags * kOpFrag;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
         if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * kOpFrag, lane, make_op<3>(cols_frag(mat, wave, ks, li, g), T{}));
     } else {
       // the outputs' own factor, rounded to the inputs' type: it enters o alone, which is rounded to that type
-      char* out = p.ws_p + blk * kTriFrags * op_frag<T, 1>();
+      const auto out = as_global(p.ws_p) + blk * kTriFrags * op_frag<T, 1>();
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
         if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * op_frag<T, 1>(), lane, make_op<1>(rows_frag(mat, wave, ks, li, g), T{}));

@@ -9,23 +9,32 @@
 //    state's rows, in registers (fp32 matrix-core results).  Wavefronts 4-7, one more on each SIMD, form the
 //    outputs (or, in the backward's run, write out the entering states and F) in the chain's shadow.
 //  - Every A operand (K, Q, K^T, T', P) has exactly one reader in the workgroup and is loaded straight into its
-//    registers, for the chunk after the next as soon as this chunk's is used: two register buffers, the
-//    loop unrolled by two.  Loads past the last chunk are clamped to it.
+//    registers, the chain's kAhead chunks ahead, as soon as the registers' present contents are used.  Loads
+//    past the last chunk are clamped to it.
 //  - What the wavefronts exchange (the state, E, U: 16 columns each) goes through LDS as ready B operands.
+//  - The compute unit's address path is what limits a step next (77 % busy when each lane fetched its own
+//    values of v and the gates and wrote its own of o), so wavefronts 4-7 move v, o and the gates in
+//    rows of 16 bytes a lane and turn them in LDS.
 // Rows behind the sequence's end read its last row; their E is set to zero, so nothing of them reaches
 // the state, and their outputs are not written.
+#include <type_traits>
+
 #include "gdr_internal.h"
 
 namespace kda {
 
 namespace {
 
+constexpr int kAhead = 2;   // chunks ahead that the chain's operands are loaded
+
 __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
+__device__ __forceinline__ float value(float x) { return x; }
 
 // Writes `rows` contraction places x 16 columns of a B-operand array (first planes) to row-major memory:
 // a lane takes 8 columns of one place.
 template <typename T>
-__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, T* out, int64_t ld, int tid) {
+__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int ld, int tid) {
   for (int i = tid; i < rows * 2; i += 256) {
     const int r = i >> 1, c0 = (i & 1) * 8;
     const char* fr = frags + (r >> 5) * frag_bytes;
@@ -34,16 +43,67 @@ __device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, in
     for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(fr, r & 31, c0 + e);
     typename Frags<T>::In v;
     __builtin_memcpy(&v, x, sizeof(v));
-    *reinterpret_cast<typename Frags<T>::In*>(out + (int64_t)r * ld + c0) = v;
+    *repoint<typename Frags<T>::In>(out + r * ld + c0) = v;
   }
 }
+
+// All ones or zeros, of a condition on values of the wavefront.  Positions advance by masked amounts, not
+// behind a branch: this compiler leaves out the wait between a matrix instruction and the vector read
+// of its result where a branch target lies between (shown in its assembly; the first value read was wrong).
+__device__ __forceinline__ int64_t mask_of(bool c) { return __builtin_amdgcn_readfirstlane(c ? -1 : 0); }
+
+// Byte offsets, from a chunk's first row, of the rows that a lane reads of a strided tensor: row `row` as
+// an A operand, rows r0 .. r0 + 3 as part of a result tile; in the last chunk the rows behind the
+// sequence's end become its last one.
+struct LaneRow {
+  uint32_t whole, tail;
+  __device__ __forceinline__ LaneRow(int row, int last_rows, int64_t stride, int at, int esz)
+      : whole((uint32_t)((row * stride + at) * esz)), tail((uint32_t)((min(row, last_rows - 1) * stride + at) * esz)) {}
+  __device__ __forceinline__ uint32_t of(bool last) const { return last ? tail : whole; }
+};
+
+// 64 tokens x 16 columns in LDS, column by column (a result tile's lane reads 4 tokens of its column).
+// Threads 0 .. 127 of four wavefronts move them: thread t has columns 8 (t & 1) .. + 7 of token t / 2.
+template <typename T> struct Turned {
+  static constexpr int kLd = sizeof(T) == 2 ? 72 : 68;
+  T x[16 * kLd];
+  __device__ __forceinline__ void put_row(int t, const typename Frags<T>::In& v) {
+    T e8[8];
+    __builtin_memcpy(e8, &v, sizeof(v));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[(8 * (t & 1) + e) * kLd + (t >> 1)] = e8[e];
+  }
+  __device__ __forceinline__ typename Frags<T>::In row(int t) const {
+    T e8[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) e8[e] = x[(8 * (t & 1) + e) * kLd + (t >> 1)];
+    typename Frags<T>::In v;
+    __builtin_memcpy(&v, e8, sizeof(v));
+    return v;
+  }
+  __device__ __forceinline__ floatx4 tile(int li, int r0) const {
+    if constexpr (sizeof(T) == 2) {
+      const u32x2v p = *reinterpret_cast<const u32x2v*>(x + li * kLd + r0);
+      return floatx4{lo_bf16(p[0]), hi_bf16(p[0]), lo_bf16(p[1]), hi_bf16(p[1])};
+    } else {
+      return *reinterpret_cast<const floatx4*>(x + li * kLd + r0);
+    }
+  }
+  __device__ __forceinline__ void put_tile(int li, int r0, floatx4 v) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2v*>(x + li * kLd + r0) = u32x2v{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+    else *reinterpret_cast<floatx4*>(x + li * kLd + r0) = v;
+  }
+};
+// a chunk's gates in LDS
+struct Gates {
+  float gam[64], eta[64], beta[64];
+};
 
 template <typename T, int DK, bool STATES>
 __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
   using Op3 = typename Frags<T>::template Op<3>;
   using Op2 = typename Frags<T>::template Op<2>;
-  using Op1 = typename Frags<T>::template Op<1>;
   constexpr int KS = DK / 32;
   constexpr int RT = DK >= 64 ? DK / 64 : 1;      // state row tiles of a wavefront
   constexpr int kIn = in_frag<T>(), kOp1 = op_frag<T, 1>(), kOp2 = op_frag<T, 2>(), kOp3 = op_frag<T, 3>();
@@ -51,6 +111,9 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
   __shared__ __attribute__((aligned(16))) char ef[2 * kOp3];               // E
   __shared__ __attribute__((aligned(16))) char wf[2 * kOp3];               // eta U
   __shared__ __attribute__((aligned(16))) char uf[2 * kOp2];               // U (F where states are written)
+  __shared__ __attribute__((aligned(16))) Turned<T> vt[2];                 // v, by the chunk's parity
+  __shared__ __attribute__((aligned(16))) Turned<T> ot;                    // o on its way out
+  __shared__ __attribute__((aligned(16))) Gates gate[2];
 
   int64_t unit;
   int part;
@@ -60,23 +123,21 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
   const GdrSeq seq = gdr_seq(p, s);
   const int64_t nc = seq.n_chunks;
   const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
-  const bool chain = threadIdx.x < 256;
-  const int wave = (threadIdx.x >> 6) & 3;
+  const int wave = wave_id() & 3;
   const int col = 16 * part + li;
   const int r0 = 16 * wave + 4 * g;               // first of this lane's 4 token rows in result tiles
+  const int last_rows = (int)(seq.len - (nc - 1) * kGdrChunk);   // tokens of the last chunk
   const int64_t blk0 = seq.slot0 * p.Hv + h;      // workspace block of chunk 0; the next is Hv further
-  const float* gates = (const float*)p.ws_gate + blk0 * kGateFloats;
-  auto clamp_chunk = [&](int64_t c) { return min64(c, nc - 1); };
-  auto row_of = [&](int64_t c) { return seq.t0 + min64(c * kGdrChunk + 16 * wave + li, seq.len - 1); };
+  const auto gates = global_in<float>(p.ws_gate) + blk0 * kGateFloats;
 
-  if (chain) {
+  if (wave_id() < 4) {
     const bool owner = wave * RT < DK / 16;
     floatx4 S[RT];
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
       S[m] = floatx4{};
       if (owner && p.S0) {
-        const float* at = p.S0 + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+        const auto at = global_in<float>(p.S0) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
       }
@@ -91,94 +152,101 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
     put_state();
     block_barrier();
 
-    const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + 8 * g;
-    const T* vp = (const T*)p.v + seq.row * p.sv.b + h * p.sv.h + col;
-    struct Buf {
-      In k[KS];
-      Op3 ti[2];
-      In kt[RT][2];
-      float v[4];
-      floatx4 gam, eta, beta;
-      float last;
-    };
-    auto load_k = [&](Buf& b, int64_t c) {
-      const T* at = kp + row_of(c) * p.sk.t;
+    // BOTH: the wavefront's rows of T' reach into both steps of 32 tokens (wavefronts 2 and 3)
+    auto walk = [&](auto both) {
+      constexpr int TS = decltype(both)::value ? 2 : 1;
+      struct Buf {
+        In k[KS];
+        Op3 ti[TS];
+        In kt[RT][2];
+      };
+      // where the next loads come from
+      int64_t at = 0;
+      auto kp = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + seq.t0 * p.sk.t;
+      auto tp = as_global((const char*)p.ws_ti) + blk0 * kTriFrags * kOp3 + lower_frag(wave, 0) * kOp3;
+      auto ktp = as_global((const char*)p.ws_kt) + (seq.slot0 * p.Hk + kh) * (int64_t)(DK / 8) * kIn + 2 * (owner ? wave * RT : 0) * kIn;
+      const LaneRow krow(16 * wave + li, last_rows, p.sk.t, 8 * g, sizeof(T));
+      auto load_k = [&](Buf& b) {
+        const auto from = lane_at(kp, krow.of(at == nc - 1));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(at + 32 * ks);
-    };
-    auto load_v = [&](Buf& b, int64_t c) {
+        for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(from + 32 * ks);
+      };
+      auto load_ti = [&](Buf& b) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) b.v[r] = load_f32(vp, (seq.t0 + min64(c * kGdrChunk + r0 + r, seq.len - 1)) * p.sv.t);
-      b.gam = ld4f(gates + c * p.Hv * kGateFloats + kGateGam + r0);
-    };
-    auto load_ti = [&](Buf& b, int64_t c) {
-      const char* at = p.ws_ti + (blk0 + c * p.Hv) * kTriFrags * kOp3;
-      b.ti[0] = load_frag<Op3>(at + lower_frag(wave, 0) * kOp3, lane);
-      if (wave >= 2) b.ti[1] = load_frag<Op3>(at + lower_frag(wave, 1) * kOp3, lane);
-      const float* gt = gates + c * p.Hv * kGateFloats;
-      b.eta = ld4f(gt + kGateEta + r0);
-      b.beta = ld4f(gt + kGateBeta + r0);
-      b.last = gt[kGateLast];
-    };
-    auto load_kt = [&](Buf& b, int64_t c) {
-      if (!owner) return;
-      const char* at = p.ws_kt + ((seq.slot0 + c) * p.Hk + kh) * (int64_t)(DK / 8) * kIn;
+        for (int ks = 0; ks < TS; ++ks) b.ti[ks] = load_frag<Op3>(tp + ks * kOp3, lane);
+      };
+      auto load_kt = [&](Buf& b) {   // and on to the next chunk
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+        for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) b.kt[m][ks] = load_frag<In>(at + (2 * (wave * RT + m) + ks) * kIn, lane);
-    };
-    auto step = [&](Buf& b, int64_t c) {
-      const int64_t left = seq.len - c * kGdrChunk, ahead = clamp_chunk(c + 2);
-      const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-      floatx4 E = {};
+          for (int ks = 0; ks < 2; ++ks) b.kt[m][ks] = load_frag<In>(ktp + (2 * m + ks) * kIn, lane);
+        const int64_t more = mask_of(at < nc - 1);
+        at += more & 1;
+        kp += more & (int64_t)(kGdrChunk * p.sk.t);
+        tp += more & (int64_t)(p.Hv * (kTriFrags * kOp3));
+        ktp += more & (int64_t)(p.Hk * (DK / 8 * kIn));
+      };
+      auto step = [&](Buf& b, int64_t c, int n) {
+        const Gates& gt = gate[c & 1];
+        Op3 sb[KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) E = mma(b.k[ks], load_frag<Op3>(sf + ks * kOp3, lane), E);
-      load_k(b, ahead);
+        for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>(sf + ks * kOp3, lane);
+        const floatx4 v = vt[c & 1].tile(li, r0), gam = ld4f((const float*)gt.gam + r0);
+        floatx4 E = mma_steps(b.k, sb, floatx4{});
+        load_k(b);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) E[r] = r0 + r < n ? b.v[r] - b.gam[r] * E[r] : 0.f;
-      load_v(b, ahead);
-      put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, E, T{});
-      block_barrier();
+        for (int r = 0; r < 4; ++r) E[r] = r0 + r < n ? v[r] - gam[r] * E[r] : 0.f;
+        put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, E, T{});
+        block_barrier();
 
-      floatx4 F = mma(b.ti[0], load_frag<Op3>(ef, lane), floatx4{});
-      if (wave >= 2) F = mma(b.ti[1], load_frag<Op3>(ef + kOp3, lane), F);
-      const floatx4 U = b.beta * F, W = b.eta * U;
-      const float last = b.last;
-      load_ti(b, ahead);
-      put_op<3>(wf + (wave >> 1) * kOp3, wave & 1, li, g, W, T{});
-      block_barrier();
-
-      put_op<2>(uf + (wave >> 1) * kOp2, wave & 1, li, g, STATES ? F : U, T{});
-      if (owner) {
-        const Op3 w0 = load_frag<Op3>(wf, lane), w1 = load_frag<Op3>(wf + kOp3, lane);
+        Op3 eb[TS];
 #pragma unroll
-        for (int m = 0; m < RT; ++m) S[m] = mma(b.kt[m][1], w1, mma(b.kt[m][0], w0, S[m] * last));
+        for (int ks = 0; ks < TS; ++ks) eb[ks] = load_frag<Op3>(ef + ks * kOp3, lane);
+        const floatx4 eta = ld4f((const float*)gt.eta + r0), beta = ld4f((const float*)gt.beta + r0);
+        const floatx4 F = mma_steps(b.ti, eb, floatx4{});
+        load_ti(b);
+        const floatx4 U = beta * F;
+        put_op<3>(wf + (wave >> 1) * kOp3, wave & 1, li, g, eta * U, T{});
+        block_barrier();
+
+        const Op3 wb[2] = {load_frag<Op3>(wf, lane), load_frag<Op3>(wf + kOp3, lane)};
+        const float last = gt.gam[63];   // e^{G_last}: tokens behind the end do not decay
+        put_op<2>(uf + (wave >> 1) * kOp2, wave & 1, li, g, STATES ? F : U, T{});
+#pragma unroll
+        for (int m = 0; m < RT; ++m) S[m] = mma_steps(b.kt[m], wb, S[m] * last);
+        load_kt(b);
+        put_state();
+        block_barrier();
+      };
+      if (nc > 0) {
+        Buf buf[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          load_k(buf[i]);
+          load_ti(buf[i]);
+          load_kt(buf[i]);
+        }
+        int64_t c = 0;
+        for (; c + kAhead < nc; c += kAhead) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) step(buf[i], c + i, kGdrChunk);
+        }
+        if (kAhead > 1 && c + 1 < nc) {
+          step(buf[0], c, kGdrChunk);
+          step(buf[kAhead - 1], c + 1, last_rows);
+        } else {
+          step(buf[0], c, last_rows);
+        }
       }
-      load_kt(b, ahead);
-      put_state();
-      block_barrier();
     };
-    if (nc > 0) {
-      Buf b0, b1;
-      const int64_t second = clamp_chunk(1);
-      load_k(b0, 0);
-      load_v(b0, 0);
-      load_ti(b0, 0);
-      load_kt(b0, 0);
-      load_k(b1, second);
-      load_v(b1, second);
-      load_ti(b1, second);
-      load_kt(b1, second);
-      for (int64_t c = 0; c < nc; c += 2) {
-        step(b0, c);
-        if (c + 1 < nc) step(b1, c + 1);
-      }
-    }
+    static_assert(kAhead == 1 || kAhead == 2, "the loop's remainder");
+    if (wave < 2) walk(std::false_type{});
+    else walk(std::true_type{});
+    if constexpr (!STATES) block_barrier();   // the last chunk's outputs, between wavefronts 4-7
     if (p.S_final && owner) {
 #pragma unroll
       for (int m = 0; m < RT; ++m) {
-        float* at = p.S_final + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+        const auto at = global_out<float>(p.S_final) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
         for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
       }
@@ -186,83 +254,131 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
     return;
   }
 
-  block_barrier();   // the first state
+  // v and the gates of one chunk ahead of the chain: loaded, then left in LDS
+  const int tid = threadIdx.x & 255;
+  typename Frags<T>::In vx;
+  float gx = 0.f;
+  int64_t ahead = 0;
+  auto vp = global_in<T>(p.v) + seq.row * p.sv.b + h * p.sv.h + seq.t0 * p.sv.t + 16 * part;
+  auto gp = gates + (wave < 3 ? wave : 0) * 64;
+  static_assert(kGateGam == 0 && kGateEta == 64 && kGateBeta == 128, "a wavefront each");
+  const LaneRow vrow(tid >> 1, last_rows, p.sv.t, 8 * (tid & 1), sizeof(T));
+  auto fetch = [&]() {
+    if (wave < 2) vx = load_row8(lane_at(vp, vrow.of(ahead == nc - 1)));
+    if (wave < 3) gx = *lane_at(gp, lane * 4);
+    const int64_t more = mask_of(ahead < nc - 1);
+    ahead += more & 1;
+    vp += more & (int64_t)(kGdrChunk * p.sv.t);
+    gp += more & (int64_t)(p.Hv * kGateFloats);
+  };
+  auto leave = [&](int64_t c) {
+    if (wave < 2) vt[c & 1].put_row(tid, vx);
+    if (wave < 3) (wave == 0 ? gate[c & 1].gam : wave == 1 ? gate[c & 1].eta : gate[c & 1].beta)[lane] = gx;
+  };
+  if (nc > 0) {
+    fetch();
+    leave(0);
+    fetch();
+  }
+  block_barrier();   // the first state, v and gates
   if constexpr (STATES) {
-    const int tid = threadIdx.x & 255;
-    T* sp = (T*)p.ws_s + blk0 * p.dk * p.dv + 16 * part;
-    T* fp = (T*)p.ws_f + blk0 * kGdrChunk * p.dv + 16 * part;
+    auto sp = global_out<T>(p.ws_s) + blk0 * p.dk * p.dv + 16 * part;
+    auto fp = global_out<T>(p.ws_f) + blk0 * kGdrChunk * p.dv + 16 * part;
     for (int64_t c = 0; c < nc; ++c) {
       // the state that enters this chunk, F of the one before
-      write_rows<T>(sf, kOp3, DK, sp + c * p.Hv * p.dk * p.dv, p.dv, tid);
-      if (c > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp + (c - 1) * p.Hv * kGdrChunk * p.dv, p.dv, tid);
+      write_rows<T>(sf, kOp3, DK, sp, p.dv, tid);
+      sp += p.Hv * (p.dk * p.dv);
+      if (c > 0) {
+        write_rows<T>(uf, kOp2, kGdrChunk, fp, p.dv, tid);
+        fp += p.Hv * (kGdrChunk * p.dv);
+      }
       block_barrier();
+      leave(c + 1);
+      fetch();
       block_barrier();
       block_barrier();
     }
-    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp + (nc - 1) * p.Hv * kGdrChunk * p.dv, p.dv, tid);
+    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp, p.dv, tid);
   } else {
-    const T* qp = (const T*)p.q + seq.row * p.sq.b + kh * p.sq.h + 8 * g;
-    T* op = (T*)p.o + seq.row * p.so.b + h * p.so.h + (seq.t0 + r0) * p.so.t + col;
-    struct Buf {
-      In q[KS];
-      Op1 pm[2];
-      floatx4 gam;
-    };
-    auto load_q = [&](Buf& b, int64_t c) {
-      const T* at = qp + row_of(c) * p.sq.t;
+    auto walk = [&](auto both) {
+      constexpr int TS = decltype(both)::value ? 2 : 1;
+      struct Buf {
+        In q[KS], pm[TS];
+      };
+      int64_t at = 0;
+      auto qp = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + seq.t0 * p.sq.t;
+      auto pp = as_global((const char*)p.ws_p) + blk0 * kTriFrags * kOp1 + lower_frag(wave, 0) * kOp1;
+      auto op = global_out<T>(p.o) + seq.row * p.so.b + h * p.so.h + seq.t0 * p.so.t + 16 * part;
+      const LaneRow qrow(16 * wave + li, last_rows, p.sq.t, 8 * g, sizeof(T));
+      const uint32_t orow = (uint32_t)(((tid >> 1) * p.so.t + 8 * (tid & 1)) * sizeof(T));
+      auto load = [&](Buf& b) {
+        const auto from = lane_at(qp, qrow.of(at == nc - 1));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) b.q[ks] = load_row8(at + 32 * ks);
-      b.gam = ld4f(gates + c * p.Hv * kGateFloats + kGateGam + r0);
-    };
-    auto load_p = [&](Buf& b, int64_t c) {
-      const char* at = p.ws_p + (blk0 + c * p.Hv) * kTriFrags * kOp1;
-      b.pm[0] = load_frag<Op1>(at + lower_frag(wave, 0) * kOp1, lane);
-      if (wave >= 2) b.pm[1] = load_frag<Op1>(at + lower_frag(wave, 1) * kOp1, lane);
-    };
-    floatx4 O = {};
-    // the outputs of chunk c, whose U the chain has left
-    auto finish = [&](Buf& b, int64_t c) {
-      const int64_t left = seq.len - c * kGdrChunk;
-      const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-      const Op2 u0 = load_frag<Op2>(uf, lane);
-      if constexpr (sizeof(T) == 2) {
-        O = mma(b.pm[0].p[0], u0, O);
-        if (wave >= 2) O = mma(b.pm[1].p[0], load_frag<Op2>(uf + kOp2, lane), O);
-      } else {
-        O = mma(b.pm[0], u0, O);
-        if (wave >= 2) O = mma(b.pm[1], load_frag<Op2>(uf + kOp2, lane), O);
-      }
-      load_p(b, clamp_chunk(c + 2));
+        for (int ks = 0; ks < KS; ++ks) b.q[ks] = load_row8(from + 32 * ks);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r0 + r < n) store_f32(op, (c * kGdrChunk + r) * p.so.t, O[r]);
-    };
-    auto step = [&](Buf& b, Buf& before, int64_t c) {
-      if (c > 0) finish(before, c - 1);
-      O = floatx4{};
+        for (int ks = 0; ks < TS; ++ks) b.pm[ks] = load_frag<In>(pp + ks * kOp1, lane);
+        const int64_t more = mask_of(at < nc - 1);
+        at += more & 1;
+        qp += more & (int64_t)(kGdrChunk * p.sq.t);
+        pp += more & (int64_t)(p.Hv * (kTriFrags * kOp1));
+      };
+      floatx4 O = {};
+      // the outputs of the chunk before, whose U the chain has left; two planes of U and of the state, as o is
+      // rounded to the inputs' type
+      auto add_own = [&](Buf& b) {
+        Op2 ub[TS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        // two planes: o is rounded to the inputs' type
-        O = mma(b.q[ks], load_frag<Op2>(sf + ks * kOp3, lane), O);
-      }
-      O *= p.scale * b.gam;
-      load_q(b, clamp_chunk(c + 2));
-      block_barrier();
-      block_barrier();
-      block_barrier();
-    };
-    if (nc > 0) {
+        for (int ks = 0; ks < TS; ++ks) ub[ks] = load_frag<Op2>(uf + ks * kOp2, lane);
+        O = mma_steps(b.pm, ub, O);
+      };
+      auto store = [&](int n) {
+        if (tid < 2 * n) *repoint<In>(lane_at(op, orow)) = ot.row(tid);
+        op += kGdrChunk * p.so.t;
+      };
+      // outputs from the chunk's entering state; meanwhile the chunk before is finished
+      auto step = [&](Buf& b, Buf& before, int64_t c) {
+        if (c > 0) add_own(before);
+        Op2 sb[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op2>(sf + ks * kOp3, lane);
+        const floatx4 gam = ld4f((const float*)gate[c & 1].gam + r0);
+        const floatx4 read = mma_steps(b.q, sb, floatx4{});
+        block_barrier();
+        if (c > 0) {
+          load(before);
+          ot.put_tile(li, r0, O);
+        }
+        O = (p.scale * gam) * read;
+        leave(c + 1);
+        fetch();
+        block_barrier();
+        if (c > 0) store(kGdrChunk);
+        block_barrier();
+      };
       Buf b0, b1;
-      load_q(b0, 0);
-      load_p(b0, 0);
-      load_q(b1, clamp_chunk(1));
-      load_p(b1, clamp_chunk(1));
-      for (int64_t c = 0; c < nc; c += 2) {
-        step(b0, b1, c);
-        if (c + 1 < nc) step(b1, b0, c + 1);
+      if (nc > 0) {
+        load(b0);
+        load(b1);
+        int64_t c = 0;
+        for (; c + 1 < nc; c += 2) {
+          step(b0, b1, c);
+          step(b1, b0, c + 1);
+        }
+        if (c < nc) {
+          step(b0, b1, c);
+          add_own(b0);
+        } else {
+          add_own(b1);
+        }
+        ot.put_tile(li, r0, O);
       }
-      if (nc & 1) finish(b0, nc - 1);
-      else finish(b1, nc - 1);
+    };
+    if (wave < 2) walk(std::false_type{});
+    else walk(std::true_type{});
+    block_barrier();
+    if (nc > 0 && tid < 2 * last_rows) {
+      const auto op = global_out<T>(p.o) + seq.row * p.so.b + h * p.so.h + (seq.t0 + (nc - 1) * kGdrChunk) * p.so.t + 16 * part;
+      *repoint<In>(lane_at(op, (uint32_t)(((tid >> 1) * p.so.t + 8 * (tid & 1)) * sizeof(T)))) = ot.row(tid);
     }
   }
 }
@@ -287,6 +403,9 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
   __shared__ __attribute__((aligned(16))) char gf[2 * kOp3];               // scale gam dO
   __shared__ __attribute__((aligned(16))) float x0[2][4 * 256];            // P^T dO, result tiles [wave][lane][4]
   __shared__ __attribute__((aligned(16))) float d0[2][DK / 16 * 256];      // Q^T (scale gam dO)
+  __shared__ __attribute__((aligned(16))) Turned<T> ot;                    // dO on its way in
+  __shared__ __attribute__((aligned(16))) Turned<float> ut;                // dU on its way out
+  __shared__ __attribute__((aligned(16))) Gates gate[4];                   // by the chunk's number modulo 4
 
   int64_t unit;
   int part;
@@ -296,22 +415,21 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
   const GdrSeq seq = gdr_seq(p, s);
   const int64_t nc = seq.n_chunks;
   const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
-  const bool chain = threadIdx.x < 256;
-  const int wave = (threadIdx.x >> 6) & 3;
+  const int wave = wave_id() & 3;
   const int col = 16 * part + li;
   const int r0 = 16 * wave + 4 * g;
+  const int last_rows = (int)(seq.len - (nc - 1) * kGdrChunk);
   const bool owner = wave * RT < DK / 16;
   const int64_t blk0 = seq.slot0 * p.Hv + h;
-  const float* gates = (const float*)p.ws_gate + blk0 * kGateFloats;
-  auto clamp_chunk = [&](int64_t c) { return c < 0 ? 0 : c; };
+  const auto gates = global_in<float>(p.ws_gate) + blk0 * kGateFloats;
 
-  if (chain) {
+  if (wave_id() < 4) {
     floatx4 S[RT];
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
       S[m] = floatx4{};
       if (owner && p.dSf) {
-        const float* at = p.dSf + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+        const auto at = global_in<float>(p.dSf) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
       }
@@ -324,104 +442,105 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
       }
     };
     put_state();
-    const T* kp = (const T*)p.k + seq.row * p.sk.b + kh * p.sk.h + 8 * g;
-    T* dvp = (T*)p.dv_ + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + r0) * p.sdv.t + col;
-    struct Buf {
-      In k[KS];
-      Op3 tt[2];
-      In kt[RT][2];
-      float f[4];
-      floatx4 gam, eta, beta;
-      float last;
-    };
-    auto load_k = [&](Buf& b, int64_t c) {
-      const T* at = kp + (seq.t0 + min64(c * kGdrChunk + 16 * wave + li, seq.len - 1)) * p.sk.t;
+    auto walk = [&](auto both) {
+      constexpr int TS = decltype(both)::value ? 2 : 1;   // T^T of wavefronts 0 and 1 reaches into both steps
+      struct Buf {
+        In k[KS];
+        Op3 tt[TS];
+        In kt[RT][2];
+      };
+      // where the next loads come from: the last chunk, then downwards
+      int64_t at = nc - 1;
+      auto kp = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (seq.t0 + at * kGdrChunk) * p.sk.t;
+      auto tp = as_global((const char*)p.ws_tt) + (blk0 + at * p.Hv) * kTriFrags * kOp3 + upper_frag(wave, wave < 2 ? 0 : 1) * kOp3;
+      auto ktp = as_global((const char*)p.ws_kt) + ((seq.slot0 + at) * p.Hk + kh) * (int64_t)(DK / 8) * kIn + 2 * (owner ? wave * RT : 0) * kIn;
+      const LaneRow krow(16 * wave + li, last_rows, p.sk.t, 8 * g, sizeof(T));
+      auto load_k = [&](Buf& b) {
+        const auto from = lane_at(kp, krow.of(at == nc - 1));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(at + 32 * ks);
-      b.eta = ld4f(gates + c * p.Hv * kGateFloats + kGateEta + r0);
-    };
-    auto load_tt = [&](Buf& b, int64_t c) {
-      const char* at = p.ws_tt + (blk0 + c * p.Hv) * kTriFrags * kOp3;
-      if (wave < 2) b.tt[0] = load_frag<Op3>(at + upper_frag(wave, 0) * kOp3, lane);
-      b.tt[1] = load_frag<Op3>(at + upper_frag(wave, 1) * kOp3, lane);
-      const float* gt = gates + c * p.Hv * kGateFloats;
-      b.gam = ld4f(gt + kGateGam + r0);
-      b.beta = ld4f(gt + kGateBeta + r0);
-      b.last = gt[kGateLast];
-    };
-    auto load_kt = [&](Buf& b, int64_t c) {
-      const T* fp = (const T*)p.ws_f + (blk0 + c * p.Hv) * kGdrChunk * p.dv + (int64_t)r0 * p.dv + col;
+        for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(from + 32 * ks);
+      };
+      auto load_tt = [&](Buf& b) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) b.f[r] = load_f32(fp, (int64_t)r * p.dv);
-      if (!owner) return;
-      const char* at = p.ws_kt + ((seq.slot0 + c) * p.Hk + kh) * (int64_t)(DK / 8) * kIn;
+        for (int ks = 0; ks < TS; ++ks) b.tt[ks] = load_frag<Op3>(tp + ks * kOp3, lane);
+      };
+      auto load_kt = [&](Buf& b) {
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+        for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) b.kt[m][ks] = load_frag<In>(at + (2 * (wave * RT + m) + ks) * kIn, lane);
-    };
-    auto step = [&](Buf& b, int64_t c) {
-      const int64_t left = seq.len - c * kGdrChunk, ahead = clamp_chunk(c - 2);
-      const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-      floatx4 X = {};
+          for (int ks = 0; ks < 2; ++ks) b.kt[m][ks] = load_frag<In>(ktp + (2 * m + ks) * kIn, lane);
+        const int64_t more = mask_of(at > 0);
+        at -= more & 1;
+        kp -= more & (int64_t)(kGdrChunk * p.sk.t);
+        tp -= more & (int64_t)(p.Hv * (kTriFrags * kOp3));
+        ktp -= more & (int64_t)(p.Hk * (DK / 8 * kIn));
+      };
+      auto step = [&](Buf& b, int64_t c, int n) {
+        const Gates& gt = gate[c & 3];
+        Op3 sb[KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) X = mma(b.k[ks], load_frag<Op3>(sf + ks * kOp3, lane), X);
-      const floatx4 first = ld4f(&x0[c & 1][(wave * 64 + lane) * 4]);
+        for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>(sf + ks * kOp3, lane);
+        const floatx4 first = ld4f((const float*)&x0[c & 1][(wave * 64 + lane) * 4]), eta = ld4f((const float*)gt.eta + r0);
+        floatx4 X = mma_steps(b.k, sb, floatx4{});
+        load_k(b);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) X[r] = r0 + r < n ? b.eta[r] * X[r] + first[r] : 0.f;
-      load_k(b, ahead);
-      put_op<3>(xf + (wave >> 1) * kOp3, wave & 1, li, g, X, T{});
-      block_barrier();
+        for (int r = 0; r < 4; ++r) X[r] = r0 + r < n ? eta[r] * X[r] + first[r] : 0.f;
+        put_op<3>(xf + (wave >> 1) * kOp3, wave & 1, li, g, X, T{});
+        block_barrier();
 
-      floatx4 dU = mma(b.tt[1], load_frag<Op3>(xf + kOp3, lane), floatx4{});
-      if (wave < 2) dU = mma(b.tt[0], load_frag<Op3>(xf, lane), dU);
-      const floatx4 dE = b.beta * dU, G = -(b.gam * dE);
-      const float last = b.last;
-      load_tt(b, ahead);
-      put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, G, T{});
-      block_barrier();
-
-      if (owner) {
-        const Op3 e0 = load_frag<Op3>(ef, lane), e1 = load_frag<Op3>(ef + kOp3, lane);
+        Op3 xb[TS];
 #pragma unroll
-        for (int m = 0; m < RT; ++m) {
-          const floatx4 add = ld4f(&d0[c & 1][((wave * RT + m) * 64 + lane) * 4]);
-          S[m] = mma(b.kt[m][1], e1, mma(b.kt[m][0], e0, S[m] * last + add));
+        for (int ks = 0; ks < TS; ++ks) xb[ks] = load_frag<Op3>(xf + (ks + 2 - TS) * kOp3, lane);
+        const floatx4 gam = ld4f((const float*)gt.gam + r0), beta = ld4f((const float*)gt.beta + r0);
+        const floatx4 dU = mma_steps(b.tt, xb, floatx4{});
+        load_tt(b);
+        put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, -(gam * beta) * dU, T{});
+        ut.put_tile(li, r0, dU);
+        block_barrier();
+
+        const Op3 eb[2] = {load_frag<Op3>(ef, lane), load_frag<Op3>(ef + kOp3, lane)};
+        const float last = gt.gam[63];
+        if (owner) {
+#pragma unroll
+          for (int m = 0; m < RT; ++m) {
+            const floatx4 add = ld4f((const float*)&d0[c & 1][((wave * RT + m) * 64 + lane) * 4]);
+            S[m] = mma_steps(b.kt[m], eb, S[m] * last + add);
+          }
+        }
+        load_kt(b);
+        put_state();
+        block_barrier();
+      };
+      if (nc > 0) {
+        Buf buf[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          load_k(buf[i]);
+          load_tt(buf[i]);
+          load_kt(buf[i]);
+        }
+        int64_t c = nc - 1;
+        step(buf[0], c--, last_rows);
+        if (kAhead == 1) {
+          for (; c >= 0; --c) step(buf[0], c, kGdrChunk);
+        } else {
+          for (; c > 0; c -= 2) {
+            step(buf[kAhead - 1], c, kGdrChunk);
+            step(buf[0], c - 1, kGdrChunk);
+          }
+          if (c == 0) step(buf[kAhead - 1], c, kGdrChunk);
         }
       }
-      float* db = (float*)p.ws_db + ((blk0 + c * p.Hv) * (p.dv / 16) + part) * kGdrChunk + r0;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (r0 + r < n) store_f32(dvp, (c * kGdrChunk + r) * p.sdv.t, dE[r]);
-        float x = dU[r] * b.f[r];
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) x += __shfl_xor(x, d);
-        if (li == 0) db[r] = x;
-      }
-      load_kt(b, ahead);
-      put_state();
-      block_barrier();
     };
     block_barrier();
     block_barrier();
-    if (nc > 0) {
-      Buf b0, b1;
-      const int64_t second = clamp_chunk(nc - 2);
-      load_k(b0, nc - 1);
-      load_tt(b0, nc - 1);
-      load_kt(b0, nc - 1);
-      load_k(b1, second);
-      load_tt(b1, second);
-      load_kt(b1, second);
-      for (int64_t c = nc - 1; c >= 0; c -= 2) {
-        step(b0, c);
-        if (c > 0) step(b1, c - 1);
-      }
-    }
+    block_barrier();
+    if (wave < 2) walk(std::true_type{});
+    else walk(std::false_type{});
     if (p.dS0 && owner) {
 #pragma unroll
       for (int m = 0; m < RT; ++m) {
-        float* at = p.dS0 + unit * p.dk * p.dv + (int64_t)(16 * (wave * RT + m) + 4 * g) * p.dv + col;
+        const auto at = global_out<float>(p.dS0) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
         for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
       }
@@ -429,70 +548,131 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
     return;
   }
 
-  const int tid = threadIdx.x & 255;
-  const T* dop = (const T*)p.dO + seq.row * p.sdo.b + h * p.sdo.h + col;
-  T* sp = (T*)p.ws_ds + blk0 * p.dk * p.dv + 16 * part;
-  struct Buf {
-    float o[4];
-    floatx4 gam;
-    Op3 pm[2];
+  // wavefronts 4-7: dO and the gates are fetched two chunks ahead of the chain and turned in LDS, what they make
+  // is ready one chunk ahead
+  auto serve = [&](auto both) {
+    constexpr int TS = decltype(both)::value ? 2 : 1;
+    const int tid = threadIdx.x & 255;
+    In ox, fx;
+    float gx = 0.f;
+    Op3 pm[TS];
     In qt[RT][2];
-  };
-  auto load_o = [&](Buf& b, int64_t c) {
+    int64_t at = nc - 1, pat = nc - 1;   // the chunk that is fetched next, and whose P and Q are loaded next
+    auto dop = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + (seq.t0 + at * kGdrChunk) * p.sdo.t + 16 * part;
+    auto gp = gates + at * p.Hv * kGateFloats + (wave < 3 ? wave : 0) * 64;
+    auto pp = as_global((const char*)p.ws_p) + ((blk0 + at * p.Hv) * kTriFrags + upper_frag(wave, TS == 2 ? 0 : 1)) * kOp3;
+    auto qp = as_global((const char*)p.ws_qt) + (((seq.slot0 + at) * p.Hk + kh) * (int64_t)(DK / 8) + 2 * (owner ? wave * RT : 0)) * kIn;
+    // of the chunk the chain is at
+    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kGdrChunk * p.dv + 16 * part;
+    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * p.dk * p.dv + 16 * part;
+    auto dvp = global_out<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + at * kGdrChunk) * p.sdv.t + 16 * part;
+    auto dbp = global_out<float>(p.ws_db) + ((blk0 + at * p.Hv) * (p.dv / 16) + part) * kGdrChunk;
+    const LaneRow orow(tid >> 1, last_rows, p.sdo.t, 8 * (tid & 1), sizeof(T));
+    const uint32_t frow = (uint32_t)(((tid >> 1) * p.dv + 8 * (tid & 1)) * sizeof(T));
+    const uint32_t vrow = (uint32_t)(((tid >> 1) * p.sdv.t + 8 * (tid & 1)) * sizeof(T));
+    auto fetch = [&]() {
+      if (wave < 2) ox = load_row8(lane_at(dop, orow.of(at == nc - 1)));
+      if (wave < 3) gx = *lane_at(gp, lane * 4);
+      const int64_t more = mask_of(at > 0);
+      at -= more & 1;
+      dop -= more & (int64_t)(kGdrChunk * p.sdo.t);
+      gp -= more & (int64_t)(p.Hv * kGateFloats);
+    };
+    auto leave = [&](int64_t c) {
+      if (wave < 2) ot.put_row(tid, ox);
+      if (wave < 3) (wave == 0 ? gate[c & 3].gam : wave == 1 ? gate[c & 3].eta : gate[c & 3].beta)[lane] = gx;
+    };
+    auto load_pq = [&]() {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) b.o[r] = load_f32(dop, (seq.t0 + min64(c * kGdrChunk + r0 + r, seq.len - 1)) * p.sdo.t);
-    b.gam = ld4f(gates + c * p.Hv * kGateFloats + kGateGam + r0);
-  };
-  auto load_pq = [&](Buf& b, int64_t c) {
-    const char* at = p.ws_p + (blk0 + c * p.Hv) * kTriFrags * kOp3;
-    if (wave < 2) b.pm[0] = load_frag<Op3>(at + upper_frag(wave, 0) * kOp3, lane);
-    b.pm[1] = load_frag<Op3>(at + upper_frag(wave, 1) * kOp3, lane);
-    if (!owner) return;
-    const char* qt = p.ws_qt + ((seq.slot0 + c) * p.Hk + kh) * (int64_t)(DK / 8) * kIn;
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) b.qt[m][ks] = load_frag<In>(qt + (2 * (wave * RT + m) + ks) * kIn, lane);
-  };
-  auto spread = [&](Buf& b, int64_t c) {       // dO of chunk c as operands
-    const int64_t left = seq.len - c * kGdrChunk;
-    floatx4 o;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] = r0 + r < left ? b.o[r] : 0.f;
-    put_op<1>(of + (wave >> 1) * kIn, wave & 1, li, g, o, T{});
-    put_op<3>(gf + (wave >> 1) * kOp3, wave & 1, li, g, p.scale * (b.gam * o), T{});
-    load_o(b, clamp_chunk(c - 1));
-  };
-  auto products = [&](Buf& b, int64_t c) {
-    floatx4 X = mma(b.pm[1], load_frag<In>(of + kIn, lane), floatx4{});
-    if (wave < 2) X = mma(b.pm[0], load_frag<In>(of, lane), X);
-    *reinterpret_cast<floatx4*>(&x0[c & 1][(wave * 64 + lane) * 4]) = X;
-    if (owner) {
-      const Op3 g0 = load_frag<Op3>(gf, lane), g1 = load_frag<Op3>(gf + kOp3, lane);
+      for (int ks = 0; ks < TS; ++ks) pm[ks] = load_frag<Op3>(pp + ks * kOp3, lane);
 #pragma unroll
       for (int m = 0; m < RT; ++m)
-        *reinterpret_cast<floatx4*>(&d0[c & 1][((wave * RT + m) * 64 + lane) * 4]) = mma(b.qt[m][1], g1, mma(b.qt[m][0], g0, floatx4{}));
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) qt[m][ks] = load_frag<In>(qp + (2 * m + ks) * kIn, lane);
+      const int64_t more = mask_of(pat > 0);
+      pat -= more & 1;
+      pp -= more & (int64_t)(p.Hv * (kTriFrags * kOp3));
+      qp -= more & (int64_t)(p.Hk * (DK / 8 * kIn));
+    };
+    auto load_f = [&](int64_t c) {
+      if (wave < 2) fx = load_row8(lane_at(fp, frow));
+      if (c > 0) fp -= p.Hv * (kGdrChunk * p.dv);
+    };
+    auto spread = [&](int64_t c) {       // dO of chunk c as operands
+      const int n = c == nc - 1 ? last_rows : kGdrChunk;
+      floatx4 x = ot.tile(li, r0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = r0 + r < n ? x[r] : 0.f;
+      put_op<1>(of + (wave >> 1) * kIn, wave & 1, li, g, x, T{});
+      put_op<3>(gf + (wave >> 1) * kOp3, wave & 1, li, g, p.scale * (ld4f((const float*)gate[c & 3].gam + r0) * x), T{});
+    };
+    auto products = [&](int64_t c) {
+      const In o1 = load_frag<In>(of + kIn, lane);
+      floatx4 X = mma(pm[TS - 1], o1, floatx4{});
+      if constexpr (TS == 2) X = mma(pm[0], load_frag<In>(of, lane), X);
+      *reinterpret_cast<floatx4*>(&x0[c & 1][(wave * 64 + lane) * 4]) = X;
+      if (owner) {
+        const Op3 gb[2] = {load_frag<Op3>(gf, lane), load_frag<Op3>(gf + kOp3, lane)};
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+          *reinterpret_cast<floatx4*>(&d0[c & 1][((wave * RT + m) * 64 + lane) * 4]) = mma_steps(qt[m], gb, floatx4{});
+      }
+      load_pq();
+    };
+    // dU as the chain has left it: the gradient of v, and beta's over these 16 columns
+    auto finish = [&](int64_t c) {
+      const int n = c == nc - 1 ? last_rows : kGdrChunk, row = tid >> 1;
+      if (wave < 2) {
+        const float b = gate[c & 3].beta[row];
+        const float8v dU = ut.row(tid);
+        T f8[8];
+        __builtin_memcpy(f8, &fx, sizeof(fx));
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x += dU[e] * value(f8[e]);
+        x += __shfl_xor(x, 1);
+        if ((tid & 1) == 0) *lane_at(dbp, row * 4) = x;
+        if (row < n) {
+          store_row4(lane_at(dvp, vrow), b * floatx4{dU[0], dU[1], dU[2], dU[3]});
+          store_row4(lane_at(dvp, vrow + 4 * sizeof(T)), b * floatx4{dU[4], dU[5], dU[6], dU[7]});
+        }
+      }
+      dvp -= kGdrChunk * p.sdv.t;
+      dbp -= p.Hv * (p.dv / 16 * kGdrChunk);
+    };
+    if (nc > 0) {
+      fetch();
+      load_pq();
+      load_f(nc - 1);
+      leave(nc - 1);
+      fetch();
     }
-    load_pq(b, clamp_chunk(c - 1));
+    block_barrier();
+    if (nc > 0) spread(nc - 1);
+    block_barrier();
+    if (nc > 0) {
+      products(nc - 1);
+      leave(nc - 2);
+      fetch();
+    }
+    block_barrier();
+    for (int64_t c = nc - 1; c >= 0; --c) {
+      // dS at this chunk's end; what the chain needs of the next one
+      write_rows<T>(sf, kOp3, DK, sp, p.dv, tid);
+      sp -= p.Hv * (p.dk * p.dv);
+      if (c > 0) spread(c - 1);
+      block_barrier();
+      if (c > 0) products(c - 1);
+      block_barrier();
+      finish(c);
+      load_f(c - 1);
+      leave(c - 2);
+      fetch();
+      block_barrier();
+    }
   };
-  Buf b;
-  if (nc > 0) {
-    load_o(b, nc - 1);
-    load_pq(b, nc - 1);
-    spread(b, nc - 1);
-  }
-  block_barrier();
-  if (nc > 0) products(b, nc - 1);
-  block_barrier();
-  for (int64_t c = nc - 1; c >= 0; --c) {
-    // dS at this chunk's end; what the next one needs
-    write_rows<T>(sf, kOp3, DK, sp + c * p.Hv * p.dk * p.dv, p.dv, tid);
-    if (c > 0) spread(b, c - 1);
-    block_barrier();
-    if (c > 0) products(b, c - 1);
-    block_barrier();
-    block_barrier();
-  }
+  if (wave < 2) serve(std::true_type{});
+  else serve(std::false_type{});
 }
 
 template <typename T, int DK>

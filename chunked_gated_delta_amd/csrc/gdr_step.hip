@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStepParams p) {
   static_assert(RPT >= 1 && RW >= 1, "tile");
   __shared__ __attribute__((aligned(16))) float part[2][4][2 * CB + 4];
   __shared__ int same[2];
-  const int tid = threadIdx.x, ct = tid % CT, rg = tid / CT, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, ct = tid % CT, rg = tid / CT, wave = wave_id(), lane = tid & 63;
   const int nblk = p.dv / CB;
   const int64_t unit = blockIdx.x / nblk;
   const int64_t b0 = unit / p.Hv;
@@ -33,10 +33,10 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStepParams p) {
   const int64_t slot = p.slots ? p.slots[b0] : b0;
   if (slot < 0 || slot >= p.n_slots) {   // a padding row: zeros
     for (int64_t t = 0; t < p.T; ++t)
-      if (rg == 0) store_row4((T*)p.o + b0 * p.so.b + h * p.so.h + t * p.so.t + col, floatx4{});
+      if (rg == 0) store_row4(global_out<T>(p.o) + b0 * p.so.b + h * p.so.h + t * p.so.t + col, floatx4{});
     return;
   }
-  float* Sp = p.S + (slot * p.Hv + h) * DK * (int64_t)p.dv + (int64_t)rg * RPT * p.dv + col;
+  const auto Sp = as_global(p.S) + (slot * p.Hv + h) * DK * (int64_t)p.dv + (int64_t)rg * RPT * p.dv + col;
   floatx4 S[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) S[i] = ld4f(Sp + (int64_t)i * p.dv);
@@ -56,16 +56,16 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStepParams p) {
   for (int64_t b = b0; b < p.B; ++b) {
     if (b != b0 && p.slots[b] != (int32_t)slot) continue;
     for (int64_t t = 0; t < p.T; ++t) {
-      const T* kp = (const T*)p.k + b * p.sk.b + kh * p.sk.h + t * p.sk.t + rg * RPT;
-      const T* qp = (const T*)p.q + b * p.sq.b + kh * p.sq.h + t * p.sq.t + rg * RPT;
-      const floatx4 v = load_row4((const T*)p.v + b * p.sv.b + h * p.sv.h + t * p.sv.t + col);
-      const float decay = expf(gdr_gate(load_f32((const T*)p.w, b * p.sw.b + h * p.sw.h + t * p.sw.t), p.gate, p.g_min));
-      const float beta = load_f32((const T*)p.beta, b * p.sb.b + h * p.sb.h + t * p.sb.t);
+      const auto kp = global_in<T>(p.k) + b * p.sk.b + kh * p.sk.h + t * p.sk.t + rg * RPT;
+      const auto qp = global_in<T>(p.q) + b * p.sq.b + kh * p.sq.h + t * p.sq.t + rg * RPT;
+      const floatx4 v = load_row4(global_in<T>(p.v) + b * p.sv.b + h * p.sv.h + t * p.sv.t + col);
+      const float decay = expf(gdr_gate(get(global_in<T>(p.w) + b * p.sw.b + h * p.sw.h + t * p.sw.t), p.gate, p.g_min));
+      const float beta = get(global_in<T>(p.beta) + b * p.sb.b + h * p.sb.h + t * p.sb.t);
       float kk[RPT], qq[RPT];
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
-        kk[i] = load_f32(kp, i);
-        qq[i] = load_f32(qp, i);
+        kk[i] = get(kp + i);
+        qq[i] = get(qp + i);
       }
       floatx4 a = {}, o = {};
       float d = 0.f;
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStepParams p) {
         sd += part[phase][w][2 * CB];
       }
       const floatx4 u = beta * (v - decay * sa);
-      if (rg == 0) store_row4((T*)p.o + b * p.so.b + h * p.so.h + t * p.so.t + col, p.scale * (decay * so + sd * u));
+      if (rg == 0) store_row4(global_out<T>(p.o) + b * p.so.b + h * p.so.h + t * p.so.t + col, p.scale * (decay * so + sd * u));
 #pragma unroll
       for (int i = 0; i < RPT; ++i) S[i] = decay * S[i] + kk[i] * u;
       phase ^= 1;   // the other buffer: this one may still be read
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStepParams p) {
     if (!later) break;
   }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) *reinterpret_cast<floatx4*>(Sp + (int64_t)i * p.dv) = S[i];
+  for (int i = 0; i < RPT; ++i) *repoint<floatx4>(Sp + (int64_t)i * p.dv) = S[i];
 }
 
 template <typename T, int DK>

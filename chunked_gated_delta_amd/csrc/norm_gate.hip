@@ -44,7 +44,7 @@ struct RowMap {
 };
 
 template <typename T, int NT, int VPT, bool VEC>
-__device__ __forceinline__ void load_part(const T* row, RowMap<NT, VEC> m, float (&x)[VPT * 8]) {
+__device__ __forceinline__ void load_part(GlobalPtr<const T> row, RowMap<NT, VEC> m, float (&x)[VPT * 8]) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if constexpr (VEC) {
@@ -58,13 +58,13 @@ __device__ __forceinline__ void load_part(const T* row, RowMap<NT, VEC> m, float
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[v * 8 + j] = m.has(v, j) ? load_f32(row, m.at(v, j)) : 0.f;
+      for (int j = 0; j < 8; ++j) x[v * 8 + j] = m.has(v, j) ? get(row + m.at(v, j)) : 0.f;
     }
   }
 }
 
 template <typename T, int NT, int VPT, bool VEC>
-__device__ __forceinline__ void store_part(T* row, RowMap<NT, VEC> m, const float (&x)[VPT * 8]) {
+__device__ __forceinline__ void store_part(GlobalPtr<T> row, RowMap<NT, VEC> m, const float (&x)[VPT * 8]) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if constexpr (VEC) {
@@ -75,22 +75,22 @@ __device__ __forceinline__ void store_part(T* row, RowMap<NT, VEC> m, const floa
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (m.has(v, j)) store_f32(row, m.at(v, j), x[v * 8 + j]);
+        if (m.has(v, j)) put(row + m.at(v, j), x[v * 8 + j]);
     }
   }
 }
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
-template <typename T> __device__ __forceinline__ const T* row_of(const void* p, kda_stride_t s, int64_t b, int64_t h, int64_t t) {
-  return (const T*)p + b * s.b + h * s.h + t * s.t;
+template <typename T> __device__ __forceinline__ GlobalPtr<T> row_of(const void* p, kda_stride_t s, int64_t b, int64_t h, int64_t t) {
+  return (GlobalPtr<T>)p + b * s.b + h * s.h + t * s.t;
 }
 
 // the weight of this thread's values, in either type
 template <typename T, int NT, int VPT, bool VEC>
 __device__ __forceinline__ void load_weight(const void* w, int wdtype, RowMap<NT, VEC> m, float (&x)[VPT * 8]) {
-  if (wdtype == KDA_DTYPE_BF16) load_part<uint16_t, NT, VPT, VEC>((const uint16_t*)w, m, x);
-  else load_part<float, NT, VPT, VEC>((const float*)w, m, x);
+  if (wdtype == KDA_DTYPE_BF16) load_part<uint16_t, NT, VPT, VEC>(global_in<uint16_t>(w), m, x);
+  else load_part<float, NT, VPT, VEC>(global_in<float>(w), m, x);
 }
 
 template <typename T, int NT, int VPT, bool VEC, int THREADS>
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormParams p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= p.alpha;
   }
-  store_part<T, NT, VPT, VEC>((T*)row_of<T>(p.s, p.ss, b, h, t), m, x);
+  store_part<T, NT, VPT, VEC>(row_of<T>(p.s, p.ss, b, h, t), m, x);
   if (p.weight2) {
     load_weight<T, NT, VPT, VEC>(p.weight2, p.wdtype, m, w);
     float q = 0.f;
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormParams p) {
     const float r = rsqrtf(row_sum<NT>(q, lds, group) / (float)p.D + p.eps);
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= r * w[e];
-    store_part<T, NT, VPT, VEC>((T*)row_of<T>(p.y, p.sy, b, h, t), m, x);
+    store_part<T, NT, VPT, VEC>(row_of<T>(p.y, p.sy, b, h, t), m, x);
   }
 }
 
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] += r2 * (dy[e] - s[e] * c);
     }
-    if (p.dres && live) store_part<T, NT, VPT, VEC>((T*)row_of<T>(p.dres, p.sdr, b, h, t), m, g);
+    if (p.dres && live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dres, p.sdr, b, h, t), m, g);
 #pragma unroll
     for (int e = 0; e < E; ++e) g[e] *= p.alpha;
     if (p.z) {
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
         a[e] = g[e] * n[e] * der;
         g[e] *= val;
       }
-      if (p.dz && live) store_part<T, NT, VPT, VEC>((T*)row_of<T>(p.dz, p.sdz, b, h, t), m, a);
+      if (p.dz && live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dz, p.sdz, b, h, t), m, a);
     }
     if (p.weight) {
       float c = 0.f;
@@ -235,13 +235,13 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] = r * (g[e] - x[e] * c);
     }
-    if (live) store_part<T, NT, VPT, VEC>((T*)row_of<T>(p.dx, p.sdx, b, h, t), m, g);
+    if (live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dx, p.sdx, b, h, t), m, g);
   }
 
   // this workgroup's sums: the row groups' one after another
   for (int which = 0; which < 2; ++which) {
     if (which == 0 ? !p.dweight : !p.dweight2) continue;
-    float* out = p.partial + ((int64_t)which * kMaxBwdBlocks + blockIdx.x) * p.D;
+    const auto out = as_global(p.partial) + ((int64_t)which * kMaxBwdBlocks + blockIdx.x) * p.D;
     float (&d)[E] = which == 0 ? dw : dw2;
     if constexpr (GROUPS > 1) {
       __syncthreads();
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(NormParams p, int blo
   const int which = blockIdx.y;
   void* out = which == 0 ? p.dweight : p.dweight2;
   if (!out) return;
-  const float* in = p.partial + (int64_t)which * kMaxBwdBlocks * p.D;
+  const auto in = global_in<float>(p.partial) + (int64_t)which * kMaxBwdBlocks * p.D;
   float s = 0.f;
   if (col < p.D)
     for (int i = y; i < blocks; i += 64) s += in[(int64_t)i * p.D + col];
@@ -284,8 +284,8 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(NormParams p, int blo
   if (y == 0 && col < p.D) {
     s = 0.f;
     for (int i = 0; i < 64; ++i) s += part[i][c];
-    if (p.wdtype == KDA_DTYPE_BF16) store_f32((uint16_t*)out, col, s);
-    else store_f32((float*)out, col, s);
+    if (p.wdtype == KDA_DTYPE_BF16) put(global_out<uint16_t>(out) + col, s);
+    else put(global_out<float>(out) + col, s);
   }
 }
 

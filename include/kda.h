@@ -268,7 +268,7 @@ KDA_API size_t kda_workspace_bytes_ex(const kda_shape_t* shape, int chunk, const
  *
  * Tensors (all of dtype, element strides given, the last dimension contiguous):
  *   q, k [B,Hk,T,dk];  v, o [B,Hv,T,dv];  w, beta [B,Hv,T];  states [n,Hv,dk,dv], dense, fp32.
- * Rows of q, k, v, o (and of their gradients) lie on 16-byte places.  Input strides may be 0 (a
+ * Rows of q, k, v, o (and of their gradients) lie on 16-byte places, tokens at most 32 MiB apart.  Input strides may be 0 (a
  * broadcast dimension); gradients are those of every element as if it were its own.  An output may
  * not hold one place twice, nor reach into the span of an input or another output.
  * Packed sequences: B = 1, seq_start (device, int32) holds n_seq + 1 offsets into T, not decreasing;
