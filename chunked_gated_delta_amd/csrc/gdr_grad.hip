@@ -2,8 +2,10 @@
 // adjoint dS at the chunk's end and dE (the gradient of v): one workgroup per (chunk, key head), the
 // value heads that share the key head one after another.
 //
-// Wavefront i owns the 16 tokens of tile i and forms the transposed gradients (channels x tokens), so a
-// lane holds one token and 4 consecutive channels.  With dO' = scale dO and D_rj = e^{G_r - G_j}:
+// A wavefront owns 16 tokens and (bf16) half of the channels and forms the transposed gradients (channels x
+// tokens), so a lane holds one token and 4 consecutive channels.  bf16: the workgroup asks for all its operands
+// at once (144 KiB at dk = dv = 128: one workgroup's whole traffic in flight) and shares them in LDS; K^T and
+// Q^T are transposing LDS reads.  With dO' = scale dO and D_rj = e^{G_r - G_j}:
 //   dP = lower(dO' U^T . D)   dA = -strict_lower(dE U^T . D)
 //   dq_r  =  gam_r S dO'_r + sum_j dP_rj k_j
 //   dk_r  = -gam_r S dE_r  + sum_j dA_rj k_j                                    (as a row: reads)
@@ -19,13 +21,285 @@ namespace kda {
 
 namespace {
 
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
-  using In = typename Frags<T>::In;
-  using Op = typename Frags<T>::template Op<2>;
+template <int DK, int DV>
+__global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
+  using T = uint16_t;
+  constexpr int KV = DV / 32, MT = DK / 16, MH = MT / 2;   // MH: channel tiles of a wavefront
+  constexpr int kOp = op_frag<T, 2>(), kLd = DV + 8;
+  constexpr int kRow8 = DV / 8;                            // 16-byte pieces of a row
+  constexpr int kTok = 64 * kRow8 / 512 ? 64 * kRow8 / 512 : 1;   // pieces a thread moves of 64 rows,
+  constexpr int kSt = DK * kRow8 / 512 ? DK * kRow8 / 512 : 1;    // and of DK rows
+  constexpr int kTri = 4 * 8 * kOp, kXBytes = 3 * 64 * kLd * 2 > kTri ? 3 * 64 * kLd * 2 : kTri;
+  // F, dO and dE; then the triangular factors: per token tile 2 steps of dP and dA over j, 2 of each over r
+  __shared__ __attribute__((aligned(16))) char xs[kXBytes];
+  __shared__ __attribute__((aligned(16))) T sl[DK * kLd];  // S, then dS
+  __shared__ __attribute__((aligned(16))) Rows<T, DK> kl, ql;
+  __shared__ float ghi[64], glo[64], bet[64];
+  __shared__ double dG[2][64], extra[8];
+  T* fl = reinterpret_cast<T*>(xs);
+  T* ol = fl + 64 * kLd;
+  T* el = ol + 64 * kLd;
+
+  GdrSeq seq;
+  int64_t chunk;
+  const int64_t slot = blockIdx.x;
+  if (!gdr_find(p, slot, &seq, &chunk)) return;
+  const int kh = blockIdx.y, grp = p.Hv / p.Hk;
+  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  const int tile = wave_id() & 3, half = wave_id() >> 2;   // token tile; half of the channels
+  const int64_t t0 = seq.t0 + chunk * kGdrChunk, left = seq.len - chunk * kGdrChunk;
+  const int n = left < kGdrChunk ? (int)left : kGdrChunk;
+  const int tok = 16 * tile + li;                          // this lane's token
+  const bool live = tok < n;
+  char* mine = xs + tile * 8 * kOp;
+
+  // K and Q, zeros behind the sequence's end
+  for (int i = tid; i < 64 * DK / 8; i += 512) {
+    const int r = i / (DK / 8), c0 = i % (DK / 8) * 8;
+    bf16x8 a = {}, b = {};
+    if (r < n) {
+      a = load_row8(global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + r) * p.sk.t + c0);
+      b = load_row8(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + r) * p.sq.t + c0);
+    }
+    kl.put8(r, c0, a);
+    ql.put8(r, c0, b);
+  }
+
+  floatx4 dq[MH], dk[MH];
+#pragma unroll
+  for (int m = 0; m < MH; ++m) dq[m] = dk[m] = floatx4{};
+
+  for (int hg = 0; hg < grp; ++hg) {
+    const int h = kh * grp + hg;
+    const int64_t blk = slot * p.Hv + h;
+    const auto gate = global_in<float>(p.ws_gate) + blk * kGateFloats;
+    const auto F = global_in<T>(p.ws_f) + blk * kGdrChunk * DV;
+    const auto St = global_in<T>(p.ws_s) + blk * DK * DV;
+    const auto dSt = global_in<T>(p.ws_ds) + blk * DK * DV;
+    const auto dO = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t;
+    const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t;
+    // everything is asked for at once
+    bf16x8 fx[kTok], ox[kTok], ex[kTok], sx[kSt], dx[kSt];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int at = tid + 512 * i, r = at / kRow8, c0 = at % kRow8 * 8;
+      fx[i] = ox[i] = ex[i] = bf16x8{};
+      if (at < 64 * kRow8) fx[i] = load_row8(F + at * 8);
+      if (r < n && at < 64 * kRow8) {
+        ox[i] = load_row8(dO + r * p.sdo.t + c0);
+        ex[i] = load_row8(dE + r * p.sdv.t + c0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSt; ++i) {
+      const int at = tid + 512 * i;
+      sx[i] = dx[i] = bf16x8{};
+      if (at < DK * kRow8) {
+        sx[i] = load_row8(St + at * 8);
+        dx[i] = load_row8(dSt + at * 8);
+      }
+    }
+    if (tid < 64) {
+      ghi[tid] = gate[kGateHi + tid];
+      glo[tid] = gate[kGateLo + tid];
+      bet[tid] = gate[kGateBeta + tid];
+    }
+    const float gam = gate[kGateGam + tok], eta = gate[kGateEta + tok], last = gate[kGateLast];
+    auto at_row = [&](T* base, int at) { return reinterpret_cast<bf16x8*>(base + at / kRow8 * kLd + at % kRow8 * 8); };
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int at = tid + 512 * i;
+      if (at < 64 * kRow8) {
+        *at_row(fl, at) = fx[i];
+        *at_row(ol, at) = ox[i];
+        *at_row(el, at) = ex[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSt; ++i)
+      if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = sx[i];
+    __syncthreads();
+
+    auto rows = [&](const T* base, int t, int kv) { return load_row8(base + (16 * t + li) * kLd + 32 * kv + 8 * g); };
+    bf16x8 fo[KV], oo[KV], eo[KV];   // this wavefront's own tokens
+#pragma unroll
+    for (int kv = 0; kv < KV; ++kv) {
+      fo[kv] = rows(fl, tile, kv);
+      oo[kv] = rows(ol, tile, kv);
+      eo[kv] = rows(el, tile, kv);
+    }
+    // dP and dA: half 0 over all j <= its tokens r (transposed), half 1 over all r >= its tokens j; tiles that
+    // hold none of it stay zeros
+    const float ghr = ghi[tok], glr = glo[tok], br = bet[tok];
+    floatx4 a4[4], b4[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      a4[m] = b4[m] = floatx4{};
+      const bool rowwise = half == 0;
+      if (rowwise ? m <= tile : m >= tile) {
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv) {
+          if (rowwise) {
+            const bf16x8 f = rows(fl, m, kv);
+            a4[m] = mma(f, oo[kv], a4[m]);
+            b4[m] = mma(f, eo[kv], b4[m]);
+          } else {
+            a4[m] = mma(rows(ol, m, kv), fo[kv], a4[m]);
+            b4[m] = mma(rows(el, m, kv), fo[kv], b4[m]);
+          }
+        }
+      }
+    }
+    __syncthreads();   // everyone has read F, dO and dE
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int o = 16 * m + 4 * g + r;                   // j of the row tok, or r of the column tok
+        const float d = half == 0 ? (ghr - ghi[o]) + (glr - glo[o]) : (ghi[o] - ghr) + (glo[o] - glr);
+        const bool in = half == 0 ? tok >= o : o >= tok;
+        const float w = in ? (half == 0 ? bet[o] : br) * expf(in ? d : 0.f) : 0.f;
+        a4[m][r] = in ? p.scale * w * a4[m][r] : 0.f;
+        b4[m][r] = in && tok != o ? -w * b4[m][r] : 0.f;
+      }
+      put_op<2>(mine + (4 * half + (m >> 1)) * kOp, m & 1, li, g, a4[m], T{});
+      put_op<2>(mine + (4 * half + 2 + (m >> 1)) * kOp, m & 1, li, g, b4[m], T{});
+    }
+    __syncthreads();
+
+    double dg = 0.0, write = 0.0, hold = 0.0;
+    // <S, dS>: this thread's pieces of both
+#pragma unroll
+    for (int i = 0; i < kSt; ++i) {
+      if (tid + 512 * i < DK * kRow8) {
+        const bf16x8 sv = *at_row(sl, tid + 512 * i);
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x += (float)sv[e] * (float)dx[i][e];
+        hold += x;
+      }
+    }
+    // from the entering state, and over j <= r
+    {
+      Planes<2> pr[2], ar[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        pr[ks] = load_frag<Planes<2>>((const char*)mine + ks * kOp, lane);
+        ar[ks] = load_frag<Planes<2>>((const char*)mine + (2 + ks) * kOp, lane);
+      }
+#pragma unroll
+      for (int mm = 0; mm < MH; ++mm) {
+        const int m = half * MH + mm;
+        floatx4 a = {}, b = {};
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv) {
+          const bf16x8 st = rows(sl, m, kv);
+          a = mma(st, oo[kv], a);
+          b = mma(st, eo[kv], b);
+        }
+        a *= gam * p.scale;
+        b *= -gam;
+        const bf16x8 kt[2] = {kl.transposed(m, 0, lane), kl.transposed(m, 1, lane)};
+        a = mma_steps(kt, pr, a);
+        b = mma_steps(kt, ar, b);
+        dq[mm] += a;
+        dk[mm] += b;
+        const u32x2v q2 = *reinterpret_cast<const u32x2v*>(ql.x + tok * ql.kLd + 16 * m + 4 * g);
+        const u32x2v k2 = *reinterpret_cast<const u32x2v*>(kl.x + tok * kl.kLd + 16 * m + 4 * g);
+        dg += (double)lo_bf16(q2[0]) * a[0] + (double)hi_bf16(q2[0]) * a[1] + (double)lo_bf16(q2[1]) * a[2] + (double)hi_bf16(q2[1]) * a[3];
+        dg += (double)lo_bf16(k2[0]) * b[0] + (double)hi_bf16(k2[0]) * b[1] + (double)lo_bf16(k2[1]) * b[2] + (double)hi_bf16(k2[1]) * b[3];
+      }
+    }
+    __syncthreads();   // S is used
+#pragma unroll
+    for (int i = 0; i < kSt; ++i)
+      if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = dx[i];
+    __syncthreads();
+    // to the leaving state, and over r >= j
+    {
+      Planes<2> pc[2], ac[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        pc[ks] = load_frag<Planes<2>>((const char*)mine + (4 + ks) * kOp, lane);
+        ac[ks] = load_frag<Planes<2>>((const char*)mine + (6 + ks) * kOp, lane);
+      }
+#pragma unroll
+      for (int mm = 0; mm < MH; ++mm) {
+        const int m = half * MH + mm;
+        floatx4 a = {};
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv) a = mma(rows(sl, m, kv), fo[kv], a);
+        a *= eta * br;
+        const u32x2v k2 = *reinterpret_cast<const u32x2v*>(kl.x + tok * kl.kLd + 16 * m + 4 * g);
+        const floatx4 k4 = {lo_bf16(k2[0]), hi_bf16(k2[0]), lo_bf16(k2[1]), hi_bf16(k2[1])};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) write += (double)k4[r] * (double)a[r];
+        const bf16x8 kt[2] = {kl.transposed(m, 0, lane), kl.transposed(m, 1, lane)};
+        const bf16x8 qt[2] = {ql.transposed(m, 0, lane), ql.transposed(m, 1, lane)};
+        a = mma_steps(kt, ac, a);
+        a = mma_steps(qt, pc, a);
+        dk[mm] += a;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dg -= (double)k4[r] * (double)a[r];
+      }
+    }
+    // the log-decay's gradient
+    dg += __shfl_xor(dg, 16);
+    dg += __shfl_xor(dg, 32);
+    double sum = write + (double)last * hold;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    if (g == 0) dG[half][tok] = dg;
+    if (lane == 0) extra[wave_id()] = sum;
+    __syncthreads();
+    if (wave_id() == 0) {
+      double x = dG[0][lane] + dG[1][lane];
+      if (lane == 63) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x += extra[i];
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const double dn = __shfl_down(x, d);
+        if (lane + d < 64) x += dn;
+      }
+      if (lane < n) {
+        const float w = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
+        put(global_out<T>(p.dw) + seq.row * p.sdw.b + h * p.sdw.h + (t0 + lane) * p.sdw.t,
+            (float)(x * (double)gdr_gate_grad(w, p.gate, p.g_min)));
+        constexpr int kParts = DV / (16 * kGdrTilesBf16);
+        const auto db = global_in<float>(p.ws_db) + blk * kParts * kGdrChunk + lane;
+        float total = 0.f;
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) total += db[c * kGdrChunk];
+        put(global_out<T>(p.dbeta) + seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, total);
+      }
+    }
+    __syncthreads();
+  }
+
+  if (live) {
+    const auto dqp = global_out<T>(p.dq) + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + tok) * p.sdq.t + 4 * g;
+    const auto dkp = global_out<T>(p.dk_) + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + tok) * p.sdk.t + 4 * g;
+#pragma unroll
+    for (int mm = 0; mm < MH; ++mm) {
+      store_row4(dqp + 16 * (half * MH + mm), dq[mm]);
+      store_row4(dkp + 16 * (half * MH + mm), dk[mm]);
+    }
+  }
+}
+
+// fp32 inputs: the same sums with 4 wavefronts, one token tile and all channels each; a lane's operands come
+// straight from memory, since three 64-row tiles and a state in fp32 would not fit LDS beside K and Q.
+template <int DK, int DV>
+__global__ __launch_bounds__(256) void gdr_grad_f32_kernel(GdrParams p) {
+  using T = float;
+  using In = Frags<float>::In;
+  using Op = float8v;
   constexpr int KV = DV / 32, MT = DK / 16;
-  constexpr int kInFrag = in_frag<T>(), kOpFrag = op_frag<T, 2>();
+  constexpr int kOpFrag = op_frag<T, 2>();
   __shared__ __attribute__((aligned(16))) char tri[4][4 * kOpFrag];   // a wavefront's dP and dA, two steps each
+  __shared__ __attribute__((aligned(16))) Rows<T, DK> kl, ql;
   __shared__ float ghi[64], glo[64], bet[64];
   __shared__ double dG[64];
   __shared__ double extra[4];
@@ -45,8 +319,18 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
 
   const auto qrow = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + tok) * p.sq.t + 4 * g;
   const auto krow = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + tok) * p.sk.t + 4 * g;
-  const auto kt = as_global((const char*)p.ws_kt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
-  const auto qt = as_global((const char*)p.ws_qt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag;
+  for (int i = threadIdx.x; i < 64 * DK / 8; i += 256) {   // K and Q, zeros behind the sequence's end
+    const int r = i / (DK / 8), c0 = i % (DK / 8) * 8;
+    In a, b;
+    zero_frag(a);
+    zero_frag(b);
+    if (r < n) {
+      a = load_row8(global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + r) * p.sk.t + c0);
+      b = load_row8(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + r) * p.sq.t + c0);
+    }
+    kl.put8(r, c0, a);
+    ql.put8(r, c0, b);
+  }
 
   floatx4 dq[MT], dk[MT];
 #pragma unroll
@@ -116,24 +400,24 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
         const In st = load_row8(St + (int64_t)(16 * m + li) * DV + 32 * kv);
+        const In dst = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += (float)st[e] * (float)dst[e];
         a = mma(st, oo[kv], a);
         b = mma(st, eo[kv], b);
-        if ((m & 3) == wave) {   // <S, dS>: every row tile once
-          const In dst = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss += (float)st[e] * (float)dst[e];
-        }
       }
-      hold += ss;
+      hold += (m & 3) == wave ? ss : 0.f;   // <S, dS>: every row tile once
       a *= gam * p.scale;
       b *= -gam;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (ks > wave / 2) continue;
-        const In x = load_frag<In>(kt + (2 * m + ks) * kInFrag, lane);
+        const In x = kl.transposed(m, ks, lane);
         a = mma(x, load_frag<Op>(dp_f + ks * kOpFrag, lane), a);
         b = mma(x, load_frag<Op>(da_f + ks * kOpFrag, lane), b);
       }
+      settle(a);
+      settle(b);
       dq[m] += a;
       dk[m] += b;
       if (live) {
@@ -180,9 +464,10 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (ks < wave / 2) continue;
-        a = mma(load_frag<In>(kt + (2 * m + ks) * kInFrag, lane), load_frag<Op>(da_f + ks * kOpFrag, lane), a);
-        a = mma(load_frag<In>(qt + (2 * m + ks) * kInFrag, lane), load_frag<Op>(dp_f + ks * kOpFrag, lane), a);
+        a = mma(kl.transposed(m, ks, lane), load_frag<Op>(da_f + ks * kOpFrag, lane), a);
+        a = mma(ql.transposed(m, ks, lane), load_frag<Op>(dp_f + ks * kOpFrag, lane), a);
       }
+      settle(a);
       dk[m] += a;
 #pragma unroll
       for (int r = 0; r < 4; ++r) dg -= (double)k4[r] * (double)a[r];
@@ -229,31 +514,32 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(GdrParams p) {
   }
 }
 
-template <typename T, int DK>
-hipError_t launch_dk(const GdrParams& p, hipStream_t s) {
+template <int DK, int DV>
+hipError_t launch_one(const GdrParams& p, hipStream_t s) {
   const dim3 grid((unsigned)gdr_slots(p.B, p.T, p.n_seq, p.seq_start != nullptr), (unsigned)p.Hk);
   if (grid.x == 0) return hipSuccess;
-  switch (p.dv) {
-    case 32: hipLaunchKernelGGL((gdr_grad_kernel<T, DK, 32>), grid, dim3(256), 0, s, p); break;
-    case 64: hipLaunchKernelGGL((gdr_grad_kernel<T, DK, 64>), grid, dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((gdr_grad_kernel<T, DK, 128>), grid, dim3(256), 0, s, p); break;
-  }
+  if (p.dtype == KDA_DTYPE_BF16) hipLaunchKernelGGL((gdr_grad_kernel<DK, DV>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((gdr_grad_f32_kernel<DK, DV>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_t(const GdrParams& p, hipStream_t s) {
-  switch (p.dk) {
-    case 32: return launch_dk<T, 32>(p, s);
-    case 64: return launch_dk<T, 64>(p, s);
-    default: return launch_dk<T, 128>(p, s);
+template <int DK>
+hipError_t launch_dk(const GdrParams& p, hipStream_t s) {
+  switch (p.dv) {
+    case 32: return launch_one<DK, 32>(p, s);
+    case 64: return launch_one<DK, 64>(p, s);
+    default: return launch_one<DK, 128>(p, s);
   }
 }
 
 }  // namespace
 
 hipError_t launch_gdr_grad(const GdrParams& p, hipStream_t s) {
-  return p.dtype == KDA_DTYPE_BF16 ? launch_t<uint16_t>(p, s) : launch_t<float>(p, s);
+  switch (p.dk) {
+    case 32: return launch_dk<32>(p, s);
+    case 64: return launch_dk<64>(p, s);
+    default: return launch_dk<128>(p, s);
+  }
 }
 
 }  // namespace kda

@@ -15,6 +15,7 @@
 namespace kda {
 
 constexpr int kGdrChunk = 64;
+constexpr int kGdrTilesBf16 = 2;   // 16-column tiles that a workgroup of the sequential kernels takes (fp32: 1)
 
 struct GdrParams {
   const void *q, *k, *v, *w, *beta;
@@ -36,7 +37,7 @@ struct GdrParams {
   kda_stride_t sdq, sdk, sdv, sdw, sdb;
   float* dS0;                   // nullable
   // workspace sections, one block per (chunk slot, head); see gdr_layout
-  char *ws_gate, *ws_ti, *ws_tt, *ws_p, *ws_kt, *ws_qt, *ws_s, *ws_ds, *ws_f, *ws_db;
+  char *ws_gate, *ws_ti, *ws_tt, *ws_p, *ws_s, *ws_ds, *ws_f, *ws_db;
 };
 
 struct GdrStepParams {
@@ -240,6 +241,11 @@ __device__ __forceinline__ floatx4 mma(const float8v& a, const float8v& b, float
   return c;
 }
 
+// To be put between a matrix instruction behind a branch and the vector reads of its result: this compiler
+// leaves out the wait between them where a branch target lies between (shown in its assembly; the first
+// value read was wrong).
+__device__ __forceinline__ void settle(floatx4& x) { asm volatile("s_nop 11" : "+v"(x)); }
+
 // acc + sum over steps of a[i] b[i], as chains of their own added at the end: one dependent matrix
 // instruction takes 32 cycles, an independent one 16
 template <int K, int N> __device__ __forceinline__ floatx4 mma_steps(const bf16x8 (&a)[K], const Planes<N> (&b)[K], floatx4 acc) {
@@ -348,6 +354,31 @@ template <int N> __device__ __forceinline__ void put_op(char* frag, int half, in
 template <int N> __device__ __forceinline__ void put_op(char* frag, int half, int li, int g, floatx4 x, float) {
   *reinterpret_cast<floatx4*>(frag + (g & 1) * kPlane + (li + 16 * (2 * half + (g >> 1))) * 16) = x;
 }
+// A chunk's rows of an input in LDS, and its transpose as an A operand: lane li has channel 16 m + li of 8
+// consecutive tokens.  bf16: ds_read_b64_tr_b16, in which 16 lanes read 4 rows of 16 values and get 4 rows of
+// one column each; a row length of 8 banks modulo 64 keeps those 4 rows on different banks.
+template <typename T, int D> struct Rows {
+  static constexpr int kLd = sizeof(T) == 2 ? D + 16 : D + 4;
+  T x[64 * kLd];
+  // row `row`, values c .. c + 7
+  __device__ __forceinline__ void put8(int row, int c, const typename Frags<T>::In& v) { *reinterpret_cast<typename Frags<T>::In*>(x + row * kLd + c) = v; }
+  __device__ __forceinline__ typename Frags<T>::In transposed(int m, int ks, int lane) const {
+    const int li = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+      typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+      const T* at = x + (32 * ks + 8 * g + (li >> 2)) * kLd + 16 * m + 4 * (li & 3);
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)at);
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)(at + 4 * kLd));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      float8v f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = x[(32 * ks + 8 * g + e) * kLd + 16 * m + li];
+      return f;
+    }
+  }
+};
+
 // one value of a fragment of the inputs' type (its first plane): contraction place `k` of column `col`
 template <typename T> __device__ __forceinline__ T frag_at(const char* frag, int k, int col) {
   const int ln = col + 16 * (k >> 3);

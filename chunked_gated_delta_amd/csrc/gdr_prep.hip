@@ -7,8 +7,7 @@
 // the four 16 x 16 diagonal blocks by substitution, one a wavefront, then block column j by wavefront j,
 //   X_ij = -X_ii sum_{j <= m < i} A_im X_mj,
 // on v_mfma_f32_16x16x4_f32, whose result registers are the next product's B operand as they are (the
-// contraction runs over places 4g + r).  The backward also needs (I + diag(beta) A)^{-1} transposed, P
-// transposed, and Q transposed.
+// contraction runs over places 4g + r).  The backward also needs (I + diag(beta) A)^{-1} and P transposed.
 #include "gdr_internal.h"
 
 namespace kda {
@@ -109,37 +108,9 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
       }
     }
   }
-  // channel-major fragments of an operand in kf: the A operand of products over the chunk's tokens
-  auto transpose_out = [&](GlobalPtr<char> out) {
-#pragma unroll
-    for (int f = 0; f < DK / 32; ++f) {   // DK / 16 row tiles x 2 steps over 4 wavefronts
-      const int id = wave + 4 * f, m = id >> 1, ks = id & 1;
-      const int c = 16 * m + li;
-      T e8[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int tok = 32 * ks + 8 * g + e;
-        const char* fr = kf + ((tok >> 4) * KS + (c >> 5)) * kInFrag;
-        const int ln = (tok & 15) + 16 * ((c & 31) >> 3), el = c & 7;
-        if constexpr (sizeof(T) == 2) e8[e] = *reinterpret_cast<const T*>(fr + ln * 16 + el * 2);
-        else e8[e] = *reinterpret_cast<const T*>(fr + (el >> 2) * kPlane + ln * 16 + (el & 3) * 4);
-      }
-      In fr;
-      __builtin_memcpy(&fr, e8, sizeof(fr));
-      store_frag(out + id * kInFrag, lane, fr);
-    }
-  };
-  if constexpr (BWD) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) store_frag(kf + (wave * KS + ks) * kInFrag, lane, qr[ks]);
-    __syncthreads();
-    transpose_out(as_global(p.ws_qt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag);
-    __syncthreads();
-  }
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) store_frag(kf + (wave * KS + ks) * kInFrag, lane, kr[ks]);
   __syncthreads();
-  transpose_out(as_global(p.ws_kt) + (slot * p.Hk + kh) * (int64_t)(DK / 8) * kInFrag);
 
   floatx4 kk[4], qk[4];
 #pragma unroll
