@@ -267,7 +267,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         const float w = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
         put(global_out<T>(p.dw) + seq.row * p.sdw.b + h * p.sdw.h + (t0 + lane) * p.sdw.t,
             (float)(x * (double)gdr_gate_grad(w, p.gate, p.g_min)));
-        constexpr int kParts = DV / (16 * kGdrTilesBf16);
+        constexpr int kParts = DV / 16;
         const auto db = global_in<float>(p.ws_db) + blk * kParts * kGdrChunk + lane;
         float total = 0.f;
 #pragma unroll

@@ -15,7 +15,6 @@
 namespace kda {
 
 constexpr int kGdrChunk = 64;
-constexpr int kGdrTilesBf16 = 2;   // 16-column tiles that a workgroup of the sequential kernels takes (fp32: 1)
 
 struct GdrParams {
   const void *q, *k, *v, *w, *beta;
@@ -360,6 +359,17 @@ template <int N> __device__ __forceinline__ void put_op(char* frag, int half, in
 template <typename T, int D> struct Rows {
   static constexpr int kLd = sizeof(T) == 2 ? D + 16 : D + 4;
   T x[64 * kLd];
+  // This wavefront's 16 rows from `row0` on: loaded as whole rows (each load covers as few cache lines as it
+  // can: a compute unit has only so many requests under way), left here, and read back as the A operand
+  // of products over the channels.
+  static constexpr int kPieces = D / 8, kLoads = D / 32;   // 16-byte (fp32: 32) pieces of a row, loads a lane
+  __device__ __forceinline__ void leave(const typename Frags<T>::In (&v)[kLoads], int row0, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) put8(row0 + (64 * i + lane) / kPieces, (64 * i + lane) % kPieces * 8, v[i]);
+  }
+  __device__ __forceinline__ typename Frags<T>::In row_frag(int tile, int ks, int lane) const {
+    return load_row8(x + (16 * tile + (lane & 15)) * kLd + 32 * ks + 8 * (lane >> 4));
+  }
   // row `row`, values c .. c + 7
   __device__ __forceinline__ void put8(int row, int c, const typename Frags<T>::In& v) { *reinterpret_cast<typename Frags<T>::In*>(x + row * kLd + c) = v; }
   __device__ __forceinline__ typename Frags<T>::In transposed(int m, int ks, int lane) const {

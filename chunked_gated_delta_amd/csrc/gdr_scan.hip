@@ -7,14 +7,13 @@
 // for the one before, so everything else is kept off it.
 //  - Wavefronts 0-3 walk the chain.  Wavefront i owns token rows 16i .. 16i + 15 and a quarter of the
 //    state's rows, in registers (fp32 matrix-core results).  Wavefronts 4-7, one more on each SIMD, form the
-//    outputs (or, in the backward's run, write out the entering states and F) in the chain's shadow.
-//  - Every A operand (K, Q, K^T, T', P) has exactly one reader in the workgroup and is loaded straight into its
-//    registers, the chain's kAhead chunks ahead, as soon as the registers' present contents are used.  Loads
-//    past the last chunk are clamped to it.
+//    outputs (or, in the backward's run, write out the entering states and F) in the chain's shadow, and move
+//    v, o and the gates in rows of 16 bytes a lane, turning them in LDS.
+//  - A compute unit gets about 20 bytes a cycle from L2, whatever is asked for (80 requests of 128 bytes under
+//    way at 500 cycles each), so a step's bytes matter: K is loaded once, as whole rows, and LDS gives both
+//    its row and its transposed operands; loads are spread over the three parts of a step and issued as
+//    soon as the registers they go to are free, one step ahead.  Loads past the last chunk are clamped to it.
 //  - What the wavefronts exchange (the state, E, U: 16 columns each) goes through LDS as ready B operands.
-//  - The compute unit's address path is what limits a step next (77 % busy when each lane fetched its own
-//    values of v and the gates and wrote its own of o), so wavefronts 4-7 move v, o and the gates in
-//    rows of 16 bytes a lane and turn them in LDS.
 // Rows behind the sequence's end read its last row; their E is set to zero, so nothing of them reaches
 // the state, and their outputs are not written.
 #include <type_traits>
@@ -25,25 +24,25 @@ namespace kda {
 
 namespace {
 
-constexpr int kAhead = 2;   // chunks ahead that the chain's operands are loaded
+constexpr int kScanWaves = 2;   // wavefronts a SIMD that the registers are to allow
 
 __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ float value(float x) { return x; }
 
-// Writes `rows` contraction places x 16 NT columns of B operands (first planes; `tile` bytes from one column
-// tile to the next) to row-major memory: a lane takes 8 columns of one place.
-template <typename T, int NT>
-__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int tile, int rows, GlobalPtr<T> out, int ld, int tid) {
-  for (int i = tid; i < rows * 2 * NT; i += 256) {
-    const int r = i / (2 * NT), c0 = (i & 1) * 8, nt = (i >> 1) % NT;
-    const char* fr = frags + nt * tile + (r >> 5) * frag_bytes;
+// Writes `rows` contraction places x 16 columns of B operands (first planes) to row-major memory: a lane
+// takes 8 columns of one place.
+template <typename T>
+__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int ld, int tid) {
+  for (int i = tid; i < rows * 2; i += 256) {
+    const int r = i >> 1, c0 = (i & 1) * 8;
+    const char* fr = frags + (r >> 5) * frag_bytes;
     T x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(fr, r & 31, c0 + e);
     typename Frags<T>::In v;
     __builtin_memcpy(&v, x, sizeof(v));
-    *repoint<typename Frags<T>::In>(out + r * ld + 16 * nt + c0) = v;
+    *repoint<typename Frags<T>::In>(out + r * ld + c0) = v;
   }
 }
 
@@ -51,240 +50,221 @@ __device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, in
 // behind a branch, which would come between matrix instructions and the reads of their results (see settle).
 __device__ __forceinline__ int64_t mask_of(bool c) { return __builtin_amdgcn_readfirstlane(c ? -1 : 0); }
 
-// Byte offsets, from a chunk's first row, of the rows that a lane reads of a strided tensor: row `row` as
-// an A operand, rows r0 .. r0 + 3 as part of a result tile; in the last chunk the rows behind the
-// sequence's end become its last one.
+// Byte offset, from a chunk's first row, of what a lane reads of row `row` of a strided tensor; in the last
+// chunk the rows behind the sequence's end become its last one.
 struct LaneRow {
   uint32_t whole, tail;
   __device__ __forceinline__ LaneRow(int row, int last_rows, int64_t stride, int at, int esz)
       : whole((uint32_t)((row * stride + at) * esz)), tail((uint32_t)((min(row, last_rows - 1) * stride + at) * esz)) {}
+  LaneRow() = default;
   __device__ __forceinline__ uint32_t of(bool last) const { return last ? tail : whole; }
 };
 
-// 64 tokens x 16 NT columns in LDS, column by column (a result tile's lane reads 4 tokens of its column).
-// 128 NT threads move them: thread t has 8 columns of token t / (2 NT).
-template <typename T, int NT> struct Turned {
-  static constexpr int kLd = sizeof(T) == 2 ? 72 : 68, kPer = 2 * NT;
-  T x[16 * NT * kLd];
+// A wavefront's 16 rows of K or Q, whole rows at a time, and where the next chunk's are
+template <typename T, int DK> struct RowLoads {
+  static constexpr int kLoads = DK / 32, kPieces = DK / 8;
+  typename Frags<T>::In v[kLoads];
+  LaneRow at[kLoads];
+  GlobalPtr<const T> from;
+  __device__ __forceinline__ RowLoads(GlobalPtr<const T> first, int wave, int lane, int last_rows, int64_t stride) : from(first) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      at[i] = LaneRow(16 * wave + (64 * i + lane) / kPieces, last_rows, stride, (64 * i + lane) % kPieces * 8, sizeof(T));
+  }
+  __device__ __forceinline__ void load(bool last) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = load_row8(lane_at(from, at[i].of(last)));
+  }
+};
+
+// 64 tokens x 16 columns in LDS, column by column (a result tile's lane reads 4 tokens of its column).
+// Threads 0 .. 127 of four wavefronts move them: thread t has columns 8 (t & 1) .. + 7 of token t / 2.
+template <typename T> struct Turned {
+  static constexpr int kLd = sizeof(T) == 2 ? 72 : 68;
+  T x[16 * kLd];
   __device__ __forceinline__ void put_row(int t, const typename Frags<T>::In& v) {
     T e8[8];
     __builtin_memcpy(e8, &v, sizeof(v));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[(8 * (t % kPer) + e) * kLd + t / kPer] = e8[e];
+    for (int e = 0; e < 8; ++e) x[(8 * (t & 1) + e) * kLd + (t >> 1)] = e8[e];
   }
   __device__ __forceinline__ typename Frags<T>::In row(int t) const {
     T e8[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) e8[e] = x[(8 * (t % kPer) + e) * kLd + t / kPer];
+    for (int e = 0; e < 8; ++e) e8[e] = x[(8 * (t & 1) + e) * kLd + (t >> 1)];
     typename Frags<T>::In v;
     __builtin_memcpy(&v, e8, sizeof(v));
     return v;
   }
-  __device__ __forceinline__ floatx4 tile(int col, int r0) const {
+  __device__ __forceinline__ floatx4 tile(int li, int r0) const {
     if constexpr (sizeof(T) == 2) {
-      const u32x2v p = *reinterpret_cast<const u32x2v*>(x + col * kLd + r0);
+      const u32x2v p = *reinterpret_cast<const u32x2v*>(x + li * kLd + r0);
       return floatx4{lo_bf16(p[0]), hi_bf16(p[0]), lo_bf16(p[1]), hi_bf16(p[1])};
     } else {
-      return *reinterpret_cast<const floatx4*>(x + col * kLd + r0);
+      return *reinterpret_cast<const floatx4*>(x + li * kLd + r0);
     }
   }
-  __device__ __forceinline__ void put_tile(int col, int r0, floatx4 v) {
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2v*>(x + col * kLd + r0) = u32x2v{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
-    else *reinterpret_cast<floatx4*>(x + col * kLd + r0) = v;
+  __device__ __forceinline__ void put_tile(int li, int r0, floatx4 v) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2v*>(x + li * kLd + r0) = u32x2v{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+    else *reinterpret_cast<floatx4*>(x + li * kLd + r0) = v;
   }
 };
 // a chunk's gates in LDS
 struct Gates {
   float gam[64], eta[64], beta[64];
 };
+static_assert(kGateGam == 0 && kGateEta == 64 && kGateBeta == 128, "a wavefront each");
 
-template <typename T, int DK, int NT, bool STATES>
-__global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
+template <typename T, int DK, bool STATES>
+__global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
   using Op3 = typename Frags<T>::template Op<3>;
   using Op2 = typename Frags<T>::template Op<2>;
   constexpr int KS = DK / 32;
   constexpr int RT = DK >= 64 ? DK / 64 : 1;      // state row tiles of a wavefront
   constexpr int kOp1 = op_frag<T, 1>(), kOp2 = op_frag<T, 2>(), kOp3 = op_frag<T, 3>();
-  __shared__ __attribute__((aligned(16))) char sf[NT][KS * kOp3];          // the state, as B operands
-  __shared__ __attribute__((aligned(16))) char ef[NT][2 * kOp3];           // E
-  __shared__ __attribute__((aligned(16))) char wf[NT][2 * kOp3];           // eta U
-  __shared__ __attribute__((aligned(16))) char uf[NT][2 * kOp2];           // U (F where states are written)
+  __shared__ __attribute__((aligned(16))) char sf[KS * kOp3];              // the state, as B operands
+  __shared__ __attribute__((aligned(16))) char ef[2 * kOp3];               // E
+  __shared__ __attribute__((aligned(16))) char wf[2 * kOp3];               // eta U
+  __shared__ __attribute__((aligned(16))) char uf[2 * kOp2];               // U (F where states are written)
   __shared__ __attribute__((aligned(16))) Rows<T, DK> kl;                  // the chunk's K
-  __shared__ __attribute__((aligned(16))) Turned<T, NT> vt[2];             // v, by the chunk's parity
-  __shared__ __attribute__((aligned(16))) Turned<T, NT> ot;                // o on its way out
+  __shared__ __attribute__((aligned(16))) Rows<T, STATES ? 32 : DK> ql;    // and Q
+  __shared__ __attribute__((aligned(16))) Turned<T> vt[2];                 // v, by the chunk's parity
+  __shared__ __attribute__((aligned(16))) Turned<T> ot;                    // o on its way out
   __shared__ __attribute__((aligned(16))) Gates gate[2];
 
   int64_t unit;
   int part;
-  if (!gdr_block(blockIdx.x, p.n_seq * p.Hv, p.dv / (16 * NT), &unit, &part)) return;
+  if (!gdr_block(blockIdx.x, p.n_seq * p.Hv, p.dv / 16, &unit, &part)) return;
   const int64_t s = unit / p.Hv;
   const int h = (int)(unit % p.Hv), kh = h / (p.Hv / p.Hk);
   const GdrSeq seq = gdr_seq(p, s);
   const int64_t nc = seq.n_chunks;
   const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
   const int wave = wave_id() & 3;
-  const int col0 = 16 * NT * part;                // first of the workgroup's columns
+  const int col = 16 * part + li;
   const int r0 = 16 * wave + 4 * g;               // first of this lane's 4 token rows in result tiles
   const int last_rows = (int)(seq.len - (nc - 1) * kGdrChunk);   // tokens of the last chunk
   const int64_t blk0 = seq.slot0 * p.Hv + h;      // workspace block of chunk 0; the next is Hv further
-  const auto gates = global_in<float>(p.ws_gate) + blk0 * kGateFloats;
 
   if (wave_id() < 4) {
     const bool owner = wave * RT < DK / 16;
-    floatx4 S[NT][RT];
+    const int first_tile = owner ? wave * RT : 0;
+    floatx4 S[RT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int m = 0; m < RT; ++m) {
+      S[m] = floatx4{};
+      if (owner && p.S0) {
+        const auto at = global_in<float>(p.S0) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        S[nt][m] = floatx4{};
-        if (owner && p.S0) {
-          const auto at = global_in<float>(p.S0) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col0 + 16 * nt + li;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[nt][m][r] = at[r * p.dv];
-        }
+        for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
       }
+    }
     auto put_state = [&]() {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int m = 0; m < RT; ++m) {
-          const int t = wave * RT + m;
-          if (owner) put_op<3>(sf[nt] + (t >> 1) * kOp3, t & 1, li, g, S[nt][m], T{});
-        }
+      for (int m = 0; m < RT; ++m) {
+        const int t = wave * RT + m;
+        if (owner) put_op<3>(sf + (t >> 1) * kOp3, t & 1, li, g, S[m], T{});
+      }
     };
     put_state();
-    block_barrier();
 
     // BOTH: the wavefront's rows of T' reach into both steps of 32 tokens (wavefronts 2 and 3)
     auto walk = [&](auto both) {
       constexpr int TS = decltype(both)::value ? 2 : 1;
-      struct Buf {
-        In k[KS];
-        Op3 ti[TS];
-      };
-      // where the next loads come from
-      int64_t at = 0;
-      auto kp = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + seq.t0 * p.sk.t;
+      RowLoads<T, DK> kr(global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + seq.t0 * p.sk.t, wave, lane, last_rows, p.sk.t);
       auto tp = as_global((const char*)p.ws_ti) + blk0 * kTriFrags * kOp3 + lower_frag(wave, 0) * kOp3;
-      const LaneRow krow(16 * wave + li, last_rows, p.sk.t, 8 * g, sizeof(T));
-      auto load_k = [&](Buf& b) {
-        const auto from = lane_at(kp, krow.of(at == nc - 1));
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(from + 32 * ks);
+      int64_t k_at = 0, t_at = 0;    // the chunks whose K and T' are loaded next
+      In kf[KS];
+      Op3 ti[TS];
+      auto load_k = [&]() {
+        kr.load(k_at == nc - 1);
+        const int64_t more = mask_of(k_at < nc - 1);
+        k_at += more & 1;
+        kr.from += more & (int64_t)(kGdrChunk * p.sk.t);
       };
-      auto load_ti = [&](Buf& b) {   // and on to the next chunk
+      auto turn_k = [&]() {          // the loaded K to LDS, and this wavefront's rows back
+        kl.leave(kr.v, 16 * wave, lane);
+        load_k();
+        compiler_fence();
 #pragma unroll
-        for (int ks = 0; ks < TS; ++ks) b.ti[ks] = load_frag<Op3>(tp + ks * kOp3, lane);
-        const int64_t more = mask_of(at < nc - 1);
-        at += more & 1;
-        kp += more & (int64_t)(kGdrChunk * p.sk.t);
+        for (int ks = 0; ks < KS; ++ks) kf[ks] = kl.row_frag(wave, ks, lane);
+      };
+      auto load_ti = [&]() {
+#pragma unroll
+        for (int ks = 0; ks < TS; ++ks) ti[ks] = load_frag<Op3>(tp + ks * kOp3, lane);
+        const int64_t more = mask_of(t_at < nc - 1);
+        t_at += more & 1;
         tp += more & (int64_t)(p.Hv * (kTriFrags * kOp3));
       };
-      auto step = [&](Buf& b, int64_t c, int n) {
+      auto step = [&](int64_t c, int n) {
         const Gates& gt = gate[c & 1];
-        const floatx4 gam = ld4f((const float*)gt.gam + r0);
-        floatx4 E[NT];
+        Op3 sb[KS];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Op3 sb[KS];
+        for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>((const char*)sf + ks * kOp3, lane);
+        const floatx4 v = vt[c & 1].tile(li, r0), gam = ld4f((const float*)gt.gam + r0);
+        floatx4 E = mma_steps(kf, sb, floatx4{});
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>((const char*)sf[nt] + ks * kOp3, lane);
-          E[nt] = mma_steps(b.k, sb, floatx4{});
-        }
-        // K also goes to LDS, for the transpose; rows behind the end meet zeros of eta U
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kl.put8(16 * wave + li, 32 * ks + 8 * g, b.k[ks]);
-        load_k(b);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const floatx4 v = vt[c & 1].tile(16 * nt + li, r0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) E[nt][r] = r0 + r < n ? v[r] - gam[r] * E[nt][r] : 0.f;
-          put_op<3>(ef[nt] + (wave >> 1) * kOp3, wave & 1, li, g, E[nt], T{});
-        }
+        for (int r = 0; r < 4; ++r) E[r] = r0 + r < n ? v[r] - gam[r] * E[r] : 0.f;
+        put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, E, T{});
         block_barrier();
 
+        Op3 eb[TS];
+#pragma unroll
+        for (int ks = 0; ks < TS; ++ks) eb[ks] = load_frag<Op3>((const char*)ef + ks * kOp3, lane);
         const floatx4 eta = ld4f((const float*)gt.eta + r0), beta = ld4f((const float*)gt.beta + r0);
-        floatx4 F[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Op3 eb[TS];
-#pragma unroll
-          for (int ks = 0; ks < TS; ++ks) eb[ks] = load_frag<Op3>((const char*)ef[nt] + ks * kOp3, lane);
-          F[nt] = mma_steps(b.ti, eb, floatx4{});
-        }
-        load_ti(b);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) put_op<3>(wf[nt] + (wave >> 1) * kOp3, wave & 1, li, g, eta * (beta * F[nt]), T{});
-        block_barrier();
-
+        const float last = gt.gam[63];   // e^{G_last}: tokens behind the end do not decay
         In kt[RT][2];
-        const int first = owner ? wave * RT : 0;
 #pragma unroll
         for (int m = 0; m < RT; ++m)
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) kt[m][ks] = kl.transposed(first + m, ks, lane);
-        const float last = gt.gam[63];   // e^{G_last}: tokens behind the end do not decay
+          for (int ks = 0; ks < 2; ++ks) kt[m][ks] = kl.transposed(first_tile + m, ks, lane);
+        const floatx4 F = mma_steps(ti, eb, floatx4{});
+        load_ti();
+        const floatx4 U = beta * F;
+        put_op<3>(wf + (wave >> 1) * kOp3, wave & 1, li, g, eta * U, T{});
+        block_barrier();
+
+        const Op3 wb[2] = {load_frag<Op3>((const char*)wf, lane), load_frag<Op3>((const char*)wf + kOp3, lane)};
+        put_op<2>(uf + (wave >> 1) * kOp2, wave & 1, li, g, STATES ? F : U, T{});
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Op3 wb[2] = {load_frag<Op3>((const char*)wf[nt], lane), load_frag<Op3>((const char*)wf[nt] + kOp3, lane)};
-          put_op<2>(uf[nt] + (wave >> 1) * kOp2, wave & 1, li, g, STATES ? F[nt] : beta * F[nt], T{});
-#pragma unroll
-          for (int m = 0; m < RT; ++m) S[nt][m] = mma_steps(kt[m], wb, S[nt][m] * last);
-        }
+        for (int m = 0; m < RT; ++m) S[m] = mma_steps(kt[m], wb, S[m] * last);
+        turn_k();
         put_state();
         block_barrier();
       };
       if (nc > 0) {
-        Buf buf[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          load_k(buf[i]);
-          load_ti(buf[i]);
-        }
-        int64_t c = 0;
-        for (; c + kAhead < nc; c += kAhead) {
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) step(buf[i], c + i, kGdrChunk);
-        }
-        if (kAhead > 1 && c + 1 < nc) {
-          step(buf[0], c, kGdrChunk);
-          step(buf[kAhead - 1], c + 1, last_rows);
-        } else {
-          step(buf[0], c, last_rows);
-        }
+        load_k();
+        load_ti();
+        turn_k();
       }
+      block_barrier();
+      for (int64_t c = 0; c < nc; ++c) step(c, c == nc - 1 ? last_rows : kGdrChunk);
     };
-    static_assert(kAhead == 1 || kAhead == 2, "the loop's remainder");
     if (wave < 2) walk(std::false_type{});
     else walk(std::true_type{});
     if constexpr (!STATES) block_barrier();   // the last chunk's outputs, between wavefronts 4-7
     if (p.S_final && owner) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int m = 0; m < RT; ++m) {
+        const auto at = global_out<float>(p.S_final) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
-        for (int m = 0; m < RT; ++m) {
-          const auto at = global_out<float>(p.S_final) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col0 + 16 * nt + li;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) at[r * p.dv] = S[nt][m][r];
-        }
+        for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
+      }
     }
     return;
   }
 
   // v and the gates of one chunk ahead of the chain: loaded, then left in LDS
   const int tid = threadIdx.x & 255;
-  constexpr int kPer = 2 * NT;                    // threads to a token's columns
   In vx;
   float gx = 0.f;
   int64_t ahead = 0;
-  auto vp = global_in<T>(p.v) + seq.row * p.sv.b + h * p.sv.h + seq.t0 * p.sv.t + col0;
-  auto gp = gates + (wave < 3 ? wave : 0) * 64;
-  static_assert(kGateGam == 0 && kGateEta == 64 && kGateBeta == 128, "a wavefront each");
-  const LaneRow vrow(tid / kPer, last_rows, p.sv.t, 8 * (tid % kPer), sizeof(T));
+  auto vp = global_in<T>(p.v) + seq.row * p.sv.b + h * p.sv.h + seq.t0 * p.sv.t + 16 * part;
+  auto gp = global_in<float>(p.ws_gate) + blk0 * kGateFloats + (wave < 3 ? wave : 0) * 64;
+  const LaneRow vrow(tid >> 1, last_rows, p.sv.t, 8 * (tid & 1), sizeof(T));
   auto fetch = [&]() {
-    if (wave < kPer) vx = load_row8(lane_at(vp, vrow.of(ahead == nc - 1)));
+    if (wave < 2) vx = load_row8(lane_at(vp, vrow.of(ahead == nc - 1)));
     if (wave < 3) gx = *lane_at(gp, lane * 4);
     const int64_t more = mask_of(ahead < nc - 1);
     ahead += more & 1;
@@ -292,7 +272,7 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
     gp += more & (int64_t)(p.Hv * kGateFloats);
   };
   auto leave = [&](int64_t c) {
-    if (wave < kPer) vt[c & 1].put_row(tid, vx);
+    if (wave < 2) vt[c & 1].put_row(tid, vx);
     if (wave < 3) (wave == 0 ? gate[c & 1].gam : wave == 1 ? gate[c & 1].eta : gate[c & 1].beta)[lane] = gx;
   };
   if (nc > 0) {
@@ -300,109 +280,94 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
     leave(0);
     fetch();
   }
-  block_barrier();   // the first state, v and gates
   if constexpr (STATES) {
-    auto sp = global_out<T>(p.ws_s) + blk0 * p.dk * p.dv + col0;
-    auto fp = global_out<T>(p.ws_f) + blk0 * kGdrChunk * p.dv + col0;
+    block_barrier();   // the first state, v and gates
+    auto sp = global_out<T>(p.ws_s) + blk0 * p.dk * p.dv + 16 * part;
+    auto fp = global_out<T>(p.ws_f) + blk0 * kGdrChunk * p.dv + 16 * part;
     for (int64_t c = 0; c < nc; ++c) {
-      // the state that enters this chunk, F of the one before
-      write_rows<T, NT>(sf[0], kOp3, KS * kOp3, DK, sp, p.dv, tid);
-      sp += p.Hv * (p.dk * p.dv);
+      // F of the chunk before; the state that enters this one; what the chain needs of the next
       if (c > 0) {
-        write_rows<T, NT>(uf[0], kOp2, 2 * kOp2, kGdrChunk, fp, p.dv, tid);
+        write_rows<T>(uf, kOp2, kGdrChunk, fp, p.dv, tid);
         fp += p.Hv * (kGdrChunk * p.dv);
       }
+      block_barrier();
+      write_rows<T>(sf, kOp3, DK, sp, p.dv, tid);
+      sp += p.Hv * (p.dk * p.dv);
       block_barrier();
       leave(c + 1);
       fetch();
       block_barrier();
-      block_barrier();
     }
-    if (nc > 0) write_rows<T, NT>(uf[0], kOp2, 2 * kOp2, kGdrChunk, fp, p.dv, tid);
+    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp, p.dv, tid);
   } else {
-    auto op = global_out<T>(p.o) + seq.row * p.so.b + h * p.so.h + seq.t0 * p.so.t + col0;
-    const uint32_t orow = (uint32_t)(((tid / kPer) * p.so.t + 8 * (tid % kPer)) * sizeof(T));
+    auto op = global_out<T>(p.o) + seq.row * p.so.b + h * p.so.h + seq.t0 * p.so.t + 16 * part;
+    const uint32_t orow = (uint32_t)(((tid >> 1) * p.so.t + 8 * (tid & 1)) * sizeof(T));
     auto store = [&](int n) {
-      if (tid < kPer * n) *repoint<In>(lane_at(op, orow)) = ot.row(tid);
+      if (tid < 2 * n) *repoint<In>(lane_at(op, orow)) = ot.row(tid);
       op += kGdrChunk * p.so.t;
     };
     auto walk = [&](auto both) {
       constexpr int TS = decltype(both)::value ? 2 : 1;
-      struct Buf {
-        In q[KS], pm[TS];
-      };
-      int64_t at = 0;
-      auto qp = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + seq.t0 * p.sq.t;
+      RowLoads<T, DK> qr(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + seq.t0 * p.sq.t, wave, lane, last_rows, p.sq.t);
       auto pp = as_global((const char*)p.ws_p) + blk0 * kTriFrags * kOp1 + lower_frag(wave, 0) * kOp1;
-      const LaneRow qrow(16 * wave + li, last_rows, p.sq.t, 8 * g, sizeof(T));
-      auto load = [&](Buf& b) {
-        const auto from = lane_at(qp, qrow.of(at == nc - 1));
+      int64_t q_at = 0, p_at = 0;
+      In qf[KS], pm[TS];
+      auto load_q = [&]() {
+        qr.load(q_at == nc - 1);
+        const int64_t more = mask_of(q_at < nc - 1);
+        q_at += more & 1;
+        qr.from += more & (int64_t)(kGdrChunk * p.sq.t);
+      };
+      auto turn_q = [&]() {          // through this wavefront's own rows of LDS
+        ql.leave(qr.v, 16 * wave, lane);
+        load_q();
+        compiler_fence();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) b.q[ks] = load_row8(from + 32 * ks);
+        for (int ks = 0; ks < KS; ++ks) qf[ks] = ql.row_frag(wave, ks, lane);
+      };
+      auto load_p = [&]() {
 #pragma unroll
-        for (int ks = 0; ks < TS; ++ks) b.pm[ks] = load_frag<In>(pp + ks * kOp1, lane);
-        const int64_t more = mask_of(at < nc - 1);
-        at += more & 1;
-        qp += more & (int64_t)(kGdrChunk * p.sq.t);
+        for (int ks = 0; ks < TS; ++ks) pm[ks] = load_frag<In>(pp + ks * kOp1, lane);
+        const int64_t more = mask_of(p_at < nc - 1);
+        p_at += more & 1;
         pp += more & (int64_t)(p.Hv * (kTriFrags * kOp1));
       };
-      floatx4 O[NT];
-      // the outputs of the chunk before, whose U the chain has left; two planes of U and of the state, as o is
-      // rounded to the inputs' type
-      auto add_own = [&](Buf& b) {
+      floatx4 O = {};
+      // the outputs of a chunk whose U the chain has left; two planes of U and of the state, as o is rounded to
+      // the inputs' type
+      auto add_own = [&]() {
+        Op2 ub[TS];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Op2 ub[TS];
-#pragma unroll
-          for (int ks = 0; ks < TS; ++ks) ub[ks] = load_frag<Op2>((const char*)uf[nt] + ks * kOp2, lane);
-          O[nt] = mma_steps(b.pm, ub, O[nt]);
-        }
+        for (int ks = 0; ks < TS; ++ks) ub[ks] = load_frag<Op2>((const char*)uf + ks * kOp2, lane);
+        O = mma_steps(pm, ub, O);
+        load_p();
+        settle(O);
+        ot.put_tile(li, r0, O);
       };
-      // outputs from the chunk's entering state; meanwhile the chunk before is finished
-      auto step = [&](Buf& b, Buf& before, int64_t c) {
-        if (c > 0) add_own(before);
-        const floatx4 gam = ld4f((const float*)gate[c & 1].gam + r0);
-        floatx4 read[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Op2 sb[KS];
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op2>((const char*)sf[nt] + ks * kOp3, lane);
-          read[nt] = mma_steps(b.q, sb, floatx4{});
-          settle(read[nt]);
-        }
+      if (nc > 0) {
+        load_q();
+        load_p();
+        turn_q();
+      }
+      block_barrier();   // the first state, v and gates
+      for (int64_t c = 0; c < nc; ++c) {
+        if (c > 0) add_own();                   // finishes the chunk before
         block_barrier();
-        if (c > 0) {
-          load(before);
+        Op2 sb[KS];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) ot.put_tile(16 * nt + li, r0, O[nt]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) O[nt] = (p.scale * gam) * read[nt];
+        for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op2>((const char*)sf + ks * kOp3, lane);
+        const floatx4 gam = ld4f((const float*)gate[c & 1].gam + r0);
+        O = mma_steps(qf, sb, floatx4{});
+        settle(O);
+        O = (p.scale * gam) * O;
+        block_barrier();
+        if (c > 0) store(kGdrChunk);
+        turn_q();
         leave(c + 1);
         fetch();
         block_barrier();
-        if (c > 0) store(kGdrChunk);
-        block_barrier();
-      };
-      if (nc > 0) {
-        Buf b0, b1;
-        load(b0);
-        load(b1);
-        int64_t c = 0;
-        for (; c + 1 < nc; c += 2) {
-          step(b0, b1, c);
-          step(b1, b0, c + 1);
-        }
-        if (c < nc) {
-          step(b0, b1, c);
-          add_own(b0);
-        } else {
-          add_own(b1);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) ot.put_tile(16 * nt + li, r0, O[nt]);
       }
+      if (nc > 0) add_own();
     };
     if (wave < 2) walk(std::false_type{});
     else walk(std::true_type{});
@@ -417,181 +382,145 @@ __global__ __launch_bounds__(512) void gdr_scan_kernel(GdrParams p) {
 // Wavefronts 0-3 walk the chain; wavefronts 4-7 form P^T dO and Q^T (scale gam dO) of the chunk that comes
 // next, which do not depend on it, and write out dS of each chunk's end for the gradient kernel.  The
 // chain leaves, per 16 columns, the sums of dU F that make beta's gradient.
-template <typename T, int DK, int NT>
-__global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
+template <typename T, int DK>
+__global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p) {
   using In = typename Frags<T>::In;
   using Op3 = typename Frags<T>::template Op<3>;
   constexpr int KS = DK / 32;
   constexpr int RT = DK >= 64 ? DK / 64 : 1;
   constexpr int kIn = in_frag<T>(), kOp3 = op_frag<T, 3>();
-  constexpr int kPer = 2 * NT;                    // threads to a token's columns
-  __shared__ __attribute__((aligned(16))) char sf[NT][KS * kOp3];          // dS
-  __shared__ __attribute__((aligned(16))) char xf[NT][2 * kOp3];           // X
-  __shared__ __attribute__((aligned(16))) char ef[NT][2 * kOp3];           // -gam dE
-  __shared__ __attribute__((aligned(16))) char of[NT][2 * kIn];            // dO
-  __shared__ __attribute__((aligned(16))) char gf[NT][2 * kOp3];           // scale gam dO
-  __shared__ __attribute__((aligned(16))) float x0[NT][4 * 256];           // P^T dO, result tiles [wave][lane][4]
-  __shared__ __attribute__((aligned(16))) float d0[NT][DK / 16 * 256];     // Q^T (scale gam dO)
+  __shared__ __attribute__((aligned(16))) char sf[KS * kOp3];          // dS
+  __shared__ __attribute__((aligned(16))) char xf[2 * kOp3];           // X
+  __shared__ __attribute__((aligned(16))) char ef[2 * kOp3];           // -gam dE
+  __shared__ __attribute__((aligned(16))) char of[2 * kIn];            // dO
+  __shared__ __attribute__((aligned(16))) char gf[2 * kOp3];           // scale gam dO
+  __shared__ __attribute__((aligned(16))) float x0[4 * 256];           // P^T dO, result tiles [wave][lane][4]
+  __shared__ __attribute__((aligned(16))) float d0[DK / 16 * 256];     // Q^T (scale gam dO)
   __shared__ __attribute__((aligned(16))) Rows<T, DK> kl, ql;              // the chain's K, the next chunk's Q
-  __shared__ __attribute__((aligned(16))) Turned<T, NT> ot;                // dO on its way in
-  __shared__ __attribute__((aligned(16))) Turned<float, NT> ut;            // dU on its way out
+  __shared__ __attribute__((aligned(16))) Turned<T> ot;                // dO on its way in
+  __shared__ __attribute__((aligned(16))) Turned<float> ut;            // dU on its way out
   __shared__ __attribute__((aligned(16))) Gates gate[4];                   // by the chunk's number modulo 4
 
   int64_t unit;
   int part;
-  if (!gdr_block(blockIdx.x, p.n_seq * p.Hv, p.dv / (16 * NT), &unit, &part)) return;
+  if (!gdr_block(blockIdx.x, p.n_seq * p.Hv, p.dv / 16, &unit, &part)) return;
   const int64_t s = unit / p.Hv;
   const int h = (int)(unit % p.Hv), kh = h / (p.Hv / p.Hk);
   const GdrSeq seq = gdr_seq(p, s);
   const int64_t nc = seq.n_chunks;
   const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
   const int wave = wave_id() & 3;
-  const int col0 = 16 * NT * part;
+  const int col = 16 * part + li;
   const int r0 = 16 * wave + 4 * g;
   const int last_rows = (int)(seq.len - (nc - 1) * kGdrChunk);
   const bool owner = wave * RT < DK / 16;
   const int first_tile = owner ? wave * RT : 0;
   const int64_t blk0 = seq.slot0 * p.Hv + h;
-  const auto gates = global_in<float>(p.ws_gate) + blk0 * kGateFloats;
 
   if (wave_id() < 4) {
-    floatx4 S[NT][RT];
+    floatx4 S[RT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int m = 0; m < RT; ++m) {
+      S[m] = floatx4{};
+      if (owner && p.dSf) {
+        const auto at = global_in<float>(p.dSf) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        S[nt][m] = floatx4{};
-        if (owner && p.dSf) {
-          const auto at = global_in<float>(p.dSf) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col0 + 16 * nt + li;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[nt][m][r] = at[r * p.dv];
-        }
+        for (int r = 0; r < 4; ++r) S[m][r] = at[r * p.dv];
       }
+    }
     auto put_state = [&]() {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int m = 0; m < RT; ++m) {
-          const int t = wave * RT + m;
-          if (owner) put_op<3>(sf[nt] + (t >> 1) * kOp3, t & 1, li, g, S[nt][m], T{});
-        }
+      for (int m = 0; m < RT; ++m) {
+        const int t = wave * RT + m;
+        if (owner) put_op<3>(sf + (t >> 1) * kOp3, t & 1, li, g, S[m], T{});
+      }
     };
     put_state();
     auto walk = [&](auto both) {
       constexpr int TS = decltype(both)::value ? 2 : 1;   // T^T of wavefronts 0 and 1 reaches into both steps
-      struct Buf {
-        In k[KS];
-        Op3 tt[TS];
+      // the last chunk first, then downwards
+      RowLoads<T, DK> kr(global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (seq.t0 + (nc - 1) * kGdrChunk) * p.sk.t, wave, lane, last_rows, p.sk.t);
+      auto tp = as_global((const char*)p.ws_tt) + (blk0 + (nc - 1) * p.Hv) * kTriFrags * kOp3 + upper_frag(wave, wave < 2 ? 0 : 1) * kOp3;
+      int64_t k_at = nc - 1, t_at = nc - 1;
+      In kf[KS];
+      Op3 tt[TS];
+      auto load_k = [&]() {
+        kr.load(k_at == nc - 1);
+        const int64_t more = mask_of(k_at > 0);
+        k_at -= more & 1;
+        kr.from -= more & (int64_t)(kGdrChunk * p.sk.t);
       };
-      // where the next loads come from: the last chunk, then downwards
-      int64_t at = nc - 1;
-      auto kp = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (seq.t0 + at * kGdrChunk) * p.sk.t;
-      auto tp = as_global((const char*)p.ws_tt) + (blk0 + at * p.Hv) * kTriFrags * kOp3 + upper_frag(wave, wave < 2 ? 0 : 1) * kOp3;
-      const LaneRow krow(16 * wave + li, last_rows, p.sk.t, 8 * g, sizeof(T));
-      auto load_k = [&](Buf& b) {
-        const auto from = lane_at(kp, krow.of(at == nc - 1));
+      auto turn_k = [&]() {
+        kl.leave(kr.v, 16 * wave, lane);
+        load_k();
+        compiler_fence();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) b.k[ks] = load_row8(from + 32 * ks);
+        for (int ks = 0; ks < KS; ++ks) kf[ks] = kl.row_frag(wave, ks, lane);
       };
-      auto load_tt = [&](Buf& b) {
+      auto load_tt = [&]() {
 #pragma unroll
-        for (int ks = 0; ks < TS; ++ks) b.tt[ks] = load_frag<Op3>(tp + ks * kOp3, lane);
-        const int64_t more = mask_of(at > 0);
-        at -= more & 1;
-        kp -= more & (int64_t)(kGdrChunk * p.sk.t);
+        for (int ks = 0; ks < TS; ++ks) tt[ks] = load_frag<Op3>(tp + ks * kOp3, lane);
+        const int64_t more = mask_of(t_at > 0);
+        t_at -= more & 1;
         tp -= more & (int64_t)(p.Hv * (kTriFrags * kOp3));
       };
-      auto step = [&](Buf& b, int64_t c, int n) {
+      auto step = [&](int64_t c, int n) {
         const Gates& gt = gate[c & 3];
-        const floatx4 eta = ld4f((const float*)gt.eta + r0);
-        floatx4 X[NT];
+        Op3 sb[KS];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Op3 sb[KS];
+        for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>((const char*)sf + ks * kOp3, lane);
+        const floatx4 first = ld4f((const float*)&x0[(wave * 64 + lane) * 4]), eta = ld4f((const float*)gt.eta + r0);
+        floatx4 X = mma_steps(kf, sb, floatx4{});
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>((const char*)sf[nt] + ks * kOp3, lane);
-          X[nt] = mma_steps(b.k, sb, floatx4{});
-        }
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kl.put8(16 * wave + li, 32 * ks + 8 * g, b.k[ks]);
-        load_k(b);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const floatx4 first = ld4f((const float*)&x0[nt][(wave * 64 + lane) * 4]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) X[nt][r] = r0 + r < n ? eta[r] * X[nt][r] + first[r] : 0.f;
-          put_op<3>(xf[nt] + (wave >> 1) * kOp3, wave & 1, li, g, X[nt], T{});
-        }
+        for (int r = 0; r < 4; ++r) X[r] = r0 + r < n ? eta[r] * X[r] + first[r] : 0.f;
+        put_op<3>(xf + (wave >> 1) * kOp3, wave & 1, li, g, X, T{});
         block_barrier();
 
+        Op3 xb[TS];
+#pragma unroll
+        for (int ks = 0; ks < TS; ++ks) xb[ks] = load_frag<Op3>((const char*)xf + (ks + 2 - TS) * kOp3, lane);
         const floatx4 gam = ld4f((const float*)gt.gam + r0), beta = ld4f((const float*)gt.beta + r0);
-        floatx4 dU[NT], add[NT][RT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          Op3 xb[TS];
-#pragma unroll
-          for (int ks = 0; ks < TS; ++ks) xb[ks] = load_frag<Op3>((const char*)xf[nt] + (ks + 2 - TS) * kOp3, lane);
-#pragma unroll
-          for (int m = 0; m < RT; ++m) add[nt][m] = ld4f((const float*)&d0[nt][((first_tile + m) * 64 + lane) * 4]);
-          dU[nt] = mma_steps(b.tt, xb, floatx4{});
-        }
-        load_tt(b);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          put_op<3>(ef[nt] + (wave >> 1) * kOp3, wave & 1, li, g, -(gam * beta) * dU[nt], T{});
-          ut.put_tile(16 * nt + li, r0, dU[nt]);
-        }
-        block_barrier();
-
+        const float last = gt.gam[63];
         In kt[RT][2];
 #pragma unroll
-        for (int m = 0; m < RT; ++m)
+        for (int m = 0; m < RT; ++m) {
+          const floatx4 add = ld4f((const float*)&d0[((first_tile + m) * 64 + lane) * 4]);
+          S[m] = S[m] * last + add;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) kt[m][ks] = kl.transposed(first_tile + m, ks, lane);
-        const float last = gt.gam[63];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Op3 eb[2] = {load_frag<Op3>((const char*)ef[nt], lane), load_frag<Op3>((const char*)ef[nt] + kOp3, lane)};
-#pragma unroll
-          for (int m = 0; m < RT; ++m) S[nt][m] = mma_steps(kt[m], eb, S[nt][m] * last + add[nt][m]);
         }
+        const floatx4 dU = mma_steps(tt, xb, floatx4{});
+        load_tt();
+        put_op<3>(ef + (wave >> 1) * kOp3, wave & 1, li, g, -(gam * beta) * dU, T{});
+        ut.put_tile(li, r0, dU);
+        block_barrier();
+
+        const Op3 eb[2] = {load_frag<Op3>((const char*)ef, lane), load_frag<Op3>((const char*)ef + kOp3, lane)};
+#pragma unroll
+        for (int m = 0; m < RT; ++m) S[m] = mma_steps(kt[m], eb, S[m]);
+        turn_k();
         put_state();
         block_barrier();
       };
       if (nc > 0) {
-        Buf buf[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          load_k(buf[i]);
-          load_tt(buf[i]);
-        }
-        int64_t c = nc - 1;
-        step(buf[0], c--, last_rows);
-        if (kAhead == 1) {
-          for (; c >= 0; --c) step(buf[0], c, kGdrChunk);
-        } else {
-          for (; c > 0; c -= 2) {
-            step(buf[kAhead - 1], c, kGdrChunk);
-            step(buf[0], c - 1, kGdrChunk);
-          }
-          if (c == 0) step(buf[kAhead - 1], c, kGdrChunk);
-        }
+        load_k();
+        load_tt();
+        turn_k();
       }
+      block_barrier();
+      block_barrier();
+      block_barrier();
+      for (int64_t c = nc - 1; c >= 0; --c) step(c, c == nc - 1 ? last_rows : kGdrChunk);
     };
-    block_barrier();
-    block_barrier();
-    block_barrier();
     if (wave < 2) walk(std::true_type{});
     else walk(std::false_type{});
     if (p.dS0 && owner) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int m = 0; m < RT; ++m) {
+        const auto at = global_out<float>(p.dS0) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col;
 #pragma unroll
-        for (int m = 0; m < RT; ++m) {
-          const auto at = global_out<float>(p.dS0) + unit * p.dk * p.dv + (16 * (wave * RT + m) + 4 * g) * p.dv + col0 + 16 * nt + li;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) at[r * p.dv] = S[nt][m][r];
-        }
+        for (int r = 0; r < 4; ++r) at[r * p.dv] = S[m][r];
+      }
     }
     return;
   }
@@ -604,24 +533,22 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
     In ox, fx;
     float gx = 0.f;
     Op3 pm[TS];
-    In q[KS];
+    RowLoads<T, DK> qr(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (seq.t0 + (nc - 1) * kGdrChunk) * p.sq.t, wave, lane, last_rows, p.sq.t);
     int64_t at = nc - 1, pat = nc - 1;   // the chunk that is fetched next, and whose P and Q are loaded next
-    auto dop = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + (seq.t0 + at * kGdrChunk) * p.sdo.t + col0;
-    auto gp = gates + at * p.Hv * kGateFloats + (wave < 3 ? wave : 0) * 64;
+    auto dop = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + (seq.t0 + at * kGdrChunk) * p.sdo.t + 16 * part;
+    auto gp = global_in<float>(p.ws_gate) + (blk0 + at * p.Hv) * kGateFloats + (wave < 3 ? wave : 0) * 64;
     auto pp = as_global((const char*)p.ws_p) + ((blk0 + at * p.Hv) * kTriFrags + upper_frag(wave, TS == 2 ? 0 : 1)) * kOp3;
-    auto qp = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (seq.t0 + at * kGdrChunk) * p.sq.t;
     // of the chunk the chain is at
-    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kGdrChunk * p.dv + col0;
-    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * p.dk * p.dv + col0;
-    auto dvp = global_out<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + at * kGdrChunk) * p.sdv.t + col0;
-    auto dbp = global_out<float>(p.ws_db) + ((blk0 + at * p.Hv) * (p.dv / (16 * NT)) + part) * kGdrChunk;
-    const int row = tid / kPer;          // this thread's token of dO, F and dU
-    const LaneRow orow(row, last_rows, p.sdo.t, 8 * (tid % kPer), sizeof(T));
-    const LaneRow qrow(16 * wave + li, last_rows, p.sq.t, 8 * g, sizeof(T));
-    const uint32_t frow = (uint32_t)((row * p.dv + 8 * (tid % kPer)) * sizeof(T));
-    const uint32_t vrow = (uint32_t)((row * p.sdv.t + 8 * (tid % kPer)) * sizeof(T));
+    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kGdrChunk * p.dv + 16 * part;
+    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * p.dk * p.dv + 16 * part;
+    auto dvp = global_out<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + at * kGdrChunk) * p.sdv.t + 16 * part;
+    auto dbp = global_out<float>(p.ws_db) + ((blk0 + at * p.Hv) * (p.dv / 16) + part) * kGdrChunk;
+    const int row = tid >> 1;          // this thread's token of dO, F and dU
+    const LaneRow orow(row, last_rows, p.sdo.t, 8 * (tid & 1), sizeof(T));
+    const uint32_t frow = (uint32_t)((row * p.dv + 8 * (tid & 1)) * sizeof(T));
+    const uint32_t vrow = (uint32_t)((row * p.sdv.t + 8 * (tid & 1)) * sizeof(T));
     auto fetch = [&]() {
-      if (wave < kPer) ox = load_row8(lane_at(dop, orow.of(at == nc - 1)));
+      if (wave < 2) ox = load_row8(lane_at(dop, orow.of(at == nc - 1)));
       if (wave < 3) gx = *lane_at(gp, lane * 4);
       const int64_t more = mask_of(at > 0);
       at -= more & 1;
@@ -629,69 +556,61 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
       gp -= more & (int64_t)(p.Hv * kGateFloats);
     };
     auto leave = [&](int64_t c) {
-      if (wave < kPer) ot.put_row(tid, ox);
+      if (wave < 2) ot.put_row(tid, ox);
       if (wave < 3) (wave == 0 ? gate[c & 3].gam : wave == 1 ? gate[c & 3].eta : gate[c & 3].beta)[lane] = gx;
     };
     auto load_pq = [&]() {
 #pragma unroll
       for (int ks = 0; ks < TS; ++ks) pm[ks] = load_frag<Op3>(pp + ks * kOp3, lane);
-      const auto from = lane_at(qp, qrow.of(pat == nc - 1));
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) q[ks] = load_row8(from + 32 * ks);
+      qr.load(pat == nc - 1);
       const int64_t more = mask_of(pat > 0);
       pat -= more & 1;
       pp -= more & (int64_t)(p.Hv * (kTriFrags * kOp3));
-      qp -= more & (int64_t)(kGdrChunk * p.sq.t);
+      qr.from -= more & (int64_t)(kGdrChunk * p.sq.t);
     };
     auto load_f = [&](int64_t c) {
-      if (wave < kPer) fx = load_row8(lane_at(fp, frow));
+      if (wave < 2) fx = load_row8(lane_at(fp, frow));
       fp -= mask_of(c > 0) & (int64_t)(p.Hv * (kGdrChunk * p.dv));
     };
     auto spread = [&](int64_t c) {       // dO of chunk c as operands, and its Q
       const int n = c == nc - 1 ? last_rows : kGdrChunk;
       const floatx4 gam = p.scale * ld4f((const float*)gate[c & 3].gam + r0);
+      ql.leave(qr.v, 16 * wave, lane);
+      floatx4 x = ot.tile(li, r0);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) ql.put8(16 * wave + li, 32 * ks + 8 * g, q[ks]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        floatx4 x = ot.tile(16 * nt + li, r0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = r0 + r < n ? x[r] : 0.f;
-        put_op<1>(of[nt] + (wave >> 1) * kIn, wave & 1, li, g, x, T{});
-        put_op<3>(gf[nt] + (wave >> 1) * kOp3, wave & 1, li, g, gam * x, T{});
-      }
+      for (int r = 0; r < 4; ++r) x[r] = r0 + r < n ? x[r] : 0.f;
+      put_op<1>(of + (wave >> 1) * kIn, wave & 1, li, g, x, T{});
+      put_op<3>(gf + (wave >> 1) * kOp3, wave & 1, li, g, gam * x, T{});
     };
     // x0 and d0 are read by the chain before this chunk's second barrier and written after it
-    floatx4 X[NT], D[NT][RT];
+    floatx4 X, D[RT];
     auto products = [&]() {
       In qt[RT][2];
 #pragma unroll
       for (int m = 0; m < RT; ++m)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) qt[m][ks] = ql.transposed(first_tile + m, ks, lane);
+      X = mma(pm[TS - 1], load_frag<In>((const char*)of + kIn, lane), floatx4{});
+      if constexpr (TS == 2) X = mma(pm[0], load_frag<In>((const char*)of, lane), X);
+      const Op3 gb[2] = {load_frag<Op3>((const char*)gf, lane), load_frag<Op3>((const char*)gf + kOp3, lane)};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        X[nt] = mma(pm[TS - 1], load_frag<In>((const char*)of[nt] + kIn, lane), floatx4{});
-        if constexpr (TS == 2) X[nt] = mma(pm[0], load_frag<In>((const char*)of[nt], lane), X[nt]);
-        const Op3 gb[2] = {load_frag<Op3>((const char*)gf[nt], lane), load_frag<Op3>((const char*)gf[nt] + kOp3, lane)};
-#pragma unroll
-        for (int m = 0; m < RT; ++m) D[nt][m] = mma_steps(qt[m], gb, floatx4{});
+      for (int m = 0; m < RT; ++m) {
+        D[m] = mma_steps(qt[m], gb, floatx4{});
+        settle(D[m]);
       }
+      settle(X);
       load_pq();
     };
     auto leave_products = [&]() {
+      *reinterpret_cast<floatx4*>(&x0[(wave * 64 + lane) * 4]) = X;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        *reinterpret_cast<floatx4*>(&x0[nt][(wave * 64 + lane) * 4]) = X[nt];
-#pragma unroll
-        for (int m = 0; m < RT; ++m)
-          if (owner) *reinterpret_cast<floatx4*>(&d0[nt][((wave * RT + m) * 64 + lane) * 4]) = D[nt][m];
-      }
+      for (int m = 0; m < RT; ++m)
+        if (owner) *reinterpret_cast<floatx4*>(&d0[((wave * RT + m) * 64 + lane) * 4]) = D[m];
     };
     // dU as the chain has left it: the gradient of v, and beta's over these columns
     auto finish = [&](int64_t c) {
       const int n = c == nc - 1 ? last_rows : kGdrChunk;
-      if (wave < kPer) {
+      if (wave < 2) {
         const float b = gate[c & 3].beta[row];
         const float8v dU = ut.row(tid);
         T f8[8];
@@ -699,16 +618,15 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
         float x = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x += dU[e] * value(f8[e]);
-#pragma unroll
-        for (int d = 1; d < kPer; d <<= 1) x += __shfl_xor(x, d);
-        if (tid % kPer == 0) *lane_at(dbp, row * 4) = x;
+        x += __shfl_xor(x, 1);
+        if ((tid & 1) == 0) *lane_at(dbp, row * 4) = x;
         if (row < n) {
           store_row4(lane_at(dvp, vrow), b * floatx4{dU[0], dU[1], dU[2], dU[3]});
           store_row4(lane_at(dvp, vrow + 4 * sizeof(T)), b * floatx4{dU[4], dU[5], dU[6], dU[7]});
         }
       }
       dvp -= kGdrChunk * p.sdv.t;
-      dbp -= p.Hv * (p.dv / (16 * NT) * kGdrChunk);
+      dbp -= p.Hv * (p.dv / 16 * kGdrChunk);
     };
     if (nc > 0) {
       fetch();
@@ -729,7 +647,7 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
     block_barrier();
     for (int64_t c = nc - 1; c >= 0; --c) {
       // dS at this chunk's end; what the chain needs of the next one
-      write_rows<T, NT>(sf[0], kOp3, KS * kOp3, DK, sp, p.dv, tid);
+      write_rows<T>(sf, kOp3, DK, sp, p.dv, tid);
       sp -= p.Hv * (p.dk * p.dv);
       if (c > 0) spread(c - 1);
       block_barrier();
@@ -747,22 +665,21 @@ __global__ __launch_bounds__(512) void gdr_rscan_kernel(GdrParams p) {
   else serve(std::false_type{});
 }
 
-template <typename T, int DK, int NT>
+template <typename T, int DK>
 hipError_t launch_scan(const GdrParams& p, hipStream_t s, int kind) {
-  const dim3 grid((unsigned)gdr_blocks(p.n_seq * p.Hv, p.dv / (16 * NT)));
-  if (kind == 0) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, NT, false>), grid, dim3(512), 0, s, p);
-  else if (kind == 1) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, NT, true>), grid, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((gdr_rscan_kernel<T, DK, NT>), grid, dim3(512), 0, s, p);
+  const dim3 grid((unsigned)gdr_blocks(p.n_seq * p.Hv, p.dv / 16));
+  if (kind == 0) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, false>), grid, dim3(512), 0, s, p);
+  else if (kind == 1) hipLaunchKernelGGL((gdr_scan_kernel<T, DK, true>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((gdr_rscan_kernel<T, DK>), grid, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_t(const GdrParams& p, hipStream_t s, int kind) {
-  constexpr int NT = sizeof(T) == 2 ? kGdrTilesBf16 : 1;
   switch (p.dk) {
-    case 32: return launch_scan<T, 32, NT>(p, s, kind);
-    case 64: return launch_scan<T, 64, NT>(p, s, kind);
-    default: return launch_scan<T, 128, NT>(p, s, kind);
+    case 32: return launch_scan<T, 32>(p, s, kind);
+    case 64: return launch_scan<T, 64>(p, s, kind);
+    default: return launch_scan<T, 128>(p, s, kind);
   }
 }
 
