@@ -28,7 +28,8 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
   constexpr int kOp = op_frag<T, 2>(), kLd = DV + 8;
   constexpr int kRow8 = DV / 8;                            // 16-byte pieces of a row
   constexpr int kTok = 64 * kRow8 / 512 ? 64 * kRow8 / 512 : 1;   // pieces a thread moves of 64 rows,
-  constexpr int kSt = DK * kRow8 / 512 ? DK * kRow8 / 512 : 1;    // and of DK rows
+  constexpr int kSt = DK * kRow8 / 512 ? DK * kRow8 / 512 : 1;    // of DK rows,
+  constexpr int kCh = 64 * (DK / 8) / 512 ? 64 * (DK / 8) / 512 : 1;   // and of K or Q
   constexpr int kTri = 4 * 8 * kOp, kXBytes = 3 * 64 * kLd * 2 > kTri ? 3 * 64 * kLd * 2 : kTri;
   // F, dO and dE; then the triangular factors: per token tile 2 steps of dP and dA over j, 2 of each over r
   __shared__ __attribute__((aligned(16))) char xs[kXBytes];
@@ -45,31 +46,22 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
   const int64_t slot = blockIdx.x;
   if (!gdr_find(p, slot, &seq, &chunk)) return;
   const int kh = blockIdx.y, grp = p.Hv / p.Hk;
-  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4;
+  int tid = threadIdx.x;
   const int tile = wave_id() & 3, half = wave_id() >> 2;   // token tile; half of the channels
   const int64_t t0 = seq.t0 + chunk * kGdrChunk, left = seq.len - chunk * kGdrChunk;
   const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-  const int tok = 16 * tile + li;                          // this lane's token
-  const bool live = tok < n;
   char* mine = xs + tile * 8 * kOp;
-
-  // K and Q, zeros behind the sequence's end
-  for (int i = tid; i < 64 * DK / 8; i += 512) {
-    const int r = i / (DK / 8), c0 = i % (DK / 8) * 8;
-    bf16x8 a = {}, b = {};
-    if (r < n) {
-      a = load_row8(global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + r) * p.sk.t + c0);
-      b = load_row8(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + r) * p.sq.t + c0);
-    }
-    kl.put8(r, c0, a);
-    ql.put8(r, c0, b);
-  }
 
   floatx4 dq[MH], dk[MH];
 #pragma unroll
   for (int m = 0; m < MH; ++m) dq[m] = dk[m] = floatx4{};
 
   for (int hg = 0; hg < grp; ++hg) {
+    // said anew for every head: addresses that the loop does not change would otherwise be kept in registers
+    // by the dozen
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, li = lane & 15, g = lane >> 4;
+    const int tok = 16 * tile + li;                        // this lane's token
     const int h = kh * grp + hg;
     const int64_t blk = slot * p.Hv + h;
     const auto gate = global_in<float>(p.ws_gate) + blk * kGateFloats;
@@ -79,7 +71,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     const auto dO = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t;
     const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t;
     // everything is asked for at once
-    bf16x8 fx[kTok], ox[kTok], ex[kTok], sx[kSt], dx[kSt];
+    bf16x8 fx[kTok], ox[kTok], ex[kTok], sx[kSt], dx[kSt], kx[kCh], qx[kCh];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const int at = tid + 512 * i, r = at / kRow8, c0 = at % kRow8 * 8;
@@ -98,6 +90,25 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         sx[i] = load_row8(St + at * 8);
         dx[i] = load_row8(dSt + at * 8);
       }
+    }
+    if (hg == 0) {   // K and Q, zeros behind the sequence's end
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) {
+        const int at = tid + 512 * i, r = at / (DK / 8), c0 = at % (DK / 8) * 8;
+        kx[i] = qx[i] = bf16x8{};
+        if (r < n) {
+          kx[i] = load_row8(global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + r) * p.sk.t + c0);
+          qx[i] = load_row8(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + r) * p.sq.t + c0);
+        }
+      }
+    }
+    // what the last wavefront needs at the end: a token a lane
+    constexpr int kParts = DV / 16;
+    float w_last = 0.f, db_last[kParts];
+    if (wave_id() == 7) {
+      if (lane < n) w_last = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) db_last[c] = global_in<float>(p.ws_db)[(blk * kParts + c) * kGdrChunk + lane];
     }
     if (tid < 64) {
       ghi[tid] = gate[kGateHi + tid];
@@ -118,6 +129,16 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
 #pragma unroll
     for (int i = 0; i < kSt; ++i)
       if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = sx[i];
+    if (hg == 0) {
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) {
+        const int at = tid + 512 * i, row = at / (DK / 8), c0 = at % (DK / 8) * 8;
+        if (row < 64) {
+          kl.put8(row, c0, kx[i]);
+          ql.put8(row, c0, qx[i]);
+        }
+      }
+    }
     __syncthreads();
 
     auto rows = [&](const T* base, int t, int kv) { return load_row8(base + (16 * t + li) * kLd + 32 * kv + 8 * g); };
@@ -133,22 +154,33 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     const float ghr = ghi[tok], glr = glo[tok], br = bet[tok];
     floatx4 a4[4], b4[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      a4[m] = b4[m] = floatx4{};
-      const bool rowwise = half == 0;
-      if (rowwise ? m <= tile : m >= tile) {
+    for (int m = 0; m < 4; ++m) a4[m] = b4[m] = floatx4{};
+    if (half == 0) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m > tile) break;
 #pragma unroll
         for (int kv = 0; kv < KV; ++kv) {
-          if (rowwise) {
-            const bf16x8 f = rows(fl, m, kv);
-            a4[m] = mma(f, oo[kv], a4[m]);
-            b4[m] = mma(f, eo[kv], b4[m]);
-          } else {
-            a4[m] = mma(rows(ol, m, kv), fo[kv], a4[m]);
-            b4[m] = mma(rows(el, m, kv), fo[kv], b4[m]);
-          }
+          const bf16x8 x = rows(fl, m, kv);
+          a4[m] = mma(x, oo[kv], a4[m]);
+          b4[m] = mma(x, eo[kv], b4[m]);
         }
       }
+    } else {
+#pragma unroll
+      for (int m = 3; m >= 0; --m) {
+        if (m < tile) break;
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv) {
+          a4[m] = mma(rows(ol, m, kv), fo[kv], a4[m]);
+          b4[m] = mma(rows(el, m, kv), fo[kv], b4[m]);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      settle(a4[m]);
+      settle(b4[m]);
     }
     __syncthreads();   // everyone has read F, dO and dE
 #pragma unroll
@@ -252,7 +284,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     if (g == 0) dG[half][tok] = dg;
     if (lane == 0) extra[wave_id()] = sum;
     __syncthreads();
-    if (wave_id() == 0) {
+    if (wave_id() == 7) {   // while the others go on
       double x = dG[0][lane] + dG[1][lane];
       if (lane == 63) {
 #pragma unroll
@@ -264,21 +296,19 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         if (lane + d < 64) x += dn;
       }
       if (lane < n) {
-        const float w = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
         put(global_out<T>(p.dw) + seq.row * p.sdw.b + h * p.sdw.h + (t0 + lane) * p.sdw.t,
-            (float)(x * (double)gdr_gate_grad(w, p.gate, p.g_min)));
-        constexpr int kParts = DV / 16;
-        const auto db = global_in<float>(p.ws_db) + blk * kParts * kGdrChunk + lane;
+            (float)(x * (double)gdr_gate_grad(w_last, p.gate, p.g_min)));
         float total = 0.f;
 #pragma unroll
-        for (int c = 0; c < kParts; ++c) total += db[c * kGdrChunk];
+        for (int c = 0; c < kParts; ++c) total += db_last[c];
         put(global_out<T>(p.dbeta) + seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, total);
       }
     }
-    __syncthreads();
+    if (hg + 1 < grp) __syncthreads();
   }
 
-  if (live) {
+  const int lane = tid & 63, g = lane >> 4, tok = 16 * tile + (lane & 15);
+  if (tok < n) {
     const auto dqp = global_out<T>(p.dq) + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + tok) * p.sdq.t + 4 * g;
     const auto dkp = global_out<T>(p.dk_) + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + tok) * p.sdk.t + 4 * g;
 #pragma unroll
@@ -292,7 +322,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
 // fp32 inputs: the same sums with 4 wavefronts, one token tile and all channels each; a lane's operands come
 // straight from memory, since three 64-row tiles and a state in fp32 would not fit LDS beside K and Q.
 template <int DK, int DV>
-__global__ __launch_bounds__(256) void gdr_grad_f32_kernel(GdrParams p) {
+__global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
   using T = float;
   using In = Frags<float>::In;
   using Op = float8v;
@@ -406,6 +436,7 @@ __global__ __launch_bounds__(256) void gdr_grad_f32_kernel(GdrParams p) {
         a = mma(st, oo[kv], a);
         b = mma(st, eo[kv], b);
       }
+      asm volatile("" : "+v"(ss));   // now: put off to the end, it would keep every row of S and dS till then
       hold += (m & 3) == wave ? ss : 0.f;   // <S, dS>: every row tile once
       a *= gam * p.scale;
       b *= -gam;

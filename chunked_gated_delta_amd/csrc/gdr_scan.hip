@@ -543,10 +543,12 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * p.dk * p.dv + 16 * part;
     auto dvp = global_out<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + at * kGdrChunk) * p.sdv.t + 16 * part;
     auto dbp = global_out<float>(p.ws_db) + ((blk0 + at * p.Hv) * (p.dv / 16) + part) * kGdrChunk;
-    const int row = tid >> 1;          // this thread's token of dO, F and dU
+    // wavefronts 4 and 5 move dO, wavefronts 6 and 7 F, dU and the gradients that are made of them: a lane has
+    // half a token's columns
+    const int tid2 = tid & 127, row = tid2 >> 1;
     const LaneRow orow(row, last_rows, p.sdo.t, 8 * (tid & 1), sizeof(T));
-    const uint32_t frow = (uint32_t)((row * p.dv + 8 * (tid & 1)) * sizeof(T));
-    const uint32_t vrow = (uint32_t)((row * p.sdv.t + 8 * (tid & 1)) * sizeof(T));
+    const uint32_t frow = (uint32_t)((row * p.dv + 8 * (tid2 & 1)) * sizeof(T));
+    const uint32_t vrow = (uint32_t)((row * p.sdv.t + 8 * (tid2 & 1)) * sizeof(T));
     auto fetch = [&]() {
       if (wave < 2) ox = load_row8(lane_at(dop, orow.of(at == nc - 1)));
       if (wave < 3) gx = *lane_at(gp, lane * 4);
@@ -569,7 +571,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       qr.from -= more & (int64_t)(kGdrChunk * p.sq.t);
     };
     auto load_f = [&](int64_t c) {
-      if (wave < 2) fx = load_row8(lane_at(fp, frow));
+      if (wave >= 2) fx = load_row8(lane_at(fp, frow));
       fp -= mask_of(c > 0) & (int64_t)(p.Hv * (kGdrChunk * p.dv));
     };
     auto spread = [&](int64_t c) {       // dO of chunk c as operands, and its Q
@@ -599,7 +601,6 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
         settle(D[m]);
       }
       settle(X);
-      load_pq();
     };
     auto leave_products = [&]() {
       *reinterpret_cast<floatx4*>(&x0[(wave * 64 + lane) * 4]) = X;
@@ -610,9 +611,9 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     // dU as the chain has left it: the gradient of v, and beta's over these columns
     auto finish = [&](int64_t c) {
       const int n = c == nc - 1 ? last_rows : kGdrChunk;
-      if (wave < 2) {
+      if (wave >= 2) {
         const float b = gate[c & 3].beta[row];
-        const float8v dU = ut.row(tid);
+        const float8v dU = ut.row(tid2);
         T f8[8];
         __builtin_memcpy(f8, &fx, sizeof(fx));
         float x = 0.f;
@@ -641,6 +642,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     if (nc > 0) {
       products();
       leave_products();
+      load_pq();
       leave(nc - 2);
       fetch();
     }
@@ -653,7 +655,10 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       block_barrier();
       if (c > 0) products();
       block_barrier();
-      if (c > 0) leave_products();
+      if (c > 0) {
+        leave_products();
+        load_pq();
+      }
       finish(c);
       load_f(c - 1);
       leave(c - 2);
