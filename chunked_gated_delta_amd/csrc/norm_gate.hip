@@ -3,11 +3,13 @@
 // with rms(t) = sqrt(mean(t^2) + eps); the norm of x, the gate, the residual and the norm of s may each be
 // absent.  Bound by HBM: every tensor is read or written once.  NT threads hold a row in registers, in
 // fp32, 8 consecutive values a vector access where the row allows it and strided single values otherwise;
-// s is normalised before it is rounded.
+// s is normalised before it is rounded.  8191 rows of 4096 in bf16 with both norms, the gate and the residual: 335 MB
+// in 78 us, 4.3 TB/s (a large copy: 4.8); with 512 threads a row 81 us.
 //
 // The backward recomputes the row's forward from the same inputs (it reads the residual in place of s: as
 // many bytes, and exact), and sums the weights' gradients over the rows a workgroup takes, in registers;
-// the workgroups' sums are added up by a second kernel in a fixed order.
+// the workgroups' sums are added up by a second kernel in a fixed order.  Each workgroup more is one more row for that
+// kernel: 512 of them, two a compute unit.  131072 gated rows of 128 in bf16: 168 MB in 50 + 4 us.
 #include "gdr_internal.h"
 
 namespace kda {
@@ -82,8 +84,19 @@ __device__ __forceinline__ void store_part(GlobalPtr<T> row, RowMap<NT, VEC> m, 
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
-template <typename T> __device__ __forceinline__ GlobalPtr<T> row_of(const void* p, kda_stride_t s, int64_t b, int64_t h, int64_t t) {
-  return (GlobalPtr<T>)p + b * s.b + h * s.h + t * s.t;
+// The place of row number (b H + h) T + t; the rows are fewer than 2^27 (checked on the host), so 32 bits divide
+// them: a lane's two 64-bit divisions would be more instructions than the rest of a short row takes.
+struct RowAt {
+  uint32_t b, h, t;
+  __device__ __forceinline__ RowAt(const NormParams& p, uint32_t row) {
+    const uint32_t T = (uint32_t)p.T, H = (uint32_t)p.H, bh = row / T;
+    t = row - bh * T;
+    b = bh / H;
+    h = bh - b * H;
+  }
+};
+template <typename T> __device__ __forceinline__ GlobalPtr<T> row_of(const void* p, kda_stride_t s, const RowAt& i) {
+  return (GlobalPtr<T>)p + i.b * s.b + i.h * s.h + i.t * s.t;
 }
 
 // the weight of this thread's values, in either type
@@ -102,10 +115,10 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormParams p) {
   const RowMap<NT, VEC> m{(int)(threadIdx.x % NT), (int)p.D};
   const int64_t row = (int64_t)blockIdx.x * GROUPS + group;
   if (row >= rows) return;
-  const int64_t t = row % p.T, bh = row / p.T, h = bh % p.H, b = bh / p.H;
+  const RowAt at(p, (uint32_t)row);
   float x[E], a[E], w[E];
-  load_part<T, NT, VPT, VEC>(row_of<T>(p.x, p.sx, b, h, t), m, x);
-  if (p.z) load_part<T, NT, VPT, VEC>(row_of<T>(p.z, p.sz, b, h, t), m, a);
+  load_part<T, NT, VPT, VEC>(row_of<T>(p.x, p.sx, at), m, x);
+  if (p.z) load_part<T, NT, VPT, VEC>(row_of<T>(p.z, p.sz, at), m, a);
   if (p.weight) {
     load_weight<T, NT, VPT, VEC>(p.weight, p.wdtype, m, w);
     float q = 0.f;
@@ -120,14 +133,14 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormParams p) {
     for (int e = 0; e < E; ++e) x[e] *= sigmoid(a[e]) * (p.act == KDA_ACT_SILU ? a[e] : 1.f);
   }
   if (p.res) {
-    load_part<T, NT, VPT, VEC>(row_of<T>(p.res, p.sr, b, h, t), m, a);
+    load_part<T, NT, VPT, VEC>(row_of<T>(p.res, p.sr, at), m, a);
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = p.alpha * x[e] + a[e];
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= p.alpha;
   }
-  store_part<T, NT, VPT, VEC>(row_of<T>(p.s, p.ss, b, h, t), m, x);
+  store_part<T, NT, VPT, VEC>(row_of<T>(p.s, p.ss, at), m, x);
   if (p.weight2) {
     load_weight<T, NT, VPT, VEC>(p.weight2, p.wdtype, m, w);
     float q = 0.f;
@@ -136,11 +149,12 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormParams p) {
     const float r = rsqrtf(row_sum<NT>(q, lds, group) / (float)p.D + p.eps);
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= r * w[e];
-    store_part<T, NT, VPT, VEC>(row_of<T>(p.y, p.sy, b, h, t), m, x);
+    store_part<T, NT, VPT, VEC>(row_of<T>(p.y, p.sy, at), m, x);
   }
 }
 
-template <typename T, int NT, int VPT, bool VEC, int THREADS>
+// SECOND: with the norm of s.  Without it the kernel needs half the registers, so twice the rows are under way.
+template <typename T, int NT, int VPT, bool VEC, int THREADS, bool SECOND>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
   constexpr int E = VPT * 8, GROUPS = THREADS / NT;
   __shared__ float lds[THREADS / 64];
@@ -148,23 +162,29 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
   const int64_t rows = p.B * p.H * p.T;
   const int group = threadIdx.x / NT;
   const RowMap<NT, VEC> m{(int)(threadIdx.x % NT), (int)p.D};
-  float dw[E], dw2[E];
+  float dw[E], dw2[SECOND ? E : 1], kept[VPT == 1 ? E : 1];
 #pragma unroll
-  for (int e = 0; e < E; ++e) dw[e] = dw2[e] = 0.f;
+  for (int e = 0; e < E; ++e) {
+    dw[e] = 0.f;
+    if constexpr (SECOND) dw2[e] = 0.f;
+  }
+  if constexpr (VPT == 1) {   // longer parts of a row leave no registers for it
+    if (p.weight) load_weight<T, NT, VPT, VEC>(p.weight, p.wdtype, m, kept);
+  }
 
   // every thread of a workgroup makes the same number of turns (the row sums hold barriers)
   for (int64_t first = (int64_t)blockIdx.x * GROUPS; first < rows; first += (int64_t)gridDim.x * GROUPS) {
     const bool live = first + group < rows;
     const int64_t row = live ? first + group : rows - 1;
-    const int64_t t = row % p.T, bh = row / p.T, h = bh % p.H, b = bh / p.H;
-    float x[E], n[E], a[E], g[E], w[E], s[E];
-    load_part<T, NT, VPT, VEC>(row_of<T>(p.x, p.sx, b, h, t), m, x);
-    if (p.ds) load_part<T, NT, VPT, VEC>(row_of<T>(p.ds, p.sds, b, h, t), m, g);
+    const RowAt at(p, (uint32_t)row);
+    float x[E], n[E], a[E], g[E], w[E];
+    load_part<T, NT, VPT, VEC>(row_of<T>(p.x, p.sx, at), m, x);
+    if (p.ds) load_part<T, NT, VPT, VEC>(row_of<T>(p.ds, p.sds, at), m, g);
     else {
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] = 0.f;
     }
-    if (p.z) load_part<T, NT, VPT, VEC>(row_of<T>(p.z, p.sz, b, h, t), m, a);
+    if (p.z) load_part<T, NT, VPT, VEC>(row_of<T>(p.z, p.sz, at), m, a);
     float r = 1.f;
     if (p.weight) {
       float q = 0.f;
@@ -173,9 +193,10 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
       r = rsqrtf(row_sum<NT>(q, lds, group) / (float)p.D + p.eps);
     }
     if (p.weight) {
-      load_weight<T, NT, VPT, VEC>(p.weight, p.wdtype, m, w);
+      if constexpr (VPT > 1) load_weight<T, NT, VPT, VEC>(p.weight, p.wdtype, m, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
+        if constexpr (VPT == 1) w[e] = kept[e];
         x[e] *= r;            // x / rms(x)
         n[e] = x[e] * w[e];
       }
@@ -183,10 +204,10 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) n[e] = x[e];
     }
-    if (p.weight2) {   // through the second norm: g becomes the whole gradient of s
-      float res[E], dy[E], w2[E];
-      if (p.res) load_part<T, NT, VPT, VEC>(row_of<T>(p.res, p.sr, b, h, t), m, res);
-      load_part<T, NT, VPT, VEC>(row_of<T>(p.dy, p.sdy, b, h, t), m, dy);
+    if constexpr (SECOND) {   // through the second norm: g becomes the whole gradient of s
+      float s[E], res[E], dy[E], w2[E];
+      if (p.res) load_part<T, NT, VPT, VEC>(row_of<T>(p.res, p.sr, at), m, res);
+      load_part<T, NT, VPT, VEC>(row_of<T>(p.dy, p.sdy, at), m, dy);
       load_weight<T, NT, VPT, VEC>(p.weight2, p.wdtype, m, w2);
       float q = 0.f;
 #pragma unroll
@@ -209,7 +230,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] += r2 * (dy[e] - s[e] * c);
     }
-    if (p.dres && live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dres, p.sdr, b, h, t), m, g);
+    if (p.dres && live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dres, p.sdr, at), m, g);
 #pragma unroll
     for (int e = 0; e < E; ++e) g[e] *= p.alpha;
     if (p.z) {
@@ -221,7 +242,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
         a[e] = g[e] * n[e] * der;
         g[e] *= val;
       }
-      if (p.dz && live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dz, p.sdz, b, h, t), m, a);
+      if (p.dz && live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dz, p.sdz, at), m, a);
     }
     if (p.weight) {
       float c = 0.f;
@@ -235,14 +256,16 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] = r * (g[e] - x[e] * c);
     }
-    if (live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dx, p.sdx, b, h, t), m, g);
+    if (live) store_part<T, NT, VPT, VEC>(row_of<T>(p.dx, p.sdx, at), m, g);
   }
 
   // this workgroup's sums: the row groups' one after another
   for (int which = 0; which < 2; ++which) {
     if (which == 0 ? !p.dweight : !p.dweight2) continue;
     const auto out = as_global(p.partial) + ((int64_t)which * kMaxBwdBlocks + blockIdx.x) * p.D;
-    float (&d)[E] = which == 0 ? dw : dw2;
+    float d[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) d[e] = which == 0 ? dw[e] : dw2[SECOND ? e : 0];
     if constexpr (GROUPS > 1) {
       __syncthreads();
 #pragma unroll
@@ -252,6 +275,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormParams p) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           float sum = 0.f;
+#pragma unroll 2   // whole, it would take more registers than the rows
           for (int q = 0; q < GROUPS; ++q) sum += acc[(q * E + e) * NT + m.t];
           d[e] = sum;
         }
@@ -277,8 +301,17 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(NormParams p, int blo
   if (!out) return;
   const auto in = global_in<float>(p.partial) + (int64_t)which * kMaxBwdBlocks * p.D;
   float s = 0.f;
-  if (col < p.D)
-    for (int i = y; i < blocks; i += 64) s += in[(int64_t)i * p.D + col];
+  if (col < p.D) {
+    int i = y;
+    for (; i + 7 * 64 < blocks; i += 8 * 64) {   // eight loads under way at once
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = in[(int64_t)(i + 64 * k) * p.D + col];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += x[k];
+    }
+    for (; i < blocks; i += 64) s += in[(int64_t)i * p.D + col];
+  }
   part[y][c] = s;
   __syncthreads();
   if (y == 0 && col < p.D) {
@@ -297,15 +330,21 @@ bool vec_ok(const void* ptr, kda_stride_t s, int esz) {
 
 template <typename T, int NT, int VPT, bool VEC>
 hipError_t launch_one(const NormParams& p, hipStream_t s, bool bwd) {
-  constexpr int THREADS = NT > 256 ? NT : 256, GROUPS = THREADS / NT;
   const int64_t rows = p.B * p.H * p.T;
-  const int64_t blocks = (rows + GROUPS - 1) / GROUPS;
   if (!bwd) {
-    hipLaunchKernelGGL((norm_fwd_kernel<T, NT, VPT, VEC, THREADS>), dim3((unsigned)blocks), dim3(THREADS), 0, s, p);
+    constexpr int THREADS = NT > 256 ? NT : 256, GROUPS = THREADS / NT;
+    hipLaunchKernelGGL((norm_fwd_kernel<T, NT, VPT, VEC, THREADS>), dim3((unsigned)((rows + GROUPS - 1) / GROUPS)), dim3(THREADS), 0, s, p);
     return hipGetLastError();
   }
+  // Short rows: workgroups of 8 wavefronts, so that two a compute unit put 16 rows' loads more under way (gradients
+  // of 131072 gated rows of 128: 50 us against 55 with 4 wavefronts and 58 with 16); 16 values a lane have no
+  // registers for that.
+  constexpr int THREADS = NT > 256 || (NT <= 64 && VPT == 1) ? 512 : 256, GROUPS = THREADS / NT;
+  const int64_t blocks = (rows + GROUPS - 1) / GROUPS;
   const int grid = (int)(blocks < kMaxBwdBlocks ? blocks : kMaxBwdBlocks);
-  hipLaunchKernelGGL((norm_bwd_kernel<T, NT, VPT, VEC, THREADS>), dim3(grid), dim3(THREADS), 0, s, p);
+  if (grid == 0) {}   // no rows: the weights' sums alone
+  else if (p.weight2) hipLaunchKernelGGL((norm_bwd_kernel<T, NT, VPT, VEC, THREADS, true>), dim3(grid), dim3(THREADS), 0, s, p);
+  else hipLaunchKernelGGL((norm_bwd_kernel<T, NT, VPT, VEC, THREADS, false>), dim3(grid), dim3(THREADS), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.dweight && !p.dweight2)) return e;
   hipLaunchKernelGGL(norm_weight_kernel, dim3((unsigned)((p.D + 15) / 16), 2), dim3(1024), 0, s, p, grid);

@@ -69,8 +69,12 @@ def _gpu(t, name):
 
 
 def _call(name, dev, args):
-    with torch.cuda.device(dev):
-        rc = getattr(_lib.load(), name)(*args)
+    fn = getattr(_lib.load(), name)
+    if dev.index == torch.cuda.current_device():   # the guard costs more than a microsecond
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
     if rc != 0:
         raise KdaError(rc, name, _lib.last_hip_error() if rc == _lib.KDA_ERR_HIP else "")
 
@@ -311,12 +315,6 @@ def norm_gate_bwd(x, ds, dy=None, weight=None, z=None, act: str = "silu", residu
         stream = torch.cuda.current_stream(dev)
     else:
         _on_stream(stream, dx, dz, dres, dw, dw2, workspace)
-    if x.numel() == 0:   # no rows: sums of nothing
-        with torch.cuda.stream(stream):
-            for t in (dw, dw2):
-                if t is not None:
-                    t.zero_()
-        return dx, dw, dz, dres, dw2
     st = [KdaStride(0, 0, 0) if t is None else KdaStride(*_rows4(t).stride()[:3]) for t in (dx, dz, dres)]
     grads = KdaNormGrads(_at(dx), _at(dz), _at(dres), _at(dw), _at(dw2), *st)
     ref = lambda t: None if t is None else ctypes.byref(t)  # noqa: E731
