@@ -322,34 +322,30 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
 // fp32 inputs: the same sums with 4 wavefronts, one token tile and all channels each; a lane's operands come
 // straight from memory, since three 64-row tiles and a state in fp32 would not fit LDS beside K and Q.
 template <int DK, int DV>
-__global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
+__global__ __launch_bounds__(512) void gdr_grad_f32_kernel(GdrParams p) {
   using T = float;
   using In = Frags<float>::In;
   using Op = float8v;
-  constexpr int KV = DV / 32, MT = DK / 16;
+  constexpr int KV = DV / 32, MH = DK / 32;   // MH: channel tiles of a wavefront
   constexpr int kOpFrag = op_frag<T, 2>();
-  __shared__ __attribute__((aligned(16))) char tri[4][4 * kOpFrag];   // a wavefront's dP and dA, two steps each
+  __shared__ __attribute__((aligned(16))) char tri[4][4 * kOpFrag];   // a token tile's dP and dA, two steps each
   __shared__ __attribute__((aligned(16))) Rows<T, DK> kl, ql;
   __shared__ float ghi[64], glo[64], bet[64];
-  __shared__ double dG[64];
-  __shared__ double extra[4];
+  __shared__ double dG[2][64], extra[8];
 
   GdrSeq seq;
   int64_t chunk;
   const int64_t slot = blockIdx.x;
   if (!gdr_find(p, slot, &seq, &chunk)) return;
   const int kh = blockIdx.y, grp = p.Hv / p.Hk;
-  const int lane = threadIdx.x & 63, wave = wave_id(), li = lane & 15, g = lane >> 4;
+  int lane = threadIdx.x & 63;
+  const int wave = wave_id() & 3, half = wave_id() >> 2;   // token tile; half of the channels
   const int64_t t0 = seq.t0 + chunk * kGdrChunk, left = seq.len - chunk * kGdrChunk;
   const int n = left < kGdrChunk ? (int)left : kGdrChunk;
-  const int tok = 16 * wave + li;                 // this lane's token
-  const bool live = tok < n;
   char* dp_f = tri[wave];                         // dP (transposed, then as it is)
   char* da_f = tri[wave] + 2 * kOpFrag;
 
-  const auto qrow = global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (t0 + tok) * p.sq.t + 4 * g;
-  const auto krow = global_in<T>(p.k) + seq.row * p.sk.b + kh * p.sk.h + (t0 + tok) * p.sk.t + 4 * g;
-  for (int i = threadIdx.x; i < 64 * DK / 8; i += 256) {   // K and Q, zeros behind the sequence's end
+  for (int i = threadIdx.x; i < 64 * DK / 8; i += 512) {   // K and Q, zeros behind the sequence's end
     const int r = i / (DK / 8), c0 = i % (DK / 8) * 8;
     In a, b;
     zero_frag(a);
@@ -362,15 +358,17 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
     ql.put8(r, c0, b);
   }
 
-  floatx4 dq[MT], dk[MT];
+  floatx4 dq[MH], dk[MH];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) dq[m] = dk[m] = floatx4{};
+  for (int m = 0; m < MH; ++m) dq[m] = dk[m] = floatx4{};
 
   for (int hg = 0; hg < grp; ++hg) {
+    asm volatile("" : "+v"(lane));   // said anew for every head, as above
+    const int li = lane & 15, g = lane >> 4, tok = 16 * wave + li;   // tok: this lane's token
     const int h = kh * grp + hg;
     const int64_t blk = slot * p.Hv + h;
     const auto gate = global_in<float>(p.ws_gate) + blk * kGateFloats;
-    if (wave == 0) {
+    if (wave_id() == 0) {
       ghi[lane] = gate[kGateHi + lane];
       glo[lane] = gate[kGateLo + lane];
       bet[lane] = gate[kGateBeta + lane];
@@ -383,10 +381,11 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
     const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t + 8 * g;
     auto f_frag = [&](int tile, int kv) { return load_row8(F + (int64_t)(16 * tile + li) * DV + 32 * kv); };
     auto rows_of = [&](GlobalPtr<const T> base, int64_t st, int tile, int kv) {
-      In x;
-      zero_frag(x);
-      if (16 * tile + li < n) x = load_row8(base + (int64_t)(16 * tile + li) * st + 32 * kv);
-      return x;
+      const int r = 16 * tile + li;   // rows behind the end: the last one's, as zeros
+      const In x = load_row8(base + (int64_t)min(r, n - 1) * st + 32 * kv);
+      In zero;
+      zero_frag(zero);
+      return r < n ? x : zero;
     };
     In fo[KV], oo[KV], eo[KV];   // this wavefront's own tokens
 #pragma unroll
@@ -398,17 +397,21 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
     __syncthreads();
     const float ghr = ghi[tok], glr = glo[tok], br = bet[tok];
 
-    // rows: dP_rj and dA_rj of this wavefront's r over all j <= r, as B operands over j
+    // rows: dP_rj and dA_rj of this tile's r over all j <= r, as B operands over j; every other tile of j
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int mm = 0; mm < 2; ++mm) {
+      const int m = 2 * mm + half;
       if (m > (wave | 1)) continue;
       floatx4 a = {}, b = {};
       if (m <= wave) {
+        In f[KV];
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv) f[kv] = f_frag(m, kv);
+        __builtin_amdgcn_sched_barrier(0);   // a tile's loads go out together: one by one, each takes a trip to memory
 #pragma unroll
         for (int kv = 0; kv < KV; ++kv) {
-          const In f = f_frag(m, kv);
-          a = mma(f, oo[kv], a);
-          b = mma(f, eo[kv], b);
+          a = mma(f[kv], oo[kv], a);
+          b = mma(f[kv], eo[kv], b);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -418,23 +421,29 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
           b[r] = tok > j ? -d * b[r] : 0.f;
         }
       }
-      put_op<2>(dp_f + (m >> 1) * kOpFrag, m & 1, li, g, a, T{});
-      put_op<2>(da_f + (m >> 1) * kOpFrag, m & 1, li, g, b, T{});
+      put_op<2>(dp_f + mm * kOpFrag, half, li, g, a, T{});
+      put_op<2>(da_f + mm * kOpFrag, half, li, g, b, T{});
     }
-    compiler_fence();
+    __syncthreads();
     double dg = 0.0, write = 0.0, hold = 0.0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int i = 0; i < MH; ++i) {
+      const int m = half * MH + i;
       floatx4 a = {}, b = {};
       float ss = 0.f;
+      In st[KV], dst[KV];
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
-        const In st = load_row8(St + (int64_t)(16 * m + li) * DV + 32 * kv);
-        const In dst = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
+        st[kv] = load_row8(St + (int64_t)(16 * m + li) * DV + 32 * kv);
+        dst[kv] = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += (float)st[e] * (float)dst[e];
-        a = mma(st, oo[kv], a);
-        b = mma(st, eo[kv], b);
+      for (int kv = 0; kv < KV; ++kv) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += (float)st[kv][e] * (float)dst[kv][e];
+        a = mma(st[kv], oo[kv], a);
+        b = mma(st[kv], eo[kv], b);
       }
       asm volatile("" : "+v"(ss));   // now: put off to the end, it would keep every row of S and dS till then
       hold += (m & 3) == wave ? ss : 0.f;   // <S, dS>: every row tile once
@@ -449,26 +458,32 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
       }
       settle(a);
       settle(b);
-      dq[m] += a;
-      dk[m] += b;
-      if (live) {
-        const floatx4 q4 = load_row4(qrow + 16 * m), k4 = load_row4(krow + 16 * m);
+      dq[i] += a;
+      dk[i] += b;
+      const floatx4 q4 = ld4f(ql.x + tok * ql.kLd + 16 * m + 4 * g), k4 = ld4f(kl.x + tok * kl.kLd + 16 * m + 4 * g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dg += (double)q4[r] * (double)a[r] + (double)k4[r] * (double)b[r];
-      }
+      for (int r = 0; r < 4; ++r) dg += (double)q4[r] * (double)a[r] + (double)k4[r] * (double)b[r];
     }
-    compiler_fence();
+    __syncthreads();
 
-    // columns: dP_rj and dA_rj of this wavefront's j over all r >= j, as B operands over r
+    // columns: dP_rj and dA_rj of this tile's j over all r >= j, as B operands over r
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int mm = 0; mm < 2; ++mm) {
+      const int m = 2 * mm + half;
       if (m < (wave & 2)) continue;
       floatx4 a = {}, b = {};
       if (m >= wave) {
+        In od[KV], ed[KV];
 #pragma unroll
         for (int kv = 0; kv < KV; ++kv) {
-          a = mma(rows_of(dO, p.sdo.t, m, kv), fo[kv], a);
-          b = mma(rows_of(dE, p.sdv.t, m, kv), fo[kv], b);
+          od[kv] = rows_of(dO, p.sdo.t, m, kv);
+          ed[kv] = rows_of(dE, p.sdv.t, m, kv);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kv = 0; kv < KV; ++kv) {
+          a = mma(od[kv], fo[kv], a);
+          b = mma(ed[kv], fo[kv], b);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -478,18 +493,22 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
           b[r] = i > tok ? -d * b[r] : 0.f;
         }
       }
-      put_op<2>(dp_f + (m >> 1) * kOpFrag, m & 1, li, g, a, T{});
-      put_op<2>(da_f + (m >> 1) * kOpFrag, m & 1, li, g, b, T{});
+      put_op<2>(dp_f + mm * kOpFrag, half, li, g, a, T{});
+      put_op<2>(da_f + mm * kOpFrag, half, li, g, b, T{});
     }
-    compiler_fence();
+    __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int i = 0; i < MH; ++i) {
+      const int m = half * MH + i;
       floatx4 a = {};
+      In dst[KV];
 #pragma unroll
-      for (int kv = 0; kv < KV; ++kv) a = mma(load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv), fo[kv], a);
+      for (int kv = 0; kv < KV; ++kv) dst[kv] = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) a = mma(dst[kv], fo[kv], a);
       a *= eta * br;
-      floatx4 k4 = {};
-      if (live) k4 = load_row4(krow + 16 * m);
+      const floatx4 k4 = ld4f(kl.x + tok * kl.kLd + 16 * m + 4 * g);
 #pragma unroll
       for (int r = 0; r < 4; ++r) write += (double)k4[r] * (double)a[r];
 #pragma unroll
@@ -499,7 +518,7 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
         a = mma(ql.transposed(m, ks, lane), load_frag<Op>(dp_f + ks * kOpFrag, lane), a);
       }
       settle(a);
-      dk[m] += a;
+      dk[i] += a;
 #pragma unroll
       for (int r = 0; r < 4; ++r) dg -= (double)k4[r] * (double)a[r];
     }
@@ -509,12 +528,15 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
     double ex = write + (double)last * hold;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) ex += __shfl_xor(ex, d);
-    if (g == 0) dG[tok] = dg;
-    if (lane == 0) extra[wave] = ex;
+    if (g == 0) dG[half][tok] = dg;
+    if (lane == 0) extra[wave_id()] = ex;
     __syncthreads();
-    if (wave == 0) {
-      double x = dG[lane];
-      if (lane == 63) x += extra[0] + extra[1] + extra[2] + extra[3];
+    if (wave_id() == 0) {
+      double x = dG[0][lane] + dG[1][lane];
+      if (lane == 63) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x += extra[i];
+      }
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const double dn = __shfl_down(x, d);
@@ -534,13 +556,15 @@ __global__ __launch_bounds__(256, 1) void gdr_grad_f32_kernel(GdrParams p) {
     __syncthreads();
   }
 
-  if (live) {
+  const int tok = 16 * wave + (lane & 15), g = lane >> 4;
+  if (tok < n) {
     const auto dqp = global_out<T>(p.dq) + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + tok) * p.sdq.t + 4 * g;
     const auto dkp = global_out<T>(p.dk_) + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + tok) * p.sdk.t + 4 * g;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      store_row4(dqp + 16 * m, dq[m]);
-      store_row4(dkp + 16 * m, dk[m]);
+    for (int i = 0; i < MH; ++i) {
+      const int m = half * MH + i;
+      store_row4(dqp + 16 * m, dq[i]);
+      store_row4(dkp + 16 * m, dk[i]);
     }
   }
 }
@@ -550,7 +574,7 @@ hipError_t launch_one(const GdrParams& p, hipStream_t s) {
   const dim3 grid((unsigned)gdr_slots(p.B, p.T, p.n_seq, p.seq_start != nullptr), (unsigned)p.Hk);
   if (grid.x == 0) return hipSuccess;
   if (p.dtype == KDA_DTYPE_BF16) hipLaunchKernelGGL((gdr_grad_kernel<DK, DV>), grid, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((gdr_grad_f32_kernel<DK, DV>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((gdr_grad_f32_kernel<DK, DV>), grid, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
