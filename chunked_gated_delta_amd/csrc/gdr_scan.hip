@@ -452,7 +452,6 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       };
       auto turn_k = [&]() {
         kl.leave(kr.v, 16 * wave, lane);
-        load_k();
         compiler_fence();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) kf[ks] = kl.row_frag(wave, ks, lane);
@@ -466,6 +465,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       };
       auto step = [&](int64_t c, int n) {
         const Gates& gt = gate[c & 3];
+        load_k();
         Op3 sb[KS];
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) sb[ks] = load_frag<Op3>((const char*)sf + ks * kOp3, lane);
@@ -534,7 +534,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     float gx = 0.f;
     Op3 pm[TS];
     RowLoads<T, DK> qr(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (seq.t0 + (nc - 1) * kGdrChunk) * p.sq.t, wave, lane, last_rows, p.sq.t);
-    int64_t at = nc - 1, pat = nc - 1;   // the chunk that is fetched next, and whose P and Q are loaded next
+    int64_t at = nc - 1, pat = nc - 1, qat = nc - 1;   // the chunk that is fetched next, and whose P and Q are loaded next
     auto dop = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + (seq.t0 + at * kGdrChunk) * p.sdo.t + 16 * part;
     auto gp = global_in<float>(p.ws_gate) + (blk0 + at * p.Hv) * kGateFloats + (wave < 3 ? wave : 0) * 64;
     auto pp = as_global((const char*)p.ws_p) + ((blk0 + at * p.Hv) * kTriFrags + upper_frag(wave, TS == 2 ? 0 : 1)) * kOp3;
@@ -561,13 +561,17 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       if (wave < 2) ot.put_row(tid, ox);
       if (wave < 3) (wave == 0 ? gate[c & 3].gam : wave == 1 ? gate[c & 3].eta : gate[c & 3].beta)[lane] = gx;
     };
-    auto load_pq = [&]() {
+    auto load_p = [&]() {
 #pragma unroll
       for (int ks = 0; ks < TS; ++ks) pm[ks] = load_frag<Op3>(pp + ks * kOp3, lane);
-      qr.load(pat == nc - 1);
       const int64_t more = mask_of(pat > 0);
       pat -= more & 1;
       pp -= more & (int64_t)(p.Hv * (kTriFrags * kOp3));
+    };
+    auto load_q = [&]() {
+      qr.load(qat == nc - 1);
+      const int64_t more = mask_of(qat > 0);
+      qat -= more & 1;
       qr.from -= more & (int64_t)(kGdrChunk * p.sq.t);
     };
     auto load_f = [&](int64_t c) {
@@ -578,6 +582,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       const int n = c == nc - 1 ? last_rows : kGdrChunk;
       const floatx4 gam = p.scale * ld4f((const float*)gate[c & 3].gam + r0);
       ql.leave(qr.v, 16 * wave, lane);
+      load_q();
       floatx4 x = ot.tile(li, r0);
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] = r0 + r < n ? x[r] : 0.f;
@@ -631,7 +636,8 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     };
     if (nc > 0) {
       fetch();
-      load_pq();
+      load_p();
+      load_q();
       load_f(nc - 1);
       leave(nc - 1);
       fetch();
@@ -642,7 +648,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     if (nc > 0) {
       products();
       leave_products();
-      load_pq();
+      load_p();
       leave(nc - 2);
       fetch();
     }
@@ -657,7 +663,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       block_barrier();
       if (c > 0) {
         leave_products();
-        load_pq();
+        load_p();
       }
       finish(c);
       load_f(c - 1);
