@@ -30,16 +30,19 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
   constexpr int kTok = 64 * kRow8 / 512 ? 64 * kRow8 / 512 : 1;   // pieces a thread moves of 64 rows,
   constexpr int kSt = DK * kRow8 / 512 ? DK * kRow8 / 512 : 1;    // of DK rows,
   constexpr int kCh = 64 * (DK / 8) / 512 ? 64 * (DK / 8) / 512 : 1;   // and of K or Q
-  constexpr int kTri = 4 * 8 * kOp, kXBytes = 3 * 64 * kLd * 2 > kTri ? 3 * 64 * kLd * 2 : kTri;
-  // F, dO and dE; then the triangular factors: per token tile 2 steps of dP and dA over j, 2 of each over r
+  constexpr int kTri = 4 * 8 * kOp, kXBytes = 5 * 64 * kLd * 2 > kTri ? 5 * 64 * kLd * 2 : kTri;
+  // F, dO and dE (F and dE in two planes); then the triangular factors: per token tile 2 steps of dP and dA over j,
+  // 2 of each over r
   __shared__ __attribute__((aligned(16))) char xs[kXBytes];
-  __shared__ __attribute__((aligned(16))) T sl[DK * kLd];  // S, then dS
+  __shared__ __attribute__((aligned(16))) T sl[DK * kLd];  // a plane of S, then of dS
   __shared__ __attribute__((aligned(16))) Rows<T, DK> kl, ql;
   __shared__ float ghi[64], glo[64], bet[64];
   __shared__ double dG[2][64], extra[8];
   T* fl = reinterpret_cast<T*>(xs);
-  T* ol = fl + 64 * kLd;
+  T* f2l = fl + 64 * kLd;
+  T* ol = f2l + 64 * kLd;
   T* el = ol + 64 * kLd;
+  T* e2l = el + 64 * kLd;
 
   GdrSeq seq;
   int64_t chunk;
@@ -65,30 +68,37 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     const int h = kh * grp + hg;
     const int64_t blk = slot * p.Hv + h;
     const auto gate = global_in<float>(p.ws_gate) + blk * kGateFloats;
-    const auto F = global_in<T>(p.ws_f) + blk * kGdrChunk * DV;
-    const auto St = global_in<T>(p.ws_s) + blk * DK * DV;
-    const auto dSt = global_in<T>(p.ws_ds) + blk * DK * DV;
+    const auto F = global_in<T>(p.ws_f) + blk * 2 * kGdrChunk * DV;
+    const auto E2 = global_in<T>(p.ws_e) + blk * kGdrChunk * DV;
+    const auto St = global_in<T>(p.ws_s) + blk * 2 * DK * DV;
+    const auto dSt = global_in<T>(p.ws_ds) + blk * 2 * DK * DV;
     const auto dO = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t;
     const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t;
     // everything is asked for at once
-    bf16x8 fx[kTok], ox[kTok], ex[kTok], sx[kSt], dx[kSt], kx[kCh], qx[kCh];
+    bf16x8 fx[kTok], f2[kTok], ox[kTok], ex[kTok], e2[kTok], sx[kSt], s2[kSt], dx[kSt], d2[kSt], kx[kCh], qx[kCh];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const int at = tid + 512 * i, r = at / kRow8, c0 = at % kRow8 * 8;
-      fx[i] = ox[i] = ex[i] = bf16x8{};
-      if (at < 64 * kRow8) fx[i] = load_row8(F + at * 8);
+      fx[i] = f2[i] = ox[i] = ex[i] = e2[i] = bf16x8{};
+      if (at < 64 * kRow8) {
+        fx[i] = load_row8(F + at * 8);
+        f2[i] = load_row8(F + kGdrChunk * DV + at * 8);
+      }
       if (r < n && at < 64 * kRow8) {
         ox[i] = load_row8(dO + r * p.sdo.t + c0);
         ex[i] = load_row8(dE + r * p.sdv.t + c0);
+        e2[i] = load_row8(E2 + at * 8);
       }
     }
 #pragma unroll
     for (int i = 0; i < kSt; ++i) {
       const int at = tid + 512 * i;
-      sx[i] = dx[i] = bf16x8{};
+      sx[i] = s2[i] = dx[i] = d2[i] = bf16x8{};
       if (at < DK * kRow8) {
         sx[i] = load_row8(St + at * 8);
+        s2[i] = load_row8(St + DK * DV + at * 8);
         dx[i] = load_row8(dSt + at * 8);
+        d2[i] = load_row8(dSt + DK * DV + at * 8);
       }
     }
     if (hg == 0) {   // K and Q, zeros behind the sequence's end
@@ -122,13 +132,18 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
       const int at = tid + 512 * i;
       if (at < 64 * kRow8) {
         *at_row(fl, at) = fx[i];
+        *at_row(f2l, at) = f2[i];
         *at_row(ol, at) = ox[i];
         *at_row(el, at) = ex[i];
+        *at_row(e2l, at) = e2[i];
       }
     }
+    auto put_plane = [&](const bf16x8 (&x)[kSt]) {
 #pragma unroll
-    for (int i = 0; i < kSt; ++i)
-      if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = sx[i];
+      for (int i = 0; i < kSt; ++i)
+        if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = x[i];
+    };
+    put_plane(sx);
     if (hg == 0) {
 #pragma unroll
       for (int i = 0; i < kCh; ++i) {
@@ -142,16 +157,71 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     __syncthreads();
 
     auto rows = [&](const T* base, int t, int kv) { return load_row8(base + (16 * t + li) * kLd + 32 * kv + 8 * g); };
-    bf16x8 fo[KV], oo[KV], eo[KV];   // this wavefront's own tokens
+    // this wavefront's own tokens
+    auto own = [&](const T* base, bf16x8 (&x)[KV]) {
 #pragma unroll
-    for (int kv = 0; kv < KV; ++kv) {
-      fo[kv] = rows(fl, tile, kv);
-      oo[kv] = rows(ol, tile, kv);
-      eo[kv] = rows(el, tile, kv);
+      for (int kv = 0; kv < KV; ++kv) x[kv] = rows(base, tile, kv);
+    };
+    bf16x8 fo[KV], fo2[KV], oo[KV], eo[KV], eo2[KV];
+    own(ol, oo);
+    own(el, eo);
+    own(e2l, eo2);
+    double dg = 0.0, write = 0.0, hold = 0.0;
+    // <S, dS>: this thread's pieces of both
+#pragma unroll
+    for (int i = 0; i < kSt; ++i) {
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x += ((float)sx[i][e] + (float)s2[i][e]) * ((float)dx[i][e] + (float)d2[i][e]);
+      hold += x;
     }
+    // S dO, S dE and dS U of this wavefront's channels, a plane of the states at a time
+    floatx4 a[MH], b[MH], c[MH];
+#pragma unroll
+    for (int mm = 0; mm < MH; ++mm) {
+      a[mm] = b[mm] = c[mm] = floatx4{};
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) {
+        const bf16x8 st = rows(sl, half * MH + mm, kv);
+        a[mm] = mma(st, oo[kv], a[mm]);
+        b[mm] = mma(st, eo2[kv], b[mm]);
+        b[mm] = mma(st, eo[kv], b[mm]);
+      }
+    }
+    __syncthreads();
+    put_plane(s2);
+    __syncthreads();
+#pragma unroll
+    for (int mm = 0; mm < MH; ++mm)
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) {
+        const bf16x8 st = rows(sl, half * MH + mm, kv);
+        a[mm] = mma(st, oo[kv], a[mm]);
+        b[mm] = mma(st, eo[kv], b[mm]);
+      }
+    own(fl, fo);
+    own(f2l, fo2);
+    __syncthreads();
+    put_plane(dx);
+    __syncthreads();
+#pragma unroll
+    for (int mm = 0; mm < MH; ++mm)
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) {
+        const bf16x8 st = rows(sl, half * MH + mm, kv);
+        c[mm] = mma(st, fo2[kv], c[mm]);
+        c[mm] = mma(st, fo[kv], c[mm]);
+      }
+    __syncthreads();
+    put_plane(d2);
+    __syncthreads();
+#pragma unroll
+    for (int mm = 0; mm < MH; ++mm)
+#pragma unroll
+      for (int kv = 0; kv < KV; ++kv) c[mm] = mma(rows(sl, half * MH + mm, kv), fo[kv], c[mm]);
     // dP and dA: half 0 over all j <= its tokens r (transposed), half 1 over all r >= its tokens j; tiles that
     // hold none of it stay zeros
-    const float ghr = ghi[tok], glr = glo[tok], br = bet[tok];
+    const float ghr = ghi[tok], glr = glo[tok], own_beta = bet[tok];
     floatx4 a4[4], b4[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) a4[m] = b4[m] = floatx4{};
@@ -161,8 +231,11 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         if (m > tile) break;
 #pragma unroll
         for (int kv = 0; kv < KV; ++kv) {
-          const bf16x8 x = rows(fl, m, kv);
+          const bf16x8 x = rows(fl, m, kv), x2 = rows(f2l, m, kv);
+          a4[m] = mma(x2, oo[kv], a4[m]);
+          b4[m] = mma(x2, eo[kv], b4[m]);
           a4[m] = mma(x, oo[kv], a4[m]);
+          b4[m] = mma(x, eo2[kv], b4[m]);
           b4[m] = mma(x, eo[kv], b4[m]);
         }
       }
@@ -172,8 +245,12 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         if (m < tile) break;
 #pragma unroll
         for (int kv = 0; kv < KV; ++kv) {
-          a4[m] = mma(rows(ol, m, kv), fo[kv], a4[m]);
-          b4[m] = mma(rows(el, m, kv), fo[kv], b4[m]);
+          const bf16x8 x = rows(ol, m, kv), y = rows(el, m, kv), y2 = rows(e2l, m, kv);
+          a4[m] = mma(x, fo2[kv], a4[m]);
+          b4[m] = mma(y, fo2[kv], b4[m]);
+          a4[m] = mma(x, fo[kv], a4[m]);
+          b4[m] = mma(y2, fo[kv], b4[m]);
+          b4[m] = mma(y, fo[kv], b4[m]);
         }
       }
     }
@@ -190,7 +267,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         const int o = 16 * m + 4 * g + r;                   // j of the row tok, or r of the column tok
         const float d = half == 0 ? (ghr - ghi[o]) + (glr - glo[o]) : (ghi[o] - ghr) + (glo[o] - glr);
         const bool in = half == 0 ? tok >= o : o >= tok;
-        const float w = in ? (half == 0 ? bet[o] : br) * expf(in ? d : 0.f) : 0.f;
+        const float w = in ? (half == 0 ? bet[o] : own_beta) * expf(in ? d : 0.f) : 0.f;
         a4[m][r] = in ? p.scale * w * a4[m][r] : 0.f;
         b4[m][r] = in && tok != o ? -w * b4[m][r] : 0.f;
       }
@@ -199,20 +276,8 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     }
     __syncthreads();
 
-    double dg = 0.0, write = 0.0, hold = 0.0;
-    // <S, dS>: this thread's pieces of both
-#pragma unroll
-    for (int i = 0; i < kSt; ++i) {
-      if (tid + 512 * i < DK * kRow8) {
-        const bf16x8 sv = *at_row(sl, tid + 512 * i);
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x += (float)sv[e] * (float)dx[i][e];
-        hold += x;
-      }
-    }
-    // from the entering state, and over j <= r
-    {
+    const float br = bet[tok];
+    {   // over j <= r
       Planes<2> pr[2], ar[2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
@@ -222,33 +287,17 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
 #pragma unroll
       for (int mm = 0; mm < MH; ++mm) {
         const int m = half * MH + mm;
-        floatx4 a = {}, b = {};
-#pragma unroll
-        for (int kv = 0; kv < KV; ++kv) {
-          const bf16x8 st = rows(sl, m, kv);
-          a = mma(st, oo[kv], a);
-          b = mma(st, eo[kv], b);
-        }
-        a *= gam * p.scale;
-        b *= -gam;
         const bf16x8 kt[2] = {kl.transposed(m, 0, lane), kl.transposed(m, 1, lane)};
-        a = mma_steps(kt, pr, a);
-        b = mma_steps(kt, ar, b);
-        dq[mm] += a;
-        dk[mm] += b;
+        const floatx4 x = mma_steps(kt, pr, a[mm] * (gam * p.scale)), y = mma_steps(kt, ar, b[mm] * -gam);
+        dq[mm] += x;
+        dk[mm] += y;
         const u32x2v q2 = *reinterpret_cast<const u32x2v*>(ql.x + tok * ql.kLd + 16 * m + 4 * g);
         const u32x2v k2 = *reinterpret_cast<const u32x2v*>(kl.x + tok * kl.kLd + 16 * m + 4 * g);
-        dg += (double)lo_bf16(q2[0]) * a[0] + (double)hi_bf16(q2[0]) * a[1] + (double)lo_bf16(q2[1]) * a[2] + (double)hi_bf16(q2[1]) * a[3];
-        dg += (double)lo_bf16(k2[0]) * b[0] + (double)hi_bf16(k2[0]) * b[1] + (double)lo_bf16(k2[1]) * b[2] + (double)hi_bf16(k2[1]) * b[3];
+        dg += (double)lo_bf16(q2[0]) * x[0] + (double)hi_bf16(q2[0]) * x[1] + (double)lo_bf16(q2[1]) * x[2] + (double)hi_bf16(q2[1]) * x[3];
+        dg += (double)lo_bf16(k2[0]) * y[0] + (double)hi_bf16(k2[0]) * y[1] + (double)lo_bf16(k2[1]) * y[2] + (double)hi_bf16(k2[1]) * y[3];
       }
     }
-    __syncthreads();   // S is used
-#pragma unroll
-    for (int i = 0; i < kSt; ++i)
-      if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = dx[i];
-    __syncthreads();
-    // to the leaving state, and over r >= j
-    {
+    {   // over r >= j
       Planes<2> pc[2], ac[2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
@@ -258,21 +307,18 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
 #pragma unroll
       for (int mm = 0; mm < MH; ++mm) {
         const int m = half * MH + mm;
-        floatx4 a = {};
-#pragma unroll
-        for (int kv = 0; kv < KV; ++kv) a = mma(rows(sl, m, kv), fo[kv], a);
-        a *= eta * br;
+        floatx4 x = c[mm] * (eta * br);
         const u32x2v k2 = *reinterpret_cast<const u32x2v*>(kl.x + tok * kl.kLd + 16 * m + 4 * g);
         const floatx4 k4 = {lo_bf16(k2[0]), hi_bf16(k2[0]), lo_bf16(k2[1]), hi_bf16(k2[1])};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) write += (double)k4[r] * (double)a[r];
+        for (int r = 0; r < 4; ++r) write += (double)k4[r] * (double)x[r];
         const bf16x8 kt[2] = {kl.transposed(m, 0, lane), kl.transposed(m, 1, lane)};
         const bf16x8 qt[2] = {ql.transposed(m, 0, lane), ql.transposed(m, 1, lane)};
-        a = mma_steps(kt, ac, a);
-        a = mma_steps(qt, pc, a);
-        dk[mm] += a;
+        x = mma_steps(kt, ac, x);
+        x = mma_steps(qt, pc, x);
+        dk[mm] += x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dg -= (double)k4[r] * (double)a[r];
+        for (int r = 0; r < 4; ++r) dg -= (double)k4[r] * (double)x[r];
       }
     }
     // the log-decay's gradient

@@ -137,7 +137,7 @@ int64_t gdr_slots(int64_t B, int64_t T, int64_t n_seq, bool packed) {
 
 size_t gdr_layout(GdrParams& p, void* base, bool bwd) {
   const size_t slots = (size_t)gdr_slots(p.B, p.T, p.n_seq, p.seq_start != nullptr);
-  const size_t e = p.dtype == KDA_DTYPE_BF16 ? 2 : 4, op = (e == 2 ? 3 : 2) * kPlane, in = (e == 2 ? 1 : 2) * kPlane;
+  const size_t e = p.dtype == KDA_DTYPE_BF16 ? 2 : 4, op = (e == 2 ? 3 : 2) * kPlane;
   const size_t vh = slots * p.Hv;
   size_t off = 0;
   auto take = [&](char*& at, size_t bytes) {
@@ -146,12 +146,13 @@ size_t gdr_layout(GdrParams& p, void* base, bool bwd) {
   };
   take(p.ws_gate, vh * kGateFloats * 4);
   take(p.ws_ti, vh * kTriFrags * op);
-  take(p.ws_p, vh * kTriFrags * (bwd ? op : in));
+  take(p.ws_p, vh * kTriFrags * (bwd ? op : 2 * kPlane));
   if (bwd) {
     take(p.ws_tt, vh * kTriFrags * op);
-    take(p.ws_s, vh * p.dk * p.dv * e);
-    take(p.ws_ds, vh * p.dk * p.dv * e);
-    take(p.ws_f, vh * kGdrChunk * p.dv * e);
+    take(p.ws_s, vh * p.dk * p.dv * 4);    // fp32, or two planes of bf16
+    take(p.ws_ds, vh * p.dk * p.dv * 4);
+    take(p.ws_f, vh * kGdrChunk * p.dv * 4);
+    take(p.ws_e, e == 2 ? vh * kGdrChunk * p.dv * 2 : 0);   // the second plane of dv
     take(p.ws_db, vh * (p.dv / 16) * kGdrChunk * 4);
   }
   return off;

@@ -36,7 +36,7 @@ struct GdrParams {
   kda_stride_t sdq, sdk, sdv, sdw, sdb;
   float* dS0;                   // nullable
   // workspace sections, one block per (chunk slot, head); see gdr_layout
-  char *ws_gate, *ws_ti, *ws_tt, *ws_p, *ws_s, *ws_ds, *ws_f, *ws_db;
+  char *ws_gate, *ws_ti, *ws_tt, *ws_p, *ws_s, *ws_ds, *ws_f, *ws_e, *ws_db;
 };
 
 struct GdrStepParams {
@@ -212,6 +212,8 @@ template <> struct Frags<float> {
   static constexpr int planes(int) { return 2; }
 };
 constexpr int kPlane = 64 * 16;   // 16 bytes a lane; an fp32 fragment is two planes (places 0-3 and 4-7)
+// planes of the states and of F that the backward keeps for its gradients (one of fp32)
+template <typename T> constexpr int kKept = sizeof(T) == 2 ? 2 : 1;
 template <typename T> constexpr int in_frag() { return Frags<T>::in_planes * kPlane; }
 template <typename T, int N> constexpr int op_frag() { return Frags<T>::planes(N) * kPlane; }
 
@@ -267,6 +269,17 @@ template <int K> __device__ __forceinline__ floatx4 mma_steps(const float8v (&a)
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[e & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[i][e], c[e & 1], 0, 0, 0);
   return c[0] + c[1];
+}
+// both sides in two planes: the three products above the last plane's size
+template <int K> __device__ __forceinline__ floatx4 mma_steps(const Planes<2> (&a)[K], const Planes<2> (&b)[K], floatx4 acc) {
+  floatx4 c[3] = {acc, floatx4{}, floatx4{}};
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    c[2] = mfma(a[i].p[1], b[i].p[0], c[2]);
+    c[1] = mfma(a[i].p[0], b[i].p[1], c[1]);
+    c[0] = mfma(a[i].p[0], b[i].p[0], c[0]);
+  }
+  return c[0] + (c[1] + c[2]);
 }
 // both sides in three planes: the six products above the last plane's size
 template <int K> __device__ __forceinline__ floatx4 mma_steps(const Planes<3> (&a)[K], const Planes<3> (&b)[K], floatx4 acc) {

@@ -214,11 +214,11 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrParams p) {
       for (int ks = 0; ks < 2; ++ks)
         if (ks >= wave / 2) store_frag(out + upper_frag(wave, ks) * kOpFrag, lane, make_op<3>(cols_frag(mat, wave, ks, li, g), T{}));
     } else {
-      // the outputs' own factor, rounded to the inputs' type: it enters o alone, which is rounded to that type
-      const auto out = as_global(p.ws_p) + blk * kTriFrags * op_frag<T, 1>();
+      // the outputs' own factor, two planes: one, as coarse as o itself, raises o's error from 1.7e-3 to 2.3e-3
+      const auto out = as_global(p.ws_p) + blk * kTriFrags * op_frag<T, 2>();
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * op_frag<T, 1>(), lane, make_op<1>(rows_frag(mat, wave, ks, li, g), T{}));
+        if (ks <= wave / 2) store_frag(out + lower_frag(wave, ks) * op_frag<T, 2>(), lane, make_op<2>(rows_frag(mat, wave, ks, li, g), T{}));
     }
     __syncthreads();
   }

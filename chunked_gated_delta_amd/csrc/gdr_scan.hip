@@ -30,19 +30,22 @@ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? 
 __device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ float value(float x) { return x; }
 
-// Writes `rows` contraction places x 16 columns of B operands (first planes) to row-major memory: a lane
-// takes 8 columns of one place.
+// Writes `rows` contraction places x 16 columns of B operands to row-major memory, bf16 in two planes of `plane`
+// values: a lane takes 8 columns of one place.
 template <typename T>
-__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int ld, int tid) {
+__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int64_t plane, int ld, int tid) {
   for (int i = tid; i < rows * 2; i += 256) {
     const int r = i >> 1, c0 = (i & 1) * 8;
-    const char* fr = frags + (r >> 5) * frag_bytes;
-    T x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(fr, r & 31, c0 + e);
-    typename Frags<T>::In v;
-    __builtin_memcpy(&v, x, sizeof(v));
-    *repoint<typename Frags<T>::In>(out + r * ld + c0) = v;
+    for (int n = 0; n < kKept<T>; ++n) {
+      const char* fr = frags + (r >> 5) * frag_bytes + n * kPlane;
+      T x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(fr, r & 31, c0 + e);
+      typename Frags<T>::In v;
+      __builtin_memcpy(&v, x, sizeof(v));
+      *repoint<typename Frags<T>::In>(out + n * plane + r * ld + c0) = v;
+    }
   }
 }
 
@@ -122,7 +125,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) 
   using Op2 = typename Frags<T>::template Op<2>;
   constexpr int KS = DK / 32;
   constexpr int RT = DK >= 64 ? DK / 64 : 1;      // state row tiles of a wavefront
-  constexpr int kOp1 = op_frag<T, 1>(), kOp2 = op_frag<T, 2>(), kOp3 = op_frag<T, 3>();
+  constexpr int kOp2 = op_frag<T, 2>(), kOp3 = op_frag<T, 3>();
   __shared__ __attribute__((aligned(16))) char sf[KS * kOp3];              // the state, as B operands
   __shared__ __attribute__((aligned(16))) char ef[2 * kOp3];               // E
   __shared__ __attribute__((aligned(16))) char wf[2 * kOp3];               // eta U
@@ -282,23 +285,24 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) 
   }
   if constexpr (STATES) {
     block_barrier();   // the first state, v and gates
-    auto sp = global_out<T>(p.ws_s) + blk0 * p.dk * p.dv + 16 * part;
-    auto fp = global_out<T>(p.ws_f) + blk0 * kGdrChunk * p.dv + 16 * part;
+    const int64_t s_plane = p.dk * p.dv, f_plane = kGdrChunk * p.dv;
+    auto sp = global_out<T>(p.ws_s) + blk0 * kKept<T> * s_plane + 16 * part;
+    auto fp = global_out<T>(p.ws_f) + blk0 * kKept<T> * f_plane + 16 * part;
     for (int64_t c = 0; c < nc; ++c) {
       // F of the chunk before; the state that enters this one; what the chain needs of the next
       if (c > 0) {
-        write_rows<T>(uf, kOp2, kGdrChunk, fp, p.dv, tid);
-        fp += p.Hv * (kGdrChunk * p.dv);
+        write_rows<T>(uf, kOp2, kGdrChunk, fp, f_plane, p.dv, tid);
+        fp += p.Hv * kKept<T> * f_plane;
       }
       block_barrier();
-      write_rows<T>(sf, kOp3, DK, sp, p.dv, tid);
-      sp += p.Hv * (p.dk * p.dv);
+      write_rows<T>(sf, kOp3, DK, sp, s_plane, p.dv, tid);
+      sp += p.Hv * kKept<T> * s_plane;
       block_barrier();
       leave(c + 1);
       fetch();
       block_barrier();
     }
-    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp, p.dv, tid);
+    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp, f_plane, p.dv, tid);
   } else {
     auto op = global_out<T>(p.o) + seq.row * p.so.b + h * p.so.h + seq.t0 * p.so.t + 16 * part;
     const uint32_t orow = (uint32_t)(((tid >> 1) * p.so.t + 8 * (tid & 1)) * sizeof(T));
@@ -309,9 +313,10 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) 
     auto walk = [&](auto both) {
       constexpr int TS = decltype(both)::value ? 2 : 1;
       RowLoads<T, DK> qr(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + seq.t0 * p.sq.t, wave, lane, last_rows, p.sq.t);
-      auto pp = as_global((const char*)p.ws_p) + blk0 * kTriFrags * kOp1 + lower_frag(wave, 0) * kOp1;
+      auto pp = as_global((const char*)p.ws_p) + blk0 * kTriFrags * kOp2 + lower_frag(wave, 0) * kOp2;
       int64_t q_at = 0, p_at = 0;
-      In qf[KS], pm[TS];
+      In qf[KS];
+      Op2 pm[TS];
       auto load_q = [&]() {
         qr.load(q_at == nc - 1);
         const int64_t more = mask_of(q_at < nc - 1);
@@ -327,13 +332,13 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) 
       };
       auto load_p = [&]() {
 #pragma unroll
-        for (int ks = 0; ks < TS; ++ks) pm[ks] = load_frag<In>(pp + ks * kOp1, lane);
+        for (int ks = 0; ks < TS; ++ks) pm[ks] = load_frag<Op2>(pp + ks * kOp2, lane);
         const int64_t more = mask_of(p_at < nc - 1);
         p_at += more & 1;
-        pp += more & (int64_t)(p.Hv * (kTriFrags * kOp1));
+        pp += more & (int64_t)(p.Hv * (kTriFrags * kOp2));
       };
       floatx4 O = {};
-      // the outputs of a chunk whose U the chain has left; two planes of U and of the state, as o is rounded to
+      // the outputs of a chunk whose U the chain has left; two planes of P, U and the state, as o is rounded to
       // the inputs' type
       auto add_own = [&]() {
         Op2 ub[TS];
@@ -530,7 +535,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
   auto serve = [&](auto both) {
     constexpr int TS = decltype(both)::value ? 2 : 1;
     const int tid = threadIdx.x & 255;
-    In ox, fx;
+    In ox, fx, f2;
     float gx = 0.f;
     Op3 pm[TS];
     RowLoads<T, DK> qr(global_in<T>(p.q) + seq.row * p.sq.b + kh * p.sq.h + (seq.t0 + (nc - 1) * kGdrChunk) * p.sq.t, wave, lane, last_rows, p.sq.t);
@@ -539,8 +544,10 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     auto gp = global_in<float>(p.ws_gate) + (blk0 + at * p.Hv) * kGateFloats + (wave < 3 ? wave : 0) * 64;
     auto pp = as_global((const char*)p.ws_p) + ((blk0 + at * p.Hv) * kTriFrags + upper_frag(wave, TS == 2 ? 0 : 1)) * kOp3;
     // of the chunk the chain is at
-    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kGdrChunk * p.dv + 16 * part;
-    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * p.dk * p.dv + 16 * part;
+    const int64_t s_plane = p.dk * p.dv, f_plane = kGdrChunk * p.dv;
+    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kKept<T> * f_plane + 16 * part;
+    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * kKept<T> * s_plane + 16 * part;
+    auto ep = global_out<T>(p.ws_e) + (blk0 + at * p.Hv) * f_plane + 16 * part;
     auto dvp = global_out<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + at * kGdrChunk) * p.sdv.t + 16 * part;
     auto dbp = global_out<float>(p.ws_db) + ((blk0 + at * p.Hv) * (p.dv / 16) + part) * kGdrChunk;
     // wavefronts 4 and 5 move dO, wavefronts 6 and 7 F, dU and the gradients that are made of them: a lane has
@@ -575,8 +582,11 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
       qr.from -= more & (int64_t)(kGdrChunk * p.sq.t);
     };
     auto load_f = [&](int64_t c) {
-      if (wave >= 2) fx = load_row8(lane_at(fp, frow));
-      fp -= mask_of(c > 0) & (int64_t)(p.Hv * (kGdrChunk * p.dv));
+      if (wave >= 2) {
+        fx = load_row8(lane_at(fp, frow));
+        if constexpr (kKept<T> == 2) f2 = load_row8(lane_at(fp + f_plane, frow));
+      }
+      fp -= mask_of(c > 0) & (int64_t)(p.Hv * kKept<T> * f_plane);
     };
     auto spread = [&](int64_t c) {       // dO of chunk c as operands, and its Q
       const int n = c == nc - 1 ? last_rows : kGdrChunk;
@@ -624,13 +634,24 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
         float x = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x += dU[e] * value(f8[e]);
+        if constexpr (kKept<T> == 2) {
+          T g8[8];
+          __builtin_memcpy(g8, &f2, sizeof(f2));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x += dU[e] * value(g8[e]);
+        }
         x += __shfl_xor(x, 1);
         if ((tid & 1) == 0) *lane_at(dbp, row * 4) = x;
-        if (row < n) {
+        if constexpr (sizeof(T) == 2) {   // dE in two planes, the first of which is the gradient itself
+          const Planes<2> dE = make_op<2>(b * dU, T{});
+          if (row < n) *repoint<bf16x8>(lane_at(dvp, vrow)) = dE.p[0];
+          *repoint<bf16x8>(lane_at(ep, frow)) = dE.p[1];
+        } else if (row < n) {
           store_row4(lane_at(dvp, vrow), b * floatx4{dU[0], dU[1], dU[2], dU[3]});
           store_row4(lane_at(dvp, vrow + 4 * sizeof(T)), b * floatx4{dU[4], dU[5], dU[6], dU[7]});
         }
       }
+      ep -= p.Hv * f_plane;
       dvp -= kGdrChunk * p.sdv.t;
       dbp -= p.Hv * (p.dv / 16 * kGdrChunk);
     };
@@ -655,8 +676,8 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     block_barrier();
     for (int64_t c = nc - 1; c >= 0; --c) {
       // dS at this chunk's end; what the chain needs of the next one
-      write_rows<T>(sf, kOp3, DK, sp, p.dv, tid);
-      sp -= p.Hv * (p.dk * p.dv);
+      write_rows<T>(sf, kOp3, DK, sp, s_plane, p.dv, tid);
+      sp -= p.Hv * kKept<T> * s_plane;
       if (c > 0) spread(c - 1);
       block_barrier();
       if (c > 0) products();
