@@ -15,6 +15,8 @@
 // The second identity gives the log-decay's gradient from the accumulators that are there anyway.  S,
 // dS, F and dE are held in the inputs' type here (their rounding is one of the gradients' own size, half a
 // step of that type); dP and dA take two planes, which keeps the error below 1.5 times the final rounding's.
+#include <type_traits>
+
 #include "gdr_internal.h"
 
 namespace kda {
@@ -29,14 +31,15 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
   constexpr int kRow8 = DV / 8;                            // 16-byte pieces of a row
   constexpr int kTok = 64 * kRow8 / 512 ? 64 * kRow8 / 512 : 1;   // pieces a thread moves of 64 rows,
   constexpr int kSt = DK * kRow8 / 512 ? DK * kRow8 / 512 : 1;    // of DK rows,
-  constexpr int kCh = 64 * (DK / 8) / 512 ? 64 * (DK / 8) / 512 : 1;   // and of K or Q
+  constexpr int kCh = 64 * (DK / 8) / 512 ? 64 * (DK / 8) / 512 : 1;   // and of K or Q,
+  constexpr bool kAllTok = 64 * kRow8 % 512 == 0, kAllSt = DK * kRow8 % 512 == 0, kAllCh = 64 * (DK / 8) % 512 == 0;   // all of them
   constexpr int kTri = 4 * 8 * kOp, kXBytes = 5 * 64 * kLd * 2 > kTri ? 5 * 64 * kLd * 2 : kTri;
   // F, dO and dE (F and dE in two planes); then the triangular factors: per token tile 2 steps of dP and dA over j,
   // 2 of each over r
   __shared__ __attribute__((aligned(16))) char xs[kXBytes];
   __shared__ __attribute__((aligned(16))) T sl[DK * kLd];  // a plane of S, then of dS
   __shared__ __attribute__((aligned(16))) Rows<T, DK> kl, ql;
-  __shared__ float ghi[64], glo[64], bet[64];
+  __shared__ __attribute__((aligned(16))) float ghi[64], glo[64], bet[64];
   __shared__ double dG[2][64], extra[8];
   T* fl = reinterpret_cast<T*>(xs);
   T* f2l = fl + 64 * kLd;
@@ -74,31 +77,22 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     const auto dSt = global_in<T>(p.ws_ds) + blk * 2 * DK * DV;
     const auto dO = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t;
     const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t;
-    // everything is asked for at once
+    // everything is asked for at once, in the order of its use: loads are waited for in the order they were asked
+    const float gates[3] = {gate[kGateHi + lane], gate[kGateLo + lane], gate[kGateBeta + lane]};
+    const float gam = gate[kGateGam + tok], eta = gate[kGateEta + tok], last = gate[kGateLast];
     bf16x8 fx[kTok], f2[kTok], ox[kTok], ex[kTok], e2[kTok], sx[kSt], s2[kSt], dx[kSt], d2[kSt], kx[kCh], qx[kCh];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const int at = tid + 512 * i, r = at / kRow8, c0 = at % kRow8 * 8;
       fx[i] = f2[i] = ox[i] = ex[i] = e2[i] = bf16x8{};
-      if (at < 64 * kRow8) {
+      if (kAllTok || at < 64 * kRow8) {
         fx[i] = load_row8(F + at * 8);
         f2[i] = load_row8(F + kGdrChunk * DV + at * 8);
       }
-      if (r < n && at < 64 * kRow8) {
+      if (r < n && (kAllTok || at < 64 * kRow8)) {
         ox[i] = load_row8(dO + r * p.sdo.t + c0);
         ex[i] = load_row8(dE + r * p.sdv.t + c0);
         e2[i] = load_row8(E2 + at * 8);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kSt; ++i) {
-      const int at = tid + 512 * i;
-      sx[i] = s2[i] = dx[i] = d2[i] = bf16x8{};
-      if (at < DK * kRow8) {
-        sx[i] = load_row8(St + at * 8);
-        s2[i] = load_row8(St + DK * DV + at * 8);
-        dx[i] = load_row8(dSt + at * 8);
-        d2[i] = load_row8(dSt + DK * DV + at * 8);
       }
     }
     if (hg == 0) {   // K and Q, zeros behind the sequence's end
@@ -112,25 +106,32 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         }
       }
     }
-    // what the last wavefront needs at the end: a token a lane
-    constexpr int kParts = DV / 16;
-    float w_last = 0.f, db_last[kParts];
-    if (wave_id() == 7) {
-      if (lane < n) w_last = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
 #pragma unroll
-      for (int c = 0; c < kParts; ++c) db_last[c] = global_in<float>(p.ws_db)[(blk * kParts + c) * kGdrChunk + lane];
+    for (int i = 0; i < kSt; ++i) {
+      const int at = tid + 512 * i;
+      sx[i] = bf16x8{};
+      if (kAllSt || at < DK * kRow8) sx[i] = load_row8(St + at * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kSt; ++i) {
+      const int at = tid + 512 * i;
+      s2[i] = dx[i] = d2[i] = bf16x8{};
+      if (kAllSt || at < DK * kRow8) {
+        s2[i] = load_row8(St + DK * DV + at * 8);
+        dx[i] = load_row8(dSt + at * 8);
+        d2[i] = load_row8(dSt + DK * DV + at * 8);
+      }
     }
     if (tid < 64) {
-      ghi[tid] = gate[kGateHi + tid];
-      glo[tid] = gate[kGateLo + tid];
-      bet[tid] = gate[kGateBeta + tid];
+      ghi[tid] = gates[0];
+      glo[tid] = gates[1];
+      bet[tid] = gates[2];
     }
-    const float gam = gate[kGateGam + tok], eta = gate[kGateEta + tok], last = gate[kGateLast];
     auto at_row = [&](T* base, int at) { return reinterpret_cast<bf16x8*>(base + at / kRow8 * kLd + at % kRow8 * 8); };
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const int at = tid + 512 * i;
-      if (at < 64 * kRow8) {
+      if (kAllTok || at < 64 * kRow8) {
         *at_row(fl, at) = fx[i];
         *at_row(f2l, at) = f2[i];
         *at_row(ol, at) = ox[i];
@@ -141,20 +142,20 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     auto put_plane = [&](const bf16x8 (&x)[kSt]) {
 #pragma unroll
       for (int i = 0; i < kSt; ++i)
-        if (tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = x[i];
+        if (kAllSt || tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = x[i];
     };
     put_plane(sx);
     if (hg == 0) {
 #pragma unroll
       for (int i = 0; i < kCh; ++i) {
         const int at = tid + 512 * i, row = at / (DK / 8), c0 = at % (DK / 8) * 8;
-        if (row < 64) {
+        if (kAllCh || row < 64) {
           kl.put8(row, c0, kx[i]);
           ql.put8(row, c0, qx[i]);
         }
       }
     }
-    __syncthreads();
+    block_barrier();
 
     auto rows = [&](const T* base, int t, int kv) { return load_row8(base + (16 * t + li) * kLd + 32 * kv + 8 * g); };
     // this wavefront's own tokens
@@ -167,14 +168,6 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     own(el, eo);
     own(e2l, eo2);
     double dg = 0.0, write = 0.0, hold = 0.0;
-    // <S, dS>: this thread's pieces of both
-#pragma unroll
-    for (int i = 0; i < kSt; ++i) {
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x += ((float)sx[i][e] + (float)s2[i][e]) * ((float)dx[i][e] + (float)d2[i][e]);
-      hold += x;
-    }
     // S dO, S dE and dS U of this wavefront's channels, a plane of the states at a time
     floatx4 a[MH], b[MH], c[MH];
 #pragma unroll
@@ -188,9 +181,9 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         b[mm] = mma(st, eo[kv], b[mm]);
       }
     }
-    __syncthreads();
+    block_barrier();
     put_plane(s2);
-    __syncthreads();
+    block_barrier();
 #pragma unroll
     for (int mm = 0; mm < MH; ++mm)
 #pragma unroll
@@ -199,11 +192,19 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         a[mm] = mma(st, oo[kv], a[mm]);
         b[mm] = mma(st, eo[kv], b[mm]);
       }
+    block_barrier();
     own(fl, fo);
     own(f2l, fo2);
-    __syncthreads();
+    // <S, dS>: this thread's pieces of both, only now, so that dS may still be on its way
+#pragma unroll
+    for (int i = 0; i < kSt; ++i) {
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x += ((float)sx[i][e] + (float)s2[i][e]) * ((float)dx[i][e] + (float)d2[i][e]);
+      hold += x;
+    }
     put_plane(dx);
-    __syncthreads();
+    block_barrier();
 #pragma unroll
     for (int mm = 0; mm < MH; ++mm)
 #pragma unroll
@@ -212,15 +213,18 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         c[mm] = mma(st, fo2[kv], c[mm]);
         c[mm] = mma(st, fo[kv], c[mm]);
       }
-    __syncthreads();
+    block_barrier();
     put_plane(d2);
-    __syncthreads();
+    block_barrier();
 #pragma unroll
     for (int mm = 0; mm < MH; ++mm)
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) c[mm] = mma(rows(sl, half * MH + mm, kv), fo[kv], c[mm]);
     // dP and dA: half 0 over all j <= its tokens r (transposed), half 1 over all r >= its tokens j; tiles that
     // hold none of it stay zeros
+    own(ol, oo);   // read again: kept, they would not leave dS's pieces room
+    own(el, eo);
+    own(e2l, eo2);
     const float ghr = ghi[tok], glr = glo[tok], own_beta = bet[tok];
     floatx4 a4[4], b4[4];
 #pragma unroll
@@ -259,22 +263,32 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
       settle(a4[m]);
       settle(b4[m]);
     }
-    __syncthreads();   // everyone has read F, dO and dE
+    block_barrier();   // everyone has read F, dO and dE
+    auto factors = [&](auto rows_of_tok) {
+      constexpr bool kRows = decltype(rows_of_tok)::value;   // o is j of the row tok, or r of the column tok
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+      for (int m = 0; m < 4; ++m) {
+        if (kRows ? m <= tile : m >= tile) {
+          const floatx4 oh = ld4f((const float*)ghi + 16 * m + 4 * g), ol4 = ld4f((const float*)glo + 16 * m + 4 * g);
+          const floatx4 ob = ld4f((const float*)bet + 16 * m + 4 * g);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int o = 16 * m + 4 * g + r;                   // j of the row tok, or r of the column tok
-        const float d = half == 0 ? (ghr - ghi[o]) + (glr - glo[o]) : (ghi[o] - ghr) + (glo[o] - glr);
-        const bool in = half == 0 ? tok >= o : o >= tok;
-        const float w = in ? (half == 0 ? bet[o] : own_beta) * expf(in ? d : 0.f) : 0.f;
-        a4[m][r] = in ? p.scale * w * a4[m][r] : 0.f;
-        b4[m][r] = in && tok != o ? -w * b4[m][r] : 0.f;
+          for (int r = 0; r < 4; ++r) {
+            const int o = 16 * m + 4 * g + r;
+            const float d = kRows ? (ghr - oh[r]) + (glr - ol4[r]) : (oh[r] - ghr) + (ol4[r] - glr);
+            const bool in = kRows ? tok >= o : o >= tok;
+            // the fast exponential is off by 2^-23 (1 + |d|): beside two planes' 2^-17 nothing where e^d still counts
+            const float w = (kRows ? ob[r] : own_beta) * __expf(in ? d : 0.f);
+            a4[m][r] = in ? p.scale * w * a4[m][r] : 0.f;
+            b4[m][r] = in && tok != o ? -w * b4[m][r] : 0.f;
+          }
+        }
+        put_op<2>(mine + ((kRows ? 0 : 4) + (m >> 1)) * kOp, m & 1, li, g, a4[m], T{});
+        put_op<2>(mine + ((kRows ? 2 : 6) + (m >> 1)) * kOp, m & 1, li, g, b4[m], T{});
       }
-      put_op<2>(mine + (4 * half + (m >> 1)) * kOp, m & 1, li, g, a4[m], T{});
-      put_op<2>(mine + (4 * half + 2 + (m >> 1)) * kOp, m & 1, li, g, b4[m], T{});
-    }
-    __syncthreads();
+    };
+    if (half == 0) factors(std::true_type{});
+    else factors(std::false_type{});
+    block_barrier();
 
     const float br = bet[tok];
     {   // over j <= r
@@ -293,9 +307,17 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         dk[mm] += y;
         const u32x2v q2 = *reinterpret_cast<const u32x2v*>(ql.x + tok * ql.kLd + 16 * m + 4 * g);
         const u32x2v k2 = *reinterpret_cast<const u32x2v*>(kl.x + tok * kl.kLd + 16 * m + 4 * g);
-        dg += (double)lo_bf16(q2[0]) * x[0] + (double)hi_bf16(q2[0]) * x[1] + (double)lo_bf16(q2[1]) * x[2] + (double)hi_bf16(q2[1]) * x[3];
-        dg += (double)lo_bf16(k2[0]) * y[0] + (double)hi_bf16(k2[0]) * y[1] + (double)lo_bf16(k2[1]) * y[2] + (double)hi_bf16(k2[1]) * y[3];
+        dg += (lo_bf16(q2[0]) * x[0] + hi_bf16(q2[0]) * x[1]) + (lo_bf16(q2[1]) * x[2] + hi_bf16(q2[1]) * x[3]);
+        dg += (lo_bf16(k2[0]) * y[0] + hi_bf16(k2[0]) * y[1]) + (lo_bf16(k2[1]) * y[2] + hi_bf16(k2[1]) * y[3]);
       }
+    }
+    // what the last wavefront needs at the end: a token a lane
+    constexpr int kParts = DV / 16;
+    float w_last = 0.f, db_last = 0.f, db_parts[kParts];
+    if (wave_id() == 7) {
+      if (lane < n) w_last = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) db_parts[c] = global_in<float>(p.ws_db)[(blk * kParts + c) * kGdrChunk + lane];
     }
     {   // over r >= j
       Planes<2> pc[2], ac[2];
@@ -310,15 +332,13 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         floatx4 x = c[mm] * (eta * br);
         const u32x2v k2 = *reinterpret_cast<const u32x2v*>(kl.x + tok * kl.kLd + 16 * m + 4 * g);
         const floatx4 k4 = {lo_bf16(k2[0]), hi_bf16(k2[0]), lo_bf16(k2[1]), hi_bf16(k2[1])};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) write += (double)k4[r] * (double)x[r];
+        write += (k4[0] * x[0] + k4[1] * x[1]) + (k4[2] * x[2] + k4[3] * x[3]);
         const bf16x8 kt[2] = {kl.transposed(m, 0, lane), kl.transposed(m, 1, lane)};
         const bf16x8 qt[2] = {ql.transposed(m, 0, lane), ql.transposed(m, 1, lane)};
         x = mma_steps(kt, ac, x);
         x = mma_steps(qt, pc, x);
         dk[mm] += x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dg -= (double)k4[r] * (double)x[r];
+        dg -= (k4[0] * x[0] + k4[1] * x[1]) + (k4[2] * x[2] + k4[3] * x[3]);
       }
     }
     // the log-decay's gradient
@@ -329,7 +349,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
     if (g == 0) dG[half][tok] = dg;
     if (lane == 0) extra[wave_id()] = sum;
-    __syncthreads();
+    block_barrier();
     if (wave_id() == 7) {   // while the others go on
       double x = dG[0][lane] + dG[1][lane];
       if (lane == 63) {
@@ -341,16 +361,15 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         const double dn = __shfl_down(x, d);
         if (lane + d < 64) x += dn;
       }
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) db_last += db_parts[c];
       if (lane < n) {
         put(global_out<T>(p.dw) + seq.row * p.sdw.b + h * p.sdw.h + (t0 + lane) * p.sdw.t,
             (float)(x * (double)gdr_gate_grad(w_last, p.gate, p.g_min)));
-        float total = 0.f;
-#pragma unroll
-        for (int c = 0; c < kParts; ++c) total += db_last[c];
-        put(global_out<T>(p.dbeta) + seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, total);
+        put(global_out<T>(p.dbeta) + seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, db_last);
       }
     }
-    if (hg + 1 < grp) __syncthreads();
+    if (hg + 1 < grp) block_barrier();
   }
 
   const int lane = tid & 63, g = lane >> 4, tok = 16 * tile + (lane & 15);
