@@ -122,6 +122,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         d2[i] = load_row8(dSt + DK * DV + at * 8);
       }
     }
+    if (hg > 0) block_barrier();   // the head before has used what lies in LDS
     if (tid < 64) {
       ghi[tid] = gates[0];
       glo[tid] = gates[1];
@@ -311,14 +312,6 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         dg += (lo_bf16(k2[0]) * y[0] + hi_bf16(k2[0]) * y[1]) + (lo_bf16(k2[1]) * y[2] + hi_bf16(k2[1]) * y[3]);
       }
     }
-    // what the last wavefront needs at the end: a token a lane
-    constexpr int kParts = DV / 16;
-    float w_last = 0.f, db_last = 0.f, db_parts[kParts];
-    if (wave_id() == 7) {
-      if (lane < n) w_last = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
-#pragma unroll
-      for (int c = 0; c < kParts; ++c) db_parts[c] = global_in<float>(p.ws_db)[(blk * kParts + c) * kGdrChunk + lane];
-    }
     {   // over r >= j
       Planes<2> pc[2], ac[2];
 #pragma unroll
@@ -350,7 +343,12 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     if (g == 0) dG[half][tok] = dg;
     if (lane == 0) extra[wave_id()] = sum;
     block_barrier();
-    if (wave_id() == 7) {   // while the others go on
+    if (wave_id() == 7) {   // while the others ask for the next head's operands
+      constexpr int kParts = DV / 16;
+      float w_last = 0.f, db_parts[kParts], db_last = 0.f;
+      if (lane < n) w_last = get(global_in<T>(p.w) + seq.row * p.sw.b + h * p.sw.h + (t0 + lane) * p.sw.t);
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) db_parts[c] = global_in<float>(p.ws_db)[(blk * kParts + c) * kGdrChunk + lane];
       double x = dG[0][lane] + dG[1][lane];
       if (lane == 63) {
 #pragma unroll
@@ -369,7 +367,6 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
         put(global_out<T>(p.dbeta) + seq.row * p.sdb.b + h * p.sdb.h + (t0 + lane) * p.sdb.t, db_last);
       }
     }
-    if (hg + 1 < grp) block_barrier();
   }
 
   const int lane = tid & 63, g = lane >> 4, tok = 16 * tile + (lane & 15);
