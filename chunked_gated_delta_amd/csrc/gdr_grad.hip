@@ -92,8 +92,8 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
       if (r < n && (kAllTok || at < 64 * kRow8)) {
         ox[i] = load_row8(dO + r * p.sdo.t + c0);
         ex[i] = load_row8(dE + r * p.sdv.t + c0);
-        e2[i] = load_row8(E2 + at * 8);
       }
+      if (at % 128 / 2 < n && (kAllTok || at < 64 * kRow8)) e2[i] = load_row8(E2 + at * 8);
     }
     if (hg == 0) {   // K and Q, zeros behind the sequence's end
 #pragma unroll
@@ -128,22 +128,26 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
       glo[tid] = gates[1];
       bet[tid] = gates[2];
     }
+    // piece `at` of a matrix kept as 16 columns after the other, `rows` of 16 values each
+    auto at_part = [&](T* base, int at, int rows) {
+      return reinterpret_cast<bf16x8*>(base + at % (2 * rows) / 2 * kLd + at / (2 * rows) * 16 + (at & 1) * 8);
+    };
     auto at_row = [&](T* base, int at) { return reinterpret_cast<bf16x8*>(base + at / kRow8 * kLd + at % kRow8 * 8); };
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const int at = tid + 512 * i;
       if (kAllTok || at < 64 * kRow8) {
-        *at_row(fl, at) = fx[i];
-        *at_row(f2l, at) = f2[i];
+        *at_part(fl, at, 64) = fx[i];
+        *at_part(f2l, at, 64) = f2[i];
         *at_row(ol, at) = ox[i];
         *at_row(el, at) = ex[i];
-        *at_row(e2l, at) = e2[i];
+        *at_part(e2l, at, 64) = e2[i];
       }
     }
     auto put_plane = [&](const bf16x8 (&x)[kSt]) {
 #pragma unroll
       for (int i = 0; i < kSt; ++i)
-        if (kAllSt || tid + 512 * i < DK * kRow8) *at_row(sl, tid + 512 * i) = x[i];
+        if (kAllSt || tid + 512 * i < DK * kRow8) *at_part(sl, tid + 512 * i, DK) = x[i];
     };
     put_plane(sx);
     if (hg == 0) {
@@ -436,12 +440,12 @@ __global__ __launch_bounds__(512) void gdr_grad_f32_kernel(GdrParams p) {
       bet[lane] = gate[kGateBeta + lane];
     }
     const float gam = gate[kGateGam + tok], eta = gate[kGateEta + tok], last = gate[kGateLast];
-    const auto F = global_in<T>(p.ws_f) + blk * kGdrChunk * DV + 8 * g;
-    const auto St = global_in<T>(p.ws_s) + blk * DK * DV + 8 * g;
-    const auto dSt = global_in<T>(p.ws_ds) + blk * DK * DV + 8 * g;
+    const auto F = global_in<T>(p.ws_f) + blk * kGdrChunk * DV + 8 * (g & 1);   // 16 columns after the other
+    const auto St = global_in<T>(p.ws_s) + blk * DK * DV + 8 * (g & 1);
+    const auto dSt = global_in<T>(p.ws_ds) + blk * DK * DV + 8 * (g & 1);
     const auto dO = global_in<T>(p.dO) + seq.row * p.sdo.b + h * p.sdo.h + t0 * p.sdo.t + 8 * g;
     const auto dE = global_in<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + t0 * p.sdv.t + 8 * g;
-    auto f_frag = [&](int tile, int kv) { return load_row8(F + (int64_t)(16 * tile + li) * DV + 32 * kv); };
+    auto f_frag = [&](int tile, int kv) { return load_row8(F + ((2 * kv + (g >> 1)) * kGdrChunk + 16 * tile + li) * 16); };
     auto rows_of = [&](GlobalPtr<const T> base, int64_t st, int tile, int kv) {
       const int r = 16 * tile + li;   // rows behind the end: the last one's, as zeros
       const In x = load_row8(base + (int64_t)min(r, n - 1) * st + 32 * kv);
@@ -496,8 +500,8 @@ __global__ __launch_bounds__(512) void gdr_grad_f32_kernel(GdrParams p) {
       In st[KV], dst[KV];
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) {
-        st[kv] = load_row8(St + (int64_t)(16 * m + li) * DV + 32 * kv);
-        dst[kv] = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
+        st[kv] = load_row8(St + ((2 * kv + (g >> 1)) * DK + 16 * m + li) * 16);
+        dst[kv] = load_row8(dSt + ((2 * kv + (g >> 1)) * DK + 16 * m + li) * 16);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -565,7 +569,7 @@ __global__ __launch_bounds__(512) void gdr_grad_f32_kernel(GdrParams p) {
       floatx4 a = {};
       In dst[KV];
 #pragma unroll
-      for (int kv = 0; kv < KV; ++kv) dst[kv] = load_row8(dSt + (int64_t)(16 * m + li) * DV + 32 * kv);
+      for (int kv = 0; kv < KV; ++kv) dst[kv] = load_row8(dSt + ((2 * kv + (g >> 1)) * DK + 16 * m + li) * 16);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int kv = 0; kv < KV; ++kv) a = mma(dst[kv], fo[kv], a);

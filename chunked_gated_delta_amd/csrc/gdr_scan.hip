@@ -30,21 +30,31 @@ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? 
 __device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ float value(float x) { return x; }
 
-// Writes `rows` contraction places x 16 columns of B operands to row-major memory, bf16 in two planes of `plane`
-// values: a lane takes 8 columns of one place.
+// Writes `rows` contraction places x 16 columns of B operands to memory, place by place, bf16 in two planes of `plane`
+// values: a lane takes 8 columns of one place.  A workgroup's 16 columns lie together there (as 32 bytes of rows of
+// all columns, 2x4096 tokens' two chains took ROWMAJOR).  bf16: transposing reads, in which 16 lanes read 16 places
+// of 4 columns and get one place's 4 columns each.
 template <typename T>
-__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int64_t plane, int ld, int tid) {
-  for (int i = tid; i < rows * 2; i += 256) {
-    const int r = i >> 1, c0 = (i & 1) * 8;
+__device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int64_t plane, int tid) {
+  if constexpr (sizeof(T) == 2) {
+    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+    const int group = tid >> 4, j = tid & 15, block = group >> 1, c0 = (group & 1) * 8;   // block of 16 places
+    if (16 * block >= rows) return;   // whole wavefronts: rows are a multiple of 32
+    const char* fr = frags + (block >> 1) * frag_bytes + (c0 + (j >> 2) + 16 * (2 * (block & 1) + ((j >> 1) & 1))) * 16 + (j & 1) * 8;
 #pragma unroll
     for (int n = 0; n < kKept<T>; ++n) {
-      const char* fr = frags + (r >> 5) * frag_bytes + n * kPlane;
-      T x[8];
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)(fr + n * kPlane));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)(fr + n * kPlane + 4 * 16));
+      *repoint<bf16x8>(out + n * plane + (16 * block + j) * 16 + c0) =
+          __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  } else {
+    for (int i = tid; i < rows * 2; i += 256) {
+      const int r = i >> 1, c0 = (i & 1) * 8;
+      float8v x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(fr, r & 31, c0 + e);
-      typename Frags<T>::In v;
-      __builtin_memcpy(&v, x, sizeof(v));
-      *repoint<typename Frags<T>::In>(out + n * plane + r * ld + c0) = v;
+      for (int e = 0; e < 8; ++e) x[e] = frag_at<T>(frags + (r >> 5) * frag_bytes, r & 31, c0 + e);
+      *repoint<float8v>(out + r * 16 + c0) = x;
     }
   }
 }
@@ -286,23 +296,23 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) 
   if constexpr (STATES) {
     block_barrier();   // the first state, v and gates
     const int64_t s_plane = p.dk * p.dv, f_plane = kGdrChunk * p.dv;
-    auto sp = global_out<T>(p.ws_s) + blk0 * kKept<T> * s_plane + 16 * part;
-    auto fp = global_out<T>(p.ws_f) + blk0 * kKept<T> * f_plane + 16 * part;
+    auto sp = global_out<T>(p.ws_s) + blk0 * kKept<T> * s_plane + part * (DK * 16);
+    auto fp = global_out<T>(p.ws_f) + blk0 * kKept<T> * f_plane + part * (kGdrChunk * 16);
     for (int64_t c = 0; c < nc; ++c) {
       // F of the chunk before; the state that enters this one; what the chain needs of the next
       if (c > 0) {
-        write_rows<T>(uf, kOp2, kGdrChunk, fp, f_plane, p.dv, tid);
+        write_rows<T>(uf, kOp2, kGdrChunk, fp, f_plane, tid);
         fp += p.Hv * kKept<T> * f_plane;
       }
       block_barrier();
-      write_rows<T>(sf, kOp3, DK, sp, s_plane, p.dv, tid);
+      write_rows<T>(sf, kOp3, DK, sp, s_plane, tid);
       sp += p.Hv * kKept<T> * s_plane;
       block_barrier();
       leave(c + 1);
       fetch();
       block_barrier();
     }
-    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp, f_plane, p.dv, tid);
+    if (nc > 0) write_rows<T>(uf, kOp2, kGdrChunk, fp, f_plane, tid);
   } else {
     auto op = global_out<T>(p.o) + seq.row * p.so.b + h * p.so.h + seq.t0 * p.so.t + 16 * part;
     const uint32_t orow = (uint32_t)(((tid >> 1) * p.so.t + 8 * (tid & 1)) * sizeof(T));
@@ -545,16 +555,16 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     auto pp = as_global((const char*)p.ws_p) + ((blk0 + at * p.Hv) * kTriFrags + upper_frag(wave, TS == 2 ? 0 : 1)) * kOp3;
     // of the chunk the chain is at
     const int64_t s_plane = p.dk * p.dv, f_plane = kGdrChunk * p.dv;
-    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kKept<T> * f_plane + 16 * part;
-    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * kKept<T> * s_plane + 16 * part;
-    auto ep = global_out<T>(p.ws_e) + (blk0 + at * p.Hv) * f_plane + 16 * part;
+    auto fp = global_in<T>(p.ws_f) + (blk0 + at * p.Hv) * kKept<T> * f_plane + part * (kGdrChunk * 16);
+    auto sp = global_out<T>(p.ws_ds) + (blk0 + at * p.Hv) * kKept<T> * s_plane + part * (DK * 16);
+    auto ep = global_out<T>(p.ws_e) + (blk0 + at * p.Hv) * f_plane + part * (kGdrChunk * 16);
     auto dvp = global_out<T>(p.dv_) + seq.row * p.sdv.b + h * p.sdv.h + (seq.t0 + at * kGdrChunk) * p.sdv.t + 16 * part;
     auto dbp = global_out<float>(p.ws_db) + ((blk0 + at * p.Hv) * (p.dv / 16) + part) * kGdrChunk;
     // wavefronts 4 and 5 move dO, wavefronts 6 and 7 F, dU and the gradients that are made of them: a lane has
     // half a token's columns
     const int tid2 = tid & 127, row = tid2 >> 1;
     const LaneRow orow(row, last_rows, p.sdo.t, 8 * (tid & 1), sizeof(T));
-    const uint32_t frow = (uint32_t)((row * p.dv + 8 * (tid2 & 1)) * sizeof(T));
+    const uint32_t frow = (uint32_t)(tid2 * 8 * sizeof(T));
     const uint32_t vrow = (uint32_t)((row * p.sdv.t + 8 * (tid2 & 1)) * sizeof(T));
     auto fetch = [&]() {
       if (wave < 2) ox = load_row8(lane_at(dop, orow.of(at == nc - 1)));
@@ -676,7 +686,7 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p)
     block_barrier();
     for (int64_t c = nc - 1; c >= 0; --c) {
       // dS at this chunk's end; what the chain needs of the next one
-      write_rows<T>(sf, kOp3, DK, sp, s_plane, p.dv, tid);
+      write_rows<T>(sf, kOp3, DK, sp, s_plane, tid);
       sp -= p.Hv * kKept<T> * s_plane;
       if (c > 0) spread(c - 1);
       block_barrier();
