@@ -373,20 +373,29 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(GdrParams p) {
     }
   }
 
+  // whole rows: 8 bytes a lane as they lie here would be written to memory twice over
+  block_barrier();   // K and Q are used
   const int lane = tid & 63, g = lane >> 4, tok = 16 * tile + (lane & 15);
-  if (tok < n) {
-    const auto dqp = global_out<T>(p.dq) + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + tok) * p.sdq.t + 4 * g;
-    const auto dkp = global_out<T>(p.dk_) + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + tok) * p.sdk.t + 4 * g;
 #pragma unroll
-    for (int mm = 0; mm < MH; ++mm) {
-      store_row4(dqp + 16 * (half * MH + mm), dq[mm]);
-      store_row4(dkp + 16 * (half * MH + mm), dk[mm]);
+  for (int mm = 0; mm < MH; ++mm) {
+    const int c = 16 * (half * MH + mm) + 4 * g;
+    *reinterpret_cast<u32x2v*>(ql.x + tok * ql.kLd + c) = u32x2v{pk_bf16(dq[mm][0], dq[mm][1]), pk_bf16(dq[mm][2], dq[mm][3])};
+    *reinterpret_cast<u32x2v*>(kl.x + tok * kl.kLd + c) = u32x2v{pk_bf16(dk[mm][0], dk[mm][1]), pk_bf16(dk[mm][2], dk[mm][3])};
+  }
+  block_barrier();
+#pragma unroll
+  for (int i = 0; i < kCh; ++i) {
+    const int at = tid + 512 * i, row = at / (DK / 8), c0 = at % (DK / 8) * 8;
+    if (row < n) {
+      *repoint<bf16x8>(global_out<T>(p.dq) + seq.row * p.sdq.b + kh * p.sdq.h + (t0 + row) * p.sdq.t + c0) = load_row8(ql.x + row * ql.kLd + c0);
+      *repoint<bf16x8>(global_out<T>(p.dk_) + seq.row * p.sdk.b + kh * p.sdk.h + (t0 + row) * p.sdk.t + c0) = load_row8(kl.x + row * kl.kLd + c0);
     }
   }
 }
 
-// fp32 inputs: the same sums with 4 wavefronts, one token tile and all channels each; a lane's operands come
-// straight from memory, since three 64-row tiles and a state in fp32 would not fit LDS beside K and Q.
+// fp32 inputs: the same sums, a lane's operands straight from memory, since three 64-row tiles and a state in fp32
+// would not fit LDS beside K and Q.  5 sequences of 0 to 447 tokens, 4 heads of 64 x 128: 69 us, of which most are the
+// trips to memory of 30 workgroups.
 template <int DK, int DV>
 __global__ __launch_bounds__(512) void gdr_grad_f32_kernel(GdrParams p) {
   using T = float;
