@@ -2,19 +2,24 @@
 // adjoint dS at the chunk's end and dE (the gradient of v): one workgroup per (chunk, key head), the
 // value heads that share the key head one after another.
 //
-// A wavefront owns 16 tokens and (bf16) half of the channels and forms the transposed gradients (channels x
+// A wavefront owns 16 tokens and half of the channels and forms the transposed gradients (channels x
 // tokens), so a lane holds one token and 4 consecutive channels.  bf16: the workgroup asks for all its operands
-// at once (144 KiB at dk = dv = 128: one workgroup's whole traffic in flight) and shares them in LDS; K^T and
-// Q^T are transposing LDS reads.  With dO' = scale dO and D_rj = e^{G_r - G_j}:
+// at once (240 KiB at dk = dv = 128: one workgroup's whole traffic in flight), in the order it uses them, and
+// shares them in LDS, the states a plane at a time; K^T and Q^T are transposing LDS reads.  With dO' = scale dO and
+// D_rj = e^{G_r - G_j}:
 //   dP = lower(dO' U^T . D)   dA = -strict_lower(dE U^T . D)
 //   dq_r  =  gam_r S dO'_r + sum_j dP_rj k_j
 //   dk_r  = -gam_r S dE_r  + sum_j dA_rj k_j                                    (as a row: reads)
 //         +  eta_r dS U_r  + sum_r' dA_r'r k_r' + sum_r' dP_r'r q_r'            (as a column: writes)
 //   dG_r  = q_r . dq_r + k_r . dk_r(row) - k_r . dk_r(column),   dG_last += sum_r k_r . eta_r dS U_r + e^{G_last} <S, dS>
 //   dg_t  = sum_{r >= t} dG_r
-// The second identity gives the log-decay's gradient from the accumulators that are there anyway.  S,
-// dS, F and dE are held in the inputs' type here (their rounding is one of the gradients' own size, half a
-// step of that type); dP and dA take two planes, which keeps the error below 1.5 times the final rounding's.
+// The second identity gives the log-decay's gradient from the accumulators that are there anyway.  S, dS, F and
+// dE come in two bf16 planes, dP and dA are made of two (off by 2^-17): with one plane of each, 2x4096 tokens' kernel
+// took 164 us, but dk and dw were off by up to 3.6e-3 where the rounding of the results is 1.7e-3.
+//
+// 2 x 4096 tokens, 16 heads of 128 x 128 in bf16: 212 us for 0.6 GB.  One workgroup fills a compute unit's LDS, so half
+// of its cycles wait for the loads (all compute units ask at once) and the other half use none of the bandwidth; where
+// value heads share a key head, the next one's operands are asked for before the last sums of the one before.
 #include <type_traits>
 
 #include "gdr_internal.h"

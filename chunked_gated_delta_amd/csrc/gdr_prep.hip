@@ -8,6 +8,9 @@
 //   X_ij = -X_ii sum_{j <= m < i} A_im X_mj,
 // on v_mfma_f32_16x16x4_f32, whose result registers are the next product's B operand as they are (the
 // contraction runs over places 4g + r).  The backward also needs (I + diag(beta) A)^{-1} and P transposed.
+//
+// Bound by HBM: it reads K and Q and writes 18 KiB of T' (three planes) and 12 of P (two) a chunk and head; 64K tokens
+// of 16 heads take 257 us for 1.05 GB, 4.1 TB/s (a large copy: 4.8), 2 x 4096 tokens' backward 59 us for 0.19 GB.
 #include "gdr_internal.h"
 
 namespace kda {

@@ -6,6 +6,8 @@
 //   a = S^T k,  b = S^T q,  d = k . q:   f = v - e^g a,  S <- e^g S + k (beta f)^T,  o = scale (e^g b + d beta f)
 // so a token costs one exchange between the row groups (lanes by shuffles, wavefronts through LDS).
 //
+// 512 rows of 16 heads of 128 x 128: 1.07 GB in 221 us, 4.8 TB/s, a large copy's rate; one row of 8 heads: 5 us.
+//
 // Rows that name the same slot are successive tokens of that state: the first such row's workgroup
 // takes them all in order and the others return, so no two workgroups touch one state.
 #include "gdr_internal.h"
