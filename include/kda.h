@@ -277,7 +277,7 @@ KDA_API size_t kda_workspace_bytes_ex(const kda_shape_t* shape, int chunk, const
  * never an access out of range.
  * Evaluated in chunks of 64 tokens: a NaN or infinity in a token may reach the other tokens of its
  * chunk and every later one, never another sequence.  bf16: inputs are exact operands; what is
- * computed is carried as a sum of two bf16, so o is off by its own rounding and states stay near fp32. */
+ * computed is carried as a sum of two or three, so a result is off by its own rounding and states are fp32's. */
 typedef struct {
   int64_t b, h, t;         /* elements between batch rows, heads and tokens */
 } kda_stride_t;
