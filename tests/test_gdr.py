@@ -144,6 +144,21 @@ def test_resets_and_zero_rates(dtype):
         check(n, x, ref[n], tol(n, dtype))
 
 
+@pytest.mark.parametrize("n", [2, 511, 512, 513, 700])
+def test_many_sequences(n):
+    """Batches on both sides of the number of sequences that are taken longest first; equal lengths among them."""
+    say(f"[case] gdr {n} sequences")
+    lens = torch.randint(0, 4, (n,), generator=torch.Generator().manual_seed(n)).tolist()
+    lens[n // 2] = 130
+    d = make(1, sum(lens), 1, 1, 32, 32, F32, seed=16, states=n)
+    o, S = run_fwd(d, lens)
+    ro, rS, ref = reference(d, lens, grads=True)
+    check("o", o, ro, tol("o", F32))
+    check("S_final", S, rS, tol("S", F32))
+    for m, x in zip(GRADS, run_bwd(d, lens)):
+        check(m, x, ref[m], tol(m, F32))
+
+
 @pytest.mark.parametrize("case", [(1, 150, 2, 4, 128, 128, "bounded"), (2, 2, 1, 4, 32, 64, "softplus"), (3, 77, 2, 2, 64, 32, "log")])
 def test_bf16_results_are_rounded_once(case):
     """The results' error is their own rounding's: what lies before it is off by the planes' 2^-17 alone."""
