@@ -63,6 +63,13 @@ def test_descriptors(call, kw, code):
     assert call(desc(**({"T": 100} | kw))) == code
 
 
+@pytest.mark.parametrize("call", [fwd, bwd, step])
+@pytest.mark.parametrize("name,dtype,stride", [("q", 1, (1 << 24) + 8), ("k", 0, (1 << 23) + 4), ("v", 1, (1 << 24) + 8), ("w", 1, (1 << 24) + 1)])
+def test_token_strides_within_32_bits_a_chunk(call, name, dtype, stride):
+    """The kernels address the 64 tokens of a chunk by 32-bit offsets: a token stride past 32 MiB is refused."""
+    assert call(desc(T=2, dtype=dtype, **{name: KdaStride(stride, stride, stride)})) == -4
+
+
 @pytest.mark.parametrize("call,names", [(fwd, ("q", "k", "v", "w", "beta", "o", "ws")), (step, ("q", "k", "v", "w", "beta", "S", "o")),
                                         (bwd, ("q", "k", "v", "w", "beta", "dO", "dq", "dk", "dv", "dw", "dbeta", "ws"))])
 def test_null_and_misaligned_pointers(call, names):
