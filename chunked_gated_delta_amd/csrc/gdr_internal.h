@@ -193,7 +193,7 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 // before it leave: three planes hold an fp32 value whole, two are off by at most 2^-17 of it.  The state,
 // its adjoint and everything between them (E, T', U) take three: with two, S_final was off by 4e-6 where
 // fp32 arithmetic is off by 5e-8, with three it keeps fp32's accuracy for 1.5 times the matrix
-// instructions.  What enters only results of the inputs' type takes one or two.
+// instructions.  What enters only results of the inputs' type takes two.
 // fp32 inputs use v_mfma_f32_16x16x4_f32 on the same 8 values, one place of each lane group at a time.
 template <int N> struct Planes {
   bf16x8 p[N];
