@@ -164,7 +164,7 @@ def gdr_chunk_fwd(q, k, v, w, beta, S0=None, g_min: float = -5.0, *, scale: floa
     need = _need(desc, False)
     workspace = _workspace(workspace, need, dev)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(dev.index)
     else:
         _on_stream(stream, out, S_final, workspace)
     _call("kda_gdr_chunk_fwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(out),
@@ -191,7 +191,7 @@ def gdr_chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -
     need = _need(desc, True)
     workspace = _workspace(workspace, need, dev)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(dev.index)
     else:
         _on_stream(stream, *outs, dS0, workspace)
     grads = KdaGdrGrads(*(_at(t) for t in outs), _at(dS0), *(KdaStride(*t.stride()[:3]) for t in outs))
@@ -219,7 +219,7 @@ def gdr_decode(q, k, v, w, beta, S, slots=None, g_min: float = -5.0, *, scale: f
         out = _like(v)
     so = _view(out, "out", v.shape, v.dtype, dev)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(dev.index)
     else:
         _on_stream(stream, out)
     _call("kda_gdr_decode", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S), S.shape[0], _at(slots), ctypes.byref(desc), _at(out),
@@ -227,10 +227,24 @@ def gdr_decode(q, k, v, w, beta, S, slots=None, g_min: float = -5.0, *, scale: f
     return out
 
 
-def _rows4(t):
-    """A tensor of up to three leading dimensions as [.,.,.,D]."""
-    d = t.dim()
-    return t if d == 4 else t[(None,) * (4 - d)]
+def _row_strides(t):
+    """Strides of a tensor of up to four dimensions over its rows' places [B,H,T] (those it lacks: 0)."""
+    return KdaStride(*((0, 0, 0) + t.stride())[-4:-1])
+
+
+def _rows(t, name, x):
+    """Checks a tensor of rows against x; its strides over them."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must be a tensor of x's shape {tuple(x.shape)}, not {tuple(t.shape)}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
+    if t.device != x.device:
+        raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return _row_strides(t)
 
 
 def _norm_inputs(x, weight, z, act, residual, alpha, next_weight, eps):
@@ -243,7 +257,7 @@ def _norm_inputs(x, weight, z, act, residual, alpha, next_weight, eps):
         raise ValueError(f"act is {act!r}: use 'silu', 'sigmoid' or, without z, 'none'")
     if act == "none" and z is not None:
         raise ValueError("z is given with act 'none'")
-    code, dt, D = _dtype_code(x), x.dtype, x.shape[-1]
+    code, D = _dtype_code(x), x.shape[-1]
     lead = weight if weight is not None else next_weight
     if not isinstance(lead, torch.Tensor):
         raise TypeError("weights must be torch tensors")
@@ -251,16 +265,9 @@ def _norm_inputs(x, weight, z, act, residual, alpha, next_weight, eps):
     for t, name in ((weight, "weight"), (next_weight, "next_weight")):
         if t is not None:
             _dense(t, name, (D,), lead.dtype, dev)
-    strides = []
-    for t, name in ((x, "x"), (z, "z"), (residual, "residual")):
-        if t is None:
-            strides.append(KdaStride(0, 0, 0))
-        else:
-            if not isinstance(t, torch.Tensor) or t.shape != x.shape:
-                raise ValueError(f"{name} must be a tensor of x's shape {tuple(x.shape)}")
-            r = _rows4(t)
-            strides.append(_view(r, name, r.shape, dt, dev))
-    B, H, T, _ = _rows4(x).shape
+    none = KdaStride(0, 0, 0)
+    strides = [none if t is None else _rows(t, name, x) for t, name in ((x, "x"), (z, "z"), (residual, "residual"))]
+    B, H, T = ((1, 1, 1) + x.shape)[-4:-1]
     return KdaNorm(B, H, T, D, code, wcode, _ACTS.get(act, 0), alpha, eps, *strides), dev
 
 
@@ -280,11 +287,10 @@ def norm_gate_fwd(x, weight=None, z=None, act: str = "silu", residual=None, alph
         y = None
     elif y is None:
         y = _like(x)
-    r = _rows4(s)
-    ss = _view(r, "s", _rows4(x).shape, x.dtype, dev)
-    sy = _view(_rows4(y), "y", r.shape, x.dtype, dev) if y is not None else ss
+    ss = _rows(s, "s", x)
+    sy = _rows(y, "y", x) if y is not None else ss
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(dev.index)
     else:
         _on_stream(stream, s, y)
     _call("kda_norm_fwd", dev, (_at(x), _at(weight), _at(z), _at(residual), _at(next_weight), ctypes.byref(desc), _at(s), ctypes.byref(ss),
@@ -302,7 +308,7 @@ def norm_gate_bwd(x, ds, dy=None, weight=None, z=None, act: str = "silu", residu
         raise ValueError("dy is given exactly when next_weight is")
     if ds is None and next_weight is None:
         raise ValueError("ds is None")
-    sds, sdy = (None if t is None else _view(_rows4(t), name, _rows4(x).shape, x.dtype, dev) for t, name in ((ds, "ds"), (dy, "dy")))
+    sds, sdy = (None if t is None else _rows(t, name, x) for t, name in ((ds, "ds"), (dy, "dy")))
     dx = _like(x)
     dz = _like(z) if z is not None else None
     dres = _like(residual) if residual is not None else None
@@ -312,10 +318,10 @@ def norm_gate_bwd(x, ds, dy=None, weight=None, z=None, act: str = "silu", residu
     need = 0 if need == ctypes.c_size_t(-1).value else need
     workspace = _workspace(workspace, need, dev)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(dev.index)
     else:
         _on_stream(stream, dx, dz, dres, dw, dw2, workspace)
-    st = [KdaStride(0, 0, 0) if t is None else KdaStride(*_rows4(t).stride()[:3]) for t in (dx, dz, dres)]
+    st = [KdaStride(0, 0, 0) if t is None else _row_strides(t) for t in (dx, dz, dres)]
     grads = KdaNormGrads(_at(dx), _at(dz), _at(dres), _at(dw), _at(dw2), *st)
     ref = lambda t: None if t is None else ctypes.byref(t)  # noqa: E731
     _call("kda_norm_bwd", dev, (_at(x), _at(weight), _at(z), _at(residual), _at(next_weight), ctypes.byref(desc), _at(ds), ref(sds), _at(dy),
