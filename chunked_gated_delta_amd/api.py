@@ -1,8 +1,12 @@
 """torch-facing wrappers over libkda.so.  Argument marshalling only: every
 step of the computation runs in the library's HIP kernels.  torch provides the
-device memory (outputs, workspace, statistics) and the stream."""
+device memory (outputs, workspace, statistics) and the stream.
+
+A call with `stream` reads its inputs there: whoever wrote them on another stream lets `stream` wait for that
+one first, and whoever uses the results on another stream lets that one wait for `stream`."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -41,13 +45,31 @@ def _check(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _on_stream(stream, *tensors):
-    """Tell torch's caching allocator that `stream` uses these tensors: memory allocated on the
-    current stream but written by kernels on another one must not be handed out again before
-    that stream's work on it is done."""
-    if stream == torch.cuda.current_stream(stream.device):
+_HERE = contextlib.nullcontext()
+
+
+def _stream_of(stream, dev):
+    """The stream of a call and the context in which the call allocates: the caching allocator hands out
+    memory whose earlier use was on the stream that is current, so what is written on `stream` is allocated
+    with that one current.  (A block freed on another stream may still be read or written there.)"""
+    if stream is None:
+        return torch.cuda.current_stream(dev.index), _HERE
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream, torch.cuda.stream(stream)
+
+
+def _on_stream(stream, results, *others):
+    """Tell torch's caching allocator which streams use a call's tensors, so that each may be dropped as
+    soon as the call returns: `stream` all of them, and the current one the results, whatever stream
+    they were allocated on."""
+    here = torch.cuda.current_stream(stream.device)
+    if stream == here:
         return
-    for t in tensors:
+    for t in results:
+        if t is not None:
+            t.record_stream(here)
+    for t in (*results, *others):
         if t is not None:
             t.record_stream(stream)
 
@@ -96,25 +118,25 @@ def chunk_fwd(q, k, v, w, beta, S0=None, g_min: float = -5.0, chunk: int = 16, *
     _check(beta, "beta", (B, H, T), dt, dev)
     if S0 is not None:
         _check(S0, "S0", (B, H, dk, dv), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-    else:
+    if out is not None:
         _check(out, "out", (B, H, T, dv), dt, dev)
-    if S_final is None:
-        S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    else:
+    if S_final is not None:
         _check(S_final, "S_final", (B, H, dk, dv), torch.float32, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
     opts = KdaOpts(int(bool(disable_fallback)), int(force_fallback), _PATHS[path], int(seg_steps),
                    events[0].handle if events else None, events[1].handle if events else None)
     plain = not (disable_fallback or force_fallback or path != "auto" or seg_steps or events)
     ws_need = _lib.workspace_bytes(shape, chunk, None if plain else opts)
-    if workspace is None and ws_need > 0:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=dev)
-    st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    _on_stream(stream, out, S_final, workspace, st)
+    stream, place = _stream_of(stream, dev)
+    with place:
+        if out is None:
+            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+        if S_final is None:
+            S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        if workspace is None and ws_need > 0:
+            workspace = torch.empty(ws_need, dtype=torch.uint8, device=dev)
+        st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
+    _on_stream(stream, (out, S_final, st), workspace, q, k, v, w, beta, S0)
     ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(S0), ctypes.c_float(g_min), int(chunk),
             ctypes.byref(shape), _ptr(out), _ptr(S_final), _ptr(workspace), ws_len, _ptr(st),
@@ -153,19 +175,19 @@ def chunk_fwd_noalloc(q, k, v, w, beta, S0=None, g_min: float = -5.0, chunk: int
     _check(beta, "beta", (B, H, T), dt, dev)
     if S0 is not None:
         _check(S0, "S0", (B, H, dk, dv), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-    else:
+    if out is not None:
         _check(out, "out", (B, H, T, dv), dt, dev)
-    if S_final is None:
-        S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    else:
+    if S_final is not None:
         _check(S_final, "S_final", (B, H, dk, dv), torch.float32, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
-    st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    _on_stream(stream, out, S_final, st)
+    stream, place = _stream_of(stream, dev)
+    with place:
+        if out is None:
+            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+        if S_final is None:
+            S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
+    _on_stream(stream, (out, S_final, st), q, k, v, w, beta, S0)
     with torch.cuda.device(dev):
         rc = _lib.load().kda_chunk_fwd_noalloc(
             _ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(S0), ctypes.c_float(g_min), int(chunk),
@@ -197,14 +219,14 @@ def gate_prefix(w, g_min: float = -5.0, chunk: int = 16, stream=None):
     _check(w, "w", (B, H, T, dk), w.dtype, dev)
     _dtype_code(w)
     NC = (T + chunk - 1) // chunk
-    g = torch.empty((B, H, T, dk), dtype=torch.float32, device=dev)
-    G = torch.empty_like(g)
-    span = torch.empty((B, H, NC), dtype=torch.float32, device=dev)
-    flags = torch.empty((B, H, NC), dtype=torch.uint8, device=dev)
     shape = make_shape(B, H, T, dk, dk, _dtype_code(w))
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    _on_stream(stream, g, G, span, flags)
+    stream, place = _stream_of(stream, dev)
+    with place:
+        g = torch.empty((B, H, T, dk), dtype=torch.float32, device=dev)
+        G = torch.empty_like(g)
+        span = torch.empty((B, H, NC), dtype=torch.float32, device=dev)
+        flags = torch.empty((B, H, NC), dtype=torch.uint8, device=dev)
+    _on_stream(stream, (g, G, span, flags), w)
     with torch.cuda.device(dev):
         rc = _lib.load().kda_gate_prefix(_ptr(w), ctypes.c_float(g_min), int(chunk), ctypes.byref(shape),
                                          _ptr(g), _ptr(G), _ptr(span), _ptr(flags),
@@ -232,14 +254,14 @@ def decode(q, k, v, w, beta, S, g_min: float = -5.0, *, out=None, stream=None):
     _check(v, "v", (B, H, T, dv), dt, dev)
     _check(beta, "beta", (B, H, T), dt, dev)
     _check(S, "S", (B, H, dk, dv), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-    else:
+    if out is not None:
         _check(out, "out", (B, H, T, dv), dt, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    _on_stream(stream, out)
+    stream, place = _stream_of(stream, dev)
+    with place:
+        if out is None:
+            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+    _on_stream(stream, (out, S), q, k, v, w, beta)
     with torch.cuda.device(dev):
         rc = _lib.load().kda_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(S),
                                     ctypes.c_float(g_min), ctypes.byref(shape), _ptr(out),
@@ -275,21 +297,21 @@ def chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -5.0,
     if dS_final is not None:
         _check(dS_final, "dS_final", (B, H, dk, dv), torch.float32, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
-    f32 = dict(dtype=torch.float32, device=dev)
-    dq = torch.empty((B, H, T, dk), **f32)
-    dk_ = torch.empty((B, H, T, dk), **f32)
-    dv_ = torch.empty((B, H, T, dv), **f32)
-    dw = torch.empty((B, H, T, dk), **f32)
-    dbeta = torch.empty((B, H, T), **f32)
-    dS0 = torch.empty((B, H, dk, dv), **f32) if want_dS0 else None
     need = _lib.bwd_workspace_bytes(shape, chunk)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif workspace.numel() * workspace.element_size() < need:
+    if workspace is not None and workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {need} needed")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    _on_stream(stream, dq, dk_, dv_, dw, dbeta, dS0, workspace)
+    f32 = dict(dtype=torch.float32, device=dev)
+    stream, place = _stream_of(stream, dev)
+    with place:
+        dq = torch.empty((B, H, T, dk), **f32)
+        dk_ = torch.empty((B, H, T, dk), **f32)
+        dv_ = torch.empty((B, H, T, dv), **f32)
+        dw = torch.empty((B, H, T, dk), **f32)
+        dbeta = torch.empty((B, H, T), **f32)
+        dS0 = torch.empty((B, H, dk, dv), **f32) if want_dS0 else None
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _on_stream(stream, (dq, dk_, dv_, dw, dbeta, dS0), workspace, q, k, v, w, beta, dO, S0, dS_final)
     with torch.cuda.device(dev):
         if events is not None:
             events[0].record(stream)

@@ -2,7 +2,10 @@
 around a block.  Argument marshalling only, as in api.py: the computation is in the library's HIP kernels.
 
 Tensors may be strided views with a contiguous last dimension, so [B,T,H,D] projections are passed as
-x.transpose(1, 2) and slices of a fused projection as they are; nothing is copied."""
+x.transpose(1, 2) and slices of a fused projection as they are; nothing is copied.
+
+A call with `stream` reads its inputs there: whoever wrote them on another stream lets `stream` wait for that
+one first, and whoever uses the results on another stream lets that one wait for `stream`."""
 from __future__ import annotations
 
 import ctypes
@@ -12,7 +15,7 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaGdr, KdaGdrGrads, KdaNorm, KdaNormGrads, KdaStride
-from .api import _dtype_code, _on_stream
+from .api import _dtype_code, _on_stream, _stream_of
 
 _ACTS = {"sigmoid": 0, "silu": 1}
 
@@ -154,19 +157,20 @@ def gdr_chunk_fwd(q, k, v, w, beta, S0=None, g_min: float = -5.0, *, scale: floa
     states = (n_seq or desc.B, desc.Hv, desc.dk, desc.dv)
     if S0 is not None:
         _dense(S0, "S0", states, torch.float32, dev)
-    if out is None:
-        out = _like(v)
-    so = _view(out, "out", v.shape, v.dtype, dev)
-    if S_final is None:
-        S_final = torch.empty(states, dtype=torch.float32, device=dev)
-    else:
-        _dense(S_final, "S_final", states, torch.float32, dev)
     need = _need(desc, False)
-    workspace = _workspace(workspace, need, dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev.index)
-    else:
-        _on_stream(stream, out, S_final, workspace)
+    given = stream is not None
+    stream, place = _stream_of(stream, dev)
+    with place:
+        if out is None:
+            out = _like(v)
+        if S_final is None:
+            S_final = torch.empty(states, dtype=torch.float32, device=dev)
+        else:
+            _dense(S_final, "S_final", states, torch.float32, dev)
+        workspace = _workspace(workspace, need, dev)
+    so = _view(out, "out", v.shape, v.dtype, dev)
+    if given:
+        _on_stream(stream, (out, S_final), workspace, q, k, v, w, beta, S0, cu_seqlens)
     _call("kda_gdr_chunk_fwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(out),
                                      ctypes.byref(so), _at(S_final), _at(workspace), need, stream.cuda_stream))
     return out, S_final
@@ -186,14 +190,15 @@ def gdr_chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -
         _dense(S0, "S0", states, torch.float32, dev)
     if dS_final is not None:
         _dense(dS_final, "dS_final", states, torch.float32, dev)
-    outs = [_like(q), _like(k), _like(v), _like(w, rows=False), _like(beta, rows=False)]
-    dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
     need = _need(desc, True)
-    workspace = _workspace(workspace, need, dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev.index)
-    else:
-        _on_stream(stream, *outs, dS0, workspace)
+    given = stream is not None
+    stream, place = _stream_of(stream, dev)
+    with place:
+        outs = [_like(q), _like(k), _like(v), _like(w, rows=False), _like(beta, rows=False)]
+        dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
+        workspace = _workspace(workspace, need, dev)
+    if given:
+        _on_stream(stream, (*outs, dS0), workspace, q, k, v, w, beta, dO, S0, dS_final, cu_seqlens)
     grads = KdaGdrGrads(*(_at(t) for t in outs), _at(dS0), *(KdaStride(*t.stride()[:3]) for t in outs))
     _call("kda_gdr_chunk_bwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(dO),
                                      ctypes.byref(sdo), _at(dS_final), ctypes.byref(grads), _at(workspace), need, stream.cuda_stream))
@@ -215,13 +220,14 @@ def gdr_decode(q, k, v, w, beta, S, slots=None, g_min: float = -5.0, *, scale: f
         _dense(slots, "slots", (desc.B,), torch.int32, dev)
     elif S.shape[0] < desc.B:
         raise ValueError(f"S has {S.shape[0]} states for {desc.B} rows")
+    given = stream is not None
+    stream, place = _stream_of(stream, dev)
     if out is None:
-        out = _like(v)
+        with place:
+            out = _like(v)
     so = _view(out, "out", v.shape, v.dtype, dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev.index)
-    else:
-        _on_stream(stream, out)
+    if given:
+        _on_stream(stream, (out, S), q, k, v, w, beta, slots)
     _call("kda_gdr_decode", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S), S.shape[0], _at(slots), ctypes.byref(desc), _at(out),
                                   ctypes.byref(so), stream.cuda_stream))
     return out
@@ -281,18 +287,19 @@ def norm_gate_fwd(x, weight=None, z=None, act: str = "silu", residual=None, alph
     second norm (y is None then).  x, z, residual: up to four dimensions, any strides with a contiguous
     last dimension, bf16 or fp32; weights [D], both bf16 or both fp32.  Asynchronous on `stream`."""
     desc, dev = _norm_inputs(x, weight, z, act, residual, alpha, next_weight, eps)
-    if s is None:
-        s = _like(x)
-    if next_weight is None:
-        y = None
-    elif y is None:
-        y = _like(x)
+    given = stream is not None
+    stream, place = _stream_of(stream, dev)
+    with place:
+        if s is None:
+            s = _like(x)
+        if next_weight is None:
+            y = None
+        elif y is None:
+            y = _like(x)
     ss = _rows(s, "s", x)
     sy = _rows(y, "y", x) if y is not None else ss
-    if stream is None:
-        stream = torch.cuda.current_stream(dev.index)
-    else:
-        _on_stream(stream, s, y)
+    if given:
+        _on_stream(stream, (s, y), x, weight, z, residual, next_weight)
     _call("kda_norm_fwd", dev, (_at(x), _at(weight), _at(z), _at(residual), _at(next_weight), ctypes.byref(desc), _at(s), ctypes.byref(ss),
                                 _at(y), ctypes.byref(sy), stream.cuda_stream))
     return s, y
@@ -309,18 +316,19 @@ def norm_gate_bwd(x, ds, dy=None, weight=None, z=None, act: str = "silu", residu
     if ds is None and next_weight is None:
         raise ValueError("ds is None")
     sds, sdy = (None if t is None else _rows(t, name, x) for t, name in ((ds, "ds"), (dy, "dy")))
-    dx = _like(x)
-    dz = _like(z) if z is not None else None
-    dres = _like(residual) if residual is not None else None
-    dw = torch.empty_like(weight) if weight is not None else None
-    dw2 = torch.empty_like(next_weight) if next_weight is not None else None
     need = _lib.load().kda_norm_bwd_workspace_bytes(ctypes.byref(desc))
     need = 0 if need == ctypes.c_size_t(-1).value else need
-    workspace = _workspace(workspace, need, dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev.index)
-    else:
-        _on_stream(stream, dx, dz, dres, dw, dw2, workspace)
+    given = stream is not None
+    stream, place = _stream_of(stream, dev)
+    with place:
+        dx = _like(x)
+        dz = _like(z) if z is not None else None
+        dres = _like(residual) if residual is not None else None
+        dw = torch.empty_like(weight) if weight is not None else None
+        dw2 = torch.empty_like(next_weight) if next_weight is not None else None
+        workspace = _workspace(workspace, need, dev)
+    if given:
+        _on_stream(stream, (dx, dz, dres, dw, dw2), workspace, x, ds, dy, weight, z, residual, next_weight)
     st = [KdaStride(0, 0, 0) if t is None else _row_strides(t) for t in (dx, dz, dres)]
     grads = KdaNormGrads(_at(dx), _at(dz), _at(dres), _at(dw), _at(dw2), *st)
     ref = lambda t: None if t is None else ctypes.byref(t)  # noqa: E731
