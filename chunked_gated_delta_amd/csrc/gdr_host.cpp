@@ -24,6 +24,8 @@ Span dense(const void* p, double bytes) {
 constexpr int64_t kMaxExtent = (int64_t)1 << 46;        // bytes
 constexpr int64_t kMaxTokenStride = (int64_t)1 << 25;   // bytes: the 64 rows of a chunk within 32 bits
 
+constexpr int64_t kMaxStride = 4 * kMaxExtent;          // bytes: no limit of its own
+
 // the span of a [B, H, T, D] view, D contiguous (strides already checked)
 Span view(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_t D, int64_t esz) {
   if (!p || B < 1 || H < 1 || T < 1) return Span{};
@@ -33,8 +35,10 @@ Span view(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_
 
 bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
 
-// strides of an input: not negative, in reach, each row `align` bytes apart from an aligned place
-int check_strides(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_t D, int64_t esz, int64_t align) {
+// strides of an input: not negative, in reach, each row `align` bytes apart from an aligned place, tokens at most
+// `most` bytes apart (the rule's kernels; the norms address every row in 64 bits)
+int check_strides(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_t D, int64_t esz, int64_t align,
+                  int64_t most = kMaxTokenStride) {
   if (!p) return KDA_OK;
   if (!aligned(p, (unsigned)align)) return KDA_ERR_ARG;
   const int64_t st[3] = {s.b, s.h, s.t}, n[3] = {B, H, T};
@@ -44,14 +48,15 @@ int check_strides(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T
     if (st[i] < 0 || st[i] > kMaxExtent || (st[i] * esz) % align != 0) return KDA_ERR_ARG;
     reach += (double)(n[i] - 1) * (double)st[i];
   }
-  if (T > 1 && s.t * esz > kMaxTokenStride) return KDA_ERR_ARG;
+  if (T > 1 && s.t * esz > most) return KDA_ERR_ARG;
   return reach * esz > (double)kMaxExtent ? KDA_ERR_SHAPE : KDA_OK;
 }
 
 // an output also may not hold one place twice: by stride, each step passes everything below it
-int check_out(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_t D, int64_t esz, int64_t align) {
+int check_out(const void* p, kda_stride_t s, int64_t B, int64_t H, int64_t T, int64_t D, int64_t esz, int64_t align,
+              int64_t most = kMaxTokenStride) {
   if (!p) return KDA_OK;
-  const int rc = check_strides(p, s, B, H, T, D, esz, align);
+  const int rc = check_strides(p, s, B, H, T, D, esz, align, most);
   if (rc != KDA_OK) return rc;
   int64_t st[3] = {s.b, s.h, s.t}, n[3] = {B, H, T};
   for (int i = 0; i < 3; ++i)
@@ -289,11 +294,11 @@ int kda_norm_fwd(const void* x, const void* weight, const void* z, const void* r
   if (!x || !s || !s_stride || (next_weight && (!y || !y_stride))) return KDA_ERR_NULL;
   if (!next_weight) y = nullptr;
   const kda_stride_t sy = y ? *y_stride : kda_stride_t{};
-  if ((rc = check_strides(x, d->x, B, H, T, D, e, e)) != KDA_OK) return rc;
-  if ((rc = check_strides(z, d->z, B, H, T, D, e, e)) != KDA_OK) return rc;
-  if ((rc = check_strides(residual, d->residual, B, H, T, D, e, e)) != KDA_OK) return rc;
-  if ((rc = check_out(s, *s_stride, B, H, T, D, e, e)) != KDA_OK) return rc;
-  if ((rc = check_out(y, sy, B, H, T, D, e, e)) != KDA_OK) return rc;
+  if ((rc = check_strides(x, d->x, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
+  if ((rc = check_strides(z, d->z, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
+  if ((rc = check_strides(residual, d->residual, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
+  if ((rc = check_out(s, *s_stride, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
+  if ((rc = check_out(y, sy, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
   if (!aligned(weight, (unsigned)we) || !aligned(next_weight, (unsigned)we)) return KDA_ERR_ARG;
   if ((rc = check_apart({view(x, d->x, B, H, T, D, e), view(z, d->z, B, H, T, D, e), view(residual, d->residual, B, H, T, D, e),
                          dense(weight, (double)D * we), dense(next_weight, (double)D * we)},
@@ -324,10 +329,10 @@ int kda_norm_bwd(const void* x, const void* weight, const void* z, const void* r
   void *dwt = weight ? g->dweight : nullptr, *dw2 = next_weight ? g->dnext_weight : nullptr;
   const struct { const void* p; kda_stride_t s; } ins[] = {{x, d->x}, {z, d->z}, {residual, d->residual}, {ds, sds}, {dy, sdy}};
   for (const auto& t : ins)
-    if ((rc = check_strides(t.p, t.s, B, H, T, D, e, e)) != KDA_OK) return rc;
+    if ((rc = check_strides(t.p, t.s, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
   const struct { const void* p; kda_stride_t s; } outs[] = {{g->dx, g->sx}, {dz, g->sz}, {dres, g->sresidual}};
   for (const auto& t : outs)
-    if ((rc = check_out(t.p, t.s, B, H, T, D, e, e)) != KDA_OK) return rc;
+    if ((rc = check_out(t.p, t.s, B, H, T, D, e, e, kMaxStride)) != KDA_OK) return rc;
   for (const void* q : {weight, next_weight, (const void*)dwt, (const void*)dw2})
     if (!aligned(q, (unsigned)we)) return KDA_ERR_ARG;
   kda::NormParams p{};
