@@ -168,7 +168,8 @@ size_t gdr_layout(GdrParams& p, void* base, bool bwd) {
 extern "C" {
 
 size_t kda_gdr_workspace_bytes(const kda_gdr_t* desc, int backward) {
-  if (!desc || check_gdr(desc, desc->n_seq != 0) != KDA_OK || desc->T == 0) return desc && desc->T == 0 ? 0 : (size_t)-1;
+  if (!desc || check_gdr(desc, desc->n_seq != 0) != KDA_OK) return (size_t)-1;
+  if (desc->T == 0) return 0;
   static const int32_t packed = 0;
   kda::GdrParams p = gdr_params(desc, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, desc->n_seq ? &packed : nullptr);
   return kda::gdr_layout(p, nullptr, backward != 0);
