@@ -88,8 +88,7 @@ int check_apart(std::initializer_list<Span> ins, std::initializer_list<Span> out
 bool head_dim(int64_t d) { return d == 32 || d == 64 || d == 128; }
 int64_t elem(int32_t dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
-// sizes, types and the gate; n_seq of the call in *n_seq.  Launch limits: a grid holds fewer than
-// 2^24 workgroups of 256 threads
+// sizes, types and the gate.  Launch limits: a grid holds fewer than 2^24 workgroups of 256 threads
 int check_gdr(const kda_gdr_t* d, bool packed) {
   if (!d) return KDA_ERR_NULL;
   if (d->B < 1 || d->Hk < 1 || d->Hv < 1 || d->T < 0 || d->dk < 1 || d->dv < 1) return KDA_ERR_SHAPE;
@@ -106,6 +105,15 @@ int check_gdr(const kda_gdr_t* d, bool packed) {
   if (slots >= (double)(1 << 24) || (double)n_seq * d->Hv * (d->dv / 16) >= (double)(1 << 23)) return KDA_ERR_SHAPE;
   if (slots * d->Hv * (double)(d->dk * d->dv) * 4.0 > (double)kMaxExtent) return KDA_ERR_SHAPE;
   return KDA_OK;
+}
+
+// and the launches of the chunked kernels, of 512 threads: a grid holds fewer than 2^23 of them
+int check_chunked(const kda_gdr_t* d, bool packed, bool bwd) {
+  const int rc = check_gdr(d, packed);
+  if (rc != KDA_OK) return rc;
+  const int64_t n_seq = packed ? d->n_seq : d->B, most = (int64_t)1 << 23;
+  if (kda::gdr_blocks(n_seq * d->Hv, (int)(d->dv / 16)) >= most) return KDA_ERR_SHAPE;
+  return bwd && kda::gdr_slots(d->B, d->T, n_seq, packed) >= most ? KDA_ERR_SHAPE : KDA_OK;
 }
 
 int check_gdr_inputs(const kda_gdr_t* d, const void* q, const void* k, const void* v, const void* w, const void* beta) {
@@ -168,7 +176,7 @@ size_t gdr_layout(GdrParams& p, void* base, bool bwd) {
 extern "C" {
 
 size_t kda_gdr_workspace_bytes(const kda_gdr_t* desc, int backward) {
-  if (!desc || check_gdr(desc, desc->n_seq != 0) != KDA_OK) return (size_t)-1;
+  if (!desc || check_chunked(desc, desc->n_seq != 0, backward != 0) != KDA_OK) return (size_t)-1;
   if (desc->T == 0) return 0;
   static const int32_t packed = 0;
   kda::GdrParams p = gdr_params(desc, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, desc->n_seq ? &packed : nullptr);
@@ -178,7 +186,7 @@ size_t kda_gdr_workspace_bytes(const kda_gdr_t* desc, int backward) {
 int kda_gdr_chunk_fwd(const void* q, const void* k, const void* v, const void* w, const void* beta, const float* S0,
                       const int32_t* seq_start, const kda_gdr_t* desc, void* o, const kda_stride_t* o_stride, float* S_final,
                       void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = check_gdr(desc, seq_start != nullptr);
+  int rc = check_chunked(desc, seq_start != nullptr, false);
   if (rc != KDA_OK) return rc;
   const int64_t B = desc->B, Hk = desc->Hk, Hv = desc->Hv, T = desc->T, dk = desc->dk, dv = desc->dv, e = elem(desc->dtype);
   if ((rc = check_gdr_inputs(desc, q, k, v, w, beta)) != KDA_OK) return rc;
@@ -205,7 +213,7 @@ int kda_gdr_chunk_bwd(const void* q, const void* k, const void* v, const void* w
                       const int32_t* seq_start, const kda_gdr_t* desc, const void* dO, const kda_stride_t* dO_stride,
                       const float* dS_final, const kda_gdr_grads_t* grads, void* workspace, size_t workspace_bytes,
                       void* stream) {
-  int rc = check_gdr(desc, seq_start != nullptr);
+  int rc = check_chunked(desc, seq_start != nullptr, true);
   if (rc != KDA_OK) return rc;
   if (!grads) return KDA_ERR_NULL;
   const int64_t B = desc->B, Hk = desc->Hk, Hv = desc->Hv, T = desc->T, dk = desc->dk, dv = desc->dv, e = elem(desc->dtype);
