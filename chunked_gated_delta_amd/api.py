@@ -6,9 +6,9 @@ A call with `stream` reads its inputs there: whoever wrote them on another strea
 one first, and whoever uses the results on another stream lets that one wait for `stream`."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
+from functools import partial
 
 import torch
 
@@ -45,33 +45,29 @@ def _check(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-_HERE = contextlib.nullcontext()
+def _on_stream(stream, call, *tensors):
+    """call() with `stream` current, and its results; `tensors` are what the caller gave it.
 
-
-def _stream_of(stream, dev):
-    """The stream of a call and the context in which the call allocates: the caching allocator hands out
-    memory whose earlier use was on the stream that is current, so what is written on `stream` is allocated
-    with that one current.  (A block freed on another stream may still be read or written there.)"""
-    if stream is None:
-        return torch.cuda.current_stream(dev.index), _HERE
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return stream, torch.cuda.stream(stream)
-
-
-def _on_stream(stream, results, *others):
-    """Tell torch's caching allocator which streams use a call's tensors, so that each may be dropped as
-    soon as the call returns: `stream` all of them, and the current one the results, whatever stream
-    they were allocated on."""
-    here = torch.cuda.current_stream(stream.device)
-    if stream == here:
-        return
-    for t in results:
-        if t is not None:
-            t.record_stream(here)
-    for t in (*results, *others):
-        if t is not None:
-            t.record_stream(stream)
+    The caching allocator hands out memory whose earlier use was on the current stream: what `stream` writes is
+    allocated with `stream` current, since a block that was freed on another stream may still be read or written
+    there.  Then it is told which streams use the call's tensors, `stream` all of them and the caller's current one
+    the results, so that each may be dropped as soon as the call returns."""
+    here = None
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.device.type == "cuda":
+            if t.device != stream.device:
+                raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+            here = here or torch.cuda.current_stream(stream.device)
+            if stream != here:
+                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        results = call()
+    if stream != here:
+        for t in results if isinstance(results, tuple) else (results,):
+            if t is not None:
+                t.record_stream(stream)   # one that the caller gave; nothing to a new one
+                t.record_stream(here)
+    return results
 
 
 def make_shape(B, H, T, dk, dv, dtype_code) -> KdaShape:
@@ -103,6 +99,11 @@ def chunk_fwd(q, k, v, w, beta, S0=None, g_min: float = -5.0, chunk: int = 16, *
     `force_fallback` = 1 (or True) gives every chunk a flagged chunk's handling, 2 the per-pair
     factors on every chunk; `disable_fallback` lets flagged chunks take the plain tiles.
     """
+    if stream is not None:
+        call = partial(chunk_fwd, q, k, v, w, beta, S0, g_min, chunk, out=out, S_final=S_final, stats=stats,
+                       workspace=workspace, disable_fallback=disable_fallback, force_fallback=force_fallback,
+                       path=path, events=events, seg_steps=seg_steps)
+        return _on_stream(stream, call, q, k, v, w, beta, S0, workspace)
     if q.dim() != 4:
         raise ValueError("q must be [B,H,T,dk]")
     B, H, T, dk = q.shape
@@ -118,25 +119,23 @@ def chunk_fwd(q, k, v, w, beta, S0=None, g_min: float = -5.0, chunk: int = 16, *
     _check(beta, "beta", (B, H, T), dt, dev)
     if S0 is not None:
         _check(S0, "S0", (B, H, dk, dv), torch.float32, dev)
-    if out is not None:
+    if out is None:
+        out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+    else:
         _check(out, "out", (B, H, T, dv), dt, dev)
-    if S_final is not None:
+    if S_final is None:
+        S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    else:
         _check(S_final, "S_final", (B, H, dk, dv), torch.float32, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
     opts = KdaOpts(int(bool(disable_fallback)), int(force_fallback), _PATHS[path], int(seg_steps),
                    events[0].handle if events else None, events[1].handle if events else None)
     plain = not (disable_fallback or force_fallback or path != "auto" or seg_steps or events)
     ws_need = _lib.workspace_bytes(shape, chunk, None if plain else opts)
-    stream, place = _stream_of(stream, dev)
-    with place:
-        if out is None:
-            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-        if S_final is None:
-            S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-        if workspace is None and ws_need > 0:
-            workspace = torch.empty(ws_need, dtype=torch.uint8, device=dev)
-        st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
-    _on_stream(stream, (out, S_final, st), workspace, q, k, v, w, beta, S0)
+    if workspace is None and ws_need > 0:
+        workspace = torch.empty(ws_need, dtype=torch.uint8, device=dev)
+    st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
+    stream = torch.cuda.current_stream(dev)
     ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(S0), ctypes.c_float(g_min), int(chunk),
             ctypes.byref(shape), _ptr(out), _ptr(S_final), _ptr(workspace), ws_len, _ptr(st),
@@ -160,6 +159,9 @@ def chunk_fwd_noalloc(q, k, v, w, beta, S0=None, g_min: float = -5.0, chunk: int
     chunk_fwd to the rounding of the two plans.  out, S_final and stats are allocated here when not
     given (the C entry point itself allocates nothing).  Calls that overlap in time on one GPU share
     that array and race."""
+    if stream is not None:
+        call = partial(chunk_fwd_noalloc, q, k, v, w, beta, S0, g_min, chunk, out=out, S_final=S_final, stats=stats)
+        return _on_stream(stream, call, q, k, v, w, beta, S0)
     if q.dim() != 4:
         raise ValueError("q must be [B,H,T,dk]")
     B, H, T, dk = q.shape
@@ -175,19 +177,17 @@ def chunk_fwd_noalloc(q, k, v, w, beta, S0=None, g_min: float = -5.0, chunk: int
     _check(beta, "beta", (B, H, T), dt, dev)
     if S0 is not None:
         _check(S0, "S0", (B, H, dk, dv), torch.float32, dev)
-    if out is not None:
+    if out is None:
+        out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+    else:
         _check(out, "out", (B, H, T, dv), dt, dev)
-    if S_final is not None:
+    if S_final is None:
+        S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    else:
         _check(S_final, "S_final", (B, H, dk, dv), torch.float32, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
-    stream, place = _stream_of(stream, dev)
-    with place:
-        if out is None:
-            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-        if S_final is None:
-            S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-        st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
-    _on_stream(stream, (out, S_final, st), q, k, v, w, beta, S0)
+    st = torch.empty(4, dtype=torch.int32, device=dev) if stats else None
+    stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
         rc = _lib.load().kda_chunk_fwd_noalloc(
             _ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(S0), ctypes.c_float(g_min), int(chunk),
@@ -210,6 +210,9 @@ def decode_stats(st: torch.Tensor) -> dict:
 
 def gate_prefix(w, g_min: float = -5.0, chunk: int = 16, stream=None):
     """Gate / in-chunk prefix stage alone: returns (g, G, span, flags) device tensors."""
+    if stream is not None:
+        call = partial(gate_prefix, w, g_min, chunk)
+        return _on_stream(stream, call, w)
     if not isinstance(w, torch.Tensor) or w.dim() != 4:
         raise ValueError("w must be a [B,H,T,dk] tensor")
     B, H, T, dk = w.shape
@@ -219,14 +222,12 @@ def gate_prefix(w, g_min: float = -5.0, chunk: int = 16, stream=None):
     _check(w, "w", (B, H, T, dk), w.dtype, dev)
     _dtype_code(w)
     NC = (T + chunk - 1) // chunk
+    g = torch.empty((B, H, T, dk), dtype=torch.float32, device=dev)
+    G = torch.empty_like(g)
+    span = torch.empty((B, H, NC), dtype=torch.float32, device=dev)
+    flags = torch.empty((B, H, NC), dtype=torch.uint8, device=dev)
     shape = make_shape(B, H, T, dk, dk, _dtype_code(w))
-    stream, place = _stream_of(stream, dev)
-    with place:
-        g = torch.empty((B, H, T, dk), dtype=torch.float32, device=dev)
-        G = torch.empty_like(g)
-        span = torch.empty((B, H, NC), dtype=torch.float32, device=dev)
-        flags = torch.empty((B, H, NC), dtype=torch.uint8, device=dev)
-    _on_stream(stream, (g, G, span, flags), w)
+    stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
         rc = _lib.load().kda_gate_prefix(_ptr(w), ctypes.c_float(g_min), int(chunk), ctypes.byref(shape),
                                          _ptr(g), _ptr(G), _ptr(span), _ptr(flags),
@@ -240,6 +241,9 @@ def decode(q, k, v, w, beta, S, g_min: float = -5.0, *, out=None, stream=None):
     """Recurrent decode through kda_decode: advances the fp32 state S [B,H,dk,dv] in place by the
     T tokens of q, k, w [B,H,T,dk], v [B,H,T,dv], beta [B,H,T] (T is typically 1) and returns
     o [B,H,T,dv].  Asynchronous on `stream` (default: the current torch stream)."""
+    if stream is not None:
+        call = partial(decode, q, k, v, w, beta, S, g_min, out=out)
+        return _on_stream(stream, call, q, k, v, w, beta, S)
     if q.dim() != 4:
         raise ValueError("q must be [B,H,T,dk]")
     B, H, T, dk = q.shape
@@ -254,14 +258,12 @@ def decode(q, k, v, w, beta, S, g_min: float = -5.0, *, out=None, stream=None):
     _check(v, "v", (B, H, T, dv), dt, dev)
     _check(beta, "beta", (B, H, T), dt, dev)
     _check(S, "S", (B, H, dk, dv), torch.float32, dev)
-    if out is not None:
+    if out is None:
+        out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
+    else:
         _check(out, "out", (B, H, T, dv), dt, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
-    stream, place = _stream_of(stream, dev)
-    with place:
-        if out is None:
-            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
-    _on_stream(stream, (out, S), q, k, v, w, beta)
+    stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
         rc = _lib.load().kda_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(S),
                                     ctypes.c_float(g_min), ctypes.byref(shape), _ptr(out),
@@ -278,6 +280,10 @@ def chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -5.0,
     (dq, dk, dv, dw, dbeta, dS0); dS0 is None when want_dS0 is False.  Asynchronous on `stream`.
     `events` = (begin, end) torch.cuda.Event pair recorded on `stream` around the library call (the
     library launches on that stream, so the pair brackets exactly its kernels)."""
+    if stream is not None:
+        call = partial(chunk_bwd, q, k, v, w, beta, dO, S0, dS_final, g_min, chunk, want_dS0=want_dS0,
+                       workspace=workspace, events=events)
+        return _on_stream(stream, call, q, k, v, w, beta, dO, S0, dS_final, workspace)
     if q.dim() != 4:
         raise ValueError("q must be [B,H,T,dk]")
     B, H, T, dk = q.shape
@@ -297,21 +303,19 @@ def chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -5.0,
     if dS_final is not None:
         _check(dS_final, "dS_final", (B, H, dk, dv), torch.float32, dev)
     shape = make_shape(B, H, T, dk, dv, _dtype_code(q))
-    need = _lib.bwd_workspace_bytes(shape, chunk)
-    if workspace is not None and workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {need} needed")
     f32 = dict(dtype=torch.float32, device=dev)
-    stream, place = _stream_of(stream, dev)
-    with place:
-        dq = torch.empty((B, H, T, dk), **f32)
-        dk_ = torch.empty((B, H, T, dk), **f32)
-        dv_ = torch.empty((B, H, T, dv), **f32)
-        dw = torch.empty((B, H, T, dk), **f32)
-        dbeta = torch.empty((B, H, T), **f32)
-        dS0 = torch.empty((B, H, dk, dv), **f32) if want_dS0 else None
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _on_stream(stream, (dq, dk_, dv_, dw, dbeta, dS0), workspace, q, k, v, w, beta, dO, S0, dS_final)
+    dq = torch.empty((B, H, T, dk), **f32)
+    dk_ = torch.empty((B, H, T, dk), **f32)
+    dv_ = torch.empty((B, H, T, dv), **f32)
+    dw = torch.empty((B, H, T, dk), **f32)
+    dbeta = torch.empty((B, H, T), **f32)
+    dS0 = torch.empty((B, H, dk, dv), **f32) if want_dS0 else None
+    need = _lib.bwd_workspace_bytes(shape, chunk)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {need} needed")
+    stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
         if events is not None:
             events[0].record(stream)

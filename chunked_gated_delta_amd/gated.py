@@ -10,12 +10,13 @@ from __future__ import annotations
 
 import ctypes
 import math
+from functools import partial
 
 import torch
 
 from . import _lib
 from ._lib import KdaError, KdaGdr, KdaGdrGrads, KdaNorm, KdaNormGrads, KdaStride
-from .api import _dtype_code, _on_stream, _stream_of
+from .api import _dtype_code, _on_stream
 
 _ACTS = {"sigmoid": 0, "silu": 1}
 
@@ -152,25 +153,25 @@ def gdr_chunk_fwd(q, k, v, w, beta, S0=None, g_min: float = -5.0, *, scale: floa
     divides T into packed sequences; tokens behind the last one are left as they were (undefined in an
     output that is allocated here).  S0, S_final: fp32 [sequences,Hv,dk,dv]; S_final may be S0 itself.
     Asynchronous on `stream` (default: the current torch stream)."""
+    if stream is not None:
+        call = partial(gdr_chunk_fwd, q, k, v, w, beta, S0, g_min, scale=scale, log_decay=log_decay,
+                       cu_seqlens=cu_seqlens, out=out, S_final=S_final, workspace=workspace)
+        return _on_stream(stream, call, q, k, v, w, beta, S0, cu_seqlens, workspace)
     n_seq = _sequences(cu_seqlens, q.device if isinstance(q, torch.Tensor) else None)
     desc, dev = _describe(q, k, v, w, beta, g_min, scale, log_decay, n_seq)
     states = (n_seq or desc.B, desc.Hv, desc.dk, desc.dv)
     if S0 is not None:
         _dense(S0, "S0", states, torch.float32, dev)
-    need = _need(desc, False)
-    given = stream is not None
-    stream, place = _stream_of(stream, dev)
-    with place:
-        if out is None:
-            out = _like(v)
-        if S_final is None:
-            S_final = torch.empty(states, dtype=torch.float32, device=dev)
-        else:
-            _dense(S_final, "S_final", states, torch.float32, dev)
-        workspace = _workspace(workspace, need, dev)
+    if out is None:
+        out = _like(v)
     so = _view(out, "out", v.shape, v.dtype, dev)
-    if given:
-        _on_stream(stream, (out, S_final), workspace, q, k, v, w, beta, S0, cu_seqlens)
+    if S_final is None:
+        S_final = torch.empty(states, dtype=torch.float32, device=dev)
+    else:
+        _dense(S_final, "S_final", states, torch.float32, dev)
+    need = _need(desc, False)
+    workspace = _workspace(workspace, need, dev)
+    stream = torch.cuda.current_stream(dev.index)
     _call("kda_gdr_chunk_fwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(out),
                                      ctypes.byref(so), _at(S_final), _at(workspace), need, stream.cuda_stream))
     return out, S_final
@@ -182,6 +183,10 @@ def gdr_chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -
     and dS_final = dL/dS_final (fp32, None for zero): (dq, dk, dv, dw, dbeta, dS0), each of its input's shape
     and type, dS0 fp32 (None when want_dS0 is False).  The gradient of a broadcast input comes at the
     broadcast shape; tokens of no sequence are left undefined.  Asynchronous on `stream`."""
+    if stream is not None:
+        call = partial(gdr_chunk_bwd, q, k, v, w, beta, dO, S0, dS_final, g_min, scale=scale, log_decay=log_decay,
+                       cu_seqlens=cu_seqlens, want_dS0=want_dS0, workspace=workspace)
+        return _on_stream(stream, call, q, k, v, w, beta, dO, S0, dS_final, cu_seqlens, workspace)
     n_seq = _sequences(cu_seqlens, q.device if isinstance(q, torch.Tensor) else None)
     desc, dev = _describe(q, k, v, w, beta, g_min, scale, log_decay, n_seq)
     states = (n_seq or desc.B, desc.Hv, desc.dk, desc.dv)
@@ -190,15 +195,11 @@ def gdr_chunk_bwd(q, k, v, w, beta, dO, S0=None, dS_final=None, g_min: float = -
         _dense(S0, "S0", states, torch.float32, dev)
     if dS_final is not None:
         _dense(dS_final, "dS_final", states, torch.float32, dev)
+    outs = [_like(q), _like(k), _like(v), _like(w, rows=False), _like(beta, rows=False)]
+    dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
     need = _need(desc, True)
-    given = stream is not None
-    stream, place = _stream_of(stream, dev)
-    with place:
-        outs = [_like(q), _like(k), _like(v), _like(w, rows=False), _like(beta, rows=False)]
-        dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
-        workspace = _workspace(workspace, need, dev)
-    if given:
-        _on_stream(stream, (*outs, dS0), workspace, q, k, v, w, beta, dO, S0, dS_final, cu_seqlens)
+    workspace = _workspace(workspace, need, dev)
+    stream = torch.cuda.current_stream(dev.index)
     grads = KdaGdrGrads(*(_at(t) for t in outs), _at(dS0), *(KdaStride(*t.stride()[:3]) for t in outs))
     _call("kda_gdr_chunk_bwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(dO),
                                      ctypes.byref(sdo), _at(dS_final), ctypes.byref(grads), _at(workspace), need, stream.cuda_stream))
@@ -212,6 +213,9 @@ def gdr_decode(q, k, v, w, beta, S, slots=None, g_min: float = -5.0, *, scale: f
     `slots` (int32 [B], on the GPU) names each row's state (None: row b has state b); a row with a slot
     outside the pool (-1, say) is padding and gets zeros; rows with the same slot are that state's
     successive tokens, in row order.  Asynchronous on `stream` (default: the current torch stream)."""
+    if stream is not None:
+        call = partial(gdr_decode, q, k, v, w, beta, S, slots, g_min, scale=scale, log_decay=log_decay, out=out)
+        return _on_stream(stream, call, q, k, v, w, beta, S, slots)
     desc, dev = _describe(q, k, v, w, beta, g_min, scale, log_decay, 0)
     if not isinstance(S, torch.Tensor) or S.dim() != 4:
         raise ValueError("S must be a [n_slots,Hv,dk,dv] tensor")
@@ -220,14 +224,10 @@ def gdr_decode(q, k, v, w, beta, S, slots=None, g_min: float = -5.0, *, scale: f
         _dense(slots, "slots", (desc.B,), torch.int32, dev)
     elif S.shape[0] < desc.B:
         raise ValueError(f"S has {S.shape[0]} states for {desc.B} rows")
-    given = stream is not None
-    stream, place = _stream_of(stream, dev)
     if out is None:
-        with place:
-            out = _like(v)
+        out = _like(v)
     so = _view(out, "out", v.shape, v.dtype, dev)
-    if given:
-        _on_stream(stream, (out, S), q, k, v, w, beta, slots)
+    stream = torch.cuda.current_stream(dev.index)
     _call("kda_gdr_decode", dev, (_at(q), _at(k), _at(v), _at(w), _at(beta), _at(S), S.shape[0], _at(slots), ctypes.byref(desc), _at(out),
                                   ctypes.byref(so), stream.cuda_stream))
     return out
@@ -286,20 +286,19 @@ def norm_gate_fwd(x, weight=None, z=None, act: str = "silu", residual=None, alph
     weight None leaves x as it is, z None leaves out the gate, residual None the sum, next_weight None the
     second norm (y is None then).  x, z, residual: up to four dimensions, any strides with a contiguous
     last dimension, bf16 or fp32; weights [D], both bf16 or both fp32.  Asynchronous on `stream`."""
+    if stream is not None:
+        call = partial(norm_gate_fwd, x, weight, z, act, residual, alpha, next_weight, eps, s=s, y=y)
+        return _on_stream(stream, call, x, weight, z, residual, next_weight)
     desc, dev = _norm_inputs(x, weight, z, act, residual, alpha, next_weight, eps)
-    given = stream is not None
-    stream, place = _stream_of(stream, dev)
-    with place:
-        if s is None:
-            s = _like(x)
-        if next_weight is None:
-            y = None
-        elif y is None:
-            y = _like(x)
+    if s is None:
+        s = _like(x)
+    if next_weight is None:
+        y = None
+    elif y is None:
+        y = _like(x)
     ss = _rows(s, "s", x)
     sy = _rows(y, "y", x) if y is not None else ss
-    if given:
-        _on_stream(stream, (s, y), x, weight, z, residual, next_weight)
+    stream = torch.cuda.current_stream(dev.index)
     _call("kda_norm_fwd", dev, (_at(x), _at(weight), _at(z), _at(residual), _at(next_weight), ctypes.byref(desc), _at(s), ctypes.byref(ss),
                                 _at(y), ctypes.byref(sy), stream.cuda_stream))
     return s, y
@@ -310,25 +309,24 @@ def norm_gate_bwd(x, ds, dy=None, weight=None, z=None, act: str = "silu", residu
     """Gradients of norm_gate_fwd through kda_norm_bwd, given ds = dL/ds (None for zero, with next_weight) and
     dy = dL/dy (with next_weight): (dx, dweight, dz, dresidual, dnext_weight), None for what was not given;
     rows' gradients in x's type, weights' in the weights'.  Asynchronous on `stream`."""
+    if stream is not None:
+        call = partial(norm_gate_bwd, x, ds, dy, weight, z, act, residual, alpha, next_weight, eps, workspace=workspace)
+        return _on_stream(stream, call, x, ds, dy, weight, z, residual, next_weight, workspace)
     desc, dev = _norm_inputs(x, weight, z, act, residual, alpha, next_weight, eps)
     if (dy is None) != (next_weight is None):
         raise ValueError("dy is given exactly when next_weight is")
     if ds is None and next_weight is None:
         raise ValueError("ds is None")
     sds, sdy = (None if t is None else _rows(t, name, x) for t, name in ((ds, "ds"), (dy, "dy")))
+    dx = _like(x)
+    dz = _like(z) if z is not None else None
+    dres = _like(residual) if residual is not None else None
+    dw = torch.empty_like(weight) if weight is not None else None
+    dw2 = torch.empty_like(next_weight) if next_weight is not None else None
     need = _lib.load().kda_norm_bwd_workspace_bytes(ctypes.byref(desc))
     need = 0 if need == ctypes.c_size_t(-1).value else need
-    given = stream is not None
-    stream, place = _stream_of(stream, dev)
-    with place:
-        dx = _like(x)
-        dz = _like(z) if z is not None else None
-        dres = _like(residual) if residual is not None else None
-        dw = torch.empty_like(weight) if weight is not None else None
-        dw2 = torch.empty_like(next_weight) if next_weight is not None else None
-        workspace = _workspace(workspace, need, dev)
-    if given:
-        _on_stream(stream, (dx, dz, dres, dw, dw2), workspace, x, ds, dy, weight, z, residual, next_weight)
+    workspace = _workspace(workspace, need, dev)
+    stream = torch.cuda.current_stream(dev.index)
     st = [KdaStride(0, 0, 0) if t is None else _row_strides(t) for t in (dx, dz, dres)]
     grads = KdaNormGrads(_at(dx), _at(dz), _at(dres), _at(dw), _at(dw2), *st)
     ref = lambda t: None if t is None else ctypes.byref(t)  # noqa: E731
