@@ -17,7 +17,8 @@
 // dE come in two bf16 planes, dP and dA are made of two (off by 2^-17): with one plane of each, 2x4096 tokens' kernel
 // took 164 us, but dk and dw were off by up to 3.6e-3 where the rounding of the results is 1.7e-3.
 //
-// 2 x 4096 tokens, 16 heads of 128 x 128 in bf16: 212 us for 0.6 GB.  One workgroup fills a compute unit's LDS, so half
+// 2 x 4096 tokens, 16 heads of 128 x 128 in bf16: 211 to 227 us for 0.6 GB.  At 128 x 128 all 256 registers are used and 25
+// more spilled (22 in fp32); no smaller size spills.  One workgroup fills a compute unit's LDS, so half
 // of its cycles wait for the loads (all compute units ask at once) and the other half use none of the bandwidth; where
 // value heads share a key head, the next one's operands are asked for before the last sums of the one before.
 #include <type_traits>

@@ -9,14 +9,13 @@
 //    state's rows, in registers (fp32 matrix-core results).  Wavefronts 4-7, one more on each SIMD, form the
 //    outputs (or, in the backward's run, write out the entering states and F) in the chain's shadow, and move
 //    v, o and the gates in rows of 16 bytes a lane, turning them in LDS.
-//  - A compute unit gets about 20 bytes a cycle from L2, whatever is asked for (80 requests of 128 bytes under
-//    way at 500 cycles each), so a step's bytes matter: K is loaded once, as whole rows, and LDS gives both
-//    its row and its transposed operands; loads are spread over the three parts of a step and issued as
+//  - A step's bytes matter too (62 KiB, 19 a cycle for a compute unit): K is loaded once, as whole rows, and LDS
+//    gives both its row and its transposed operands; loads are spread over the three parts of a step and issued as
 //    soon as the registers they go to are free, one step ahead.  Loads past the last chunk are clamped to it.
 //  - What the wavefronts exchange (the state, E, U: 16 columns each) goes through LDS as ready B operands.
-// 64K tokens of 16 heads (dk = dv = 128, bf16): 1.42 ms, 3250 cycles for a step of 64 tokens, of which the chain's own
-// work is 2500 and the step's 62 KiB at 20 bytes a cycle 3100.  32 columns a workgroup: 4400 cycles, with half the
-// workgroups; two workgroups a compute unit (128 registers) spill and take 2.8 ms.
+// 64K tokens of 16 heads (dk = dv = 128, bf16): 1.42 ms, 3250 cycles for a step of 64 tokens, of which the chain's
+// wavefronts work 2500 to 2900 and wait for the serving ones or for each other the rest.  32 columns a workgroup:
+// 4400 cycles, with half the workgroups; two workgroups a compute unit (128 registers) spill and take 2.8 ms.
 // Rows behind the sequence's end read its last row; their E is set to zero, so nothing of them reaches
 // the state, and their outputs are not written.
 #include <type_traits>
@@ -35,7 +34,7 @@ __device__ __forceinline__ float value(float x) { return x; }
 
 // Writes `rows` contraction places x 16 columns of B operands to memory, place by place, bf16 in two planes of `plane`
 // values: a lane takes 8 columns of one place.  A workgroup's 16 columns lie together there (as 32 bytes of rows of
-// all columns, 2x4096 tokens' two chains took ROWMAJOR).  bf16: transposing reads, in which 16 lanes read 16 places
+// all columns, 2x4096 tokens' two chains took 126 and 220 us in place of 109 and 201).  bf16: transposing reads, in which 16 lanes read 16 places
 // of 4 columns and get one place's 4 columns each.
 template <typename T>
 __device__ __forceinline__ void write_rows(const char* frags, int frag_bytes, int rows, GlobalPtr<T> out, int64_t plane, int tid) {
@@ -418,9 +417,10 @@ __global__ __launch_bounds__(512, kScanWaves) void gdr_scan_kernel(GdrParams p) 
 //   |  dS <- e^{G_last} dS + Q^T (scale gam dO) - K^T (gam dE)
 // Wavefronts 0-3 walk the chain; wavefronts 4-7 form P^T dO and Q^T (scale gam dO) of the chunk that comes
 // next, which do not depend on it, and write out dS of each chunk's end for the gradient kernel.  The
-// chain leaves, per 16 columns, the sums of dU F that make beta's gradient.  2 x 4096 tokens of 16 heads: 200 us, bound
-// by a step's 88 KiB (without the 18 of P^T it took 158 in place of 192; formed by the preparation kernel instead,
-// P^T dO cost that kernel 23 us more and saved 17 here).
+// chain leaves, per 16 columns, the sums of dU F that make beta's gradient.  2 x 4096 tokens of 16 heads: 204 us.
+// The serving wavefronts set the pace: of a step's 5900 cycles they work about 5000, wavefronts 0-3 about 2900.
+// (At 192 us, a copy without P^T's loads and products took 158; formed by the preparation kernel instead, P^T dO cost
+// that kernel 23 us more and saved 17 here.)
 template <typename T, int DK>
 __global__ __launch_bounds__(512, kScanWaves) void gdr_rscan_kernel(GdrParams p) {
   using In = typename Frags<T>::In;

@@ -9,7 +9,11 @@
 // The backward recomputes the row's forward from the same inputs (it reads the residual in place of s: as
 // many bytes, and exact), and sums the weights' gradients over the rows a workgroup takes, in registers;
 // the workgroups' sums are added up by a second kernel in a fixed order.  Each workgroup more is one more row for that
-// kernel: 512 of them, two a compute unit.  131072 gated rows of 128 in bf16: 168 MB in 50 + 4 us.
+// kernel: 512 of them, two a compute unit.  131072 gated rows of 128 in bf16: 168 MB in 50 + 5 us; both norms, gate and
+// residual, bf16: 8192 rows of 4096 (537 MB) 238 + 8 us, 4096 of 8192 288 + 13.  Rows of more than 4096 values with both norms do
+// not fit 256 registers: 16 are spilled up to 8192 values, 284 to 306 above, and on the path of single values (an odd
+// size or alignment) 128 to 132 and 625 to 629, so 4096 rows of 8191 take 918 + 16 us.  One norm above 8192 values spills 4 to 6, or
+// 128 on the path of single values.
 #include "gdr_internal.h"
 
 namespace kda {

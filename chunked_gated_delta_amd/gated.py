@@ -285,7 +285,8 @@ def norm_gate_fwd(x, weight=None, z=None, act: str = "silu", residual=None, alph
 
     weight None leaves x as it is, z None leaves out the gate, residual None the sum, next_weight None the
     second norm (y is None then).  x, z, residual: up to four dimensions, any strides with a contiguous
-    last dimension, bf16 or fp32; weights [D], both bf16 or both fp32.  Asynchronous on `stream`."""
+    last dimension, bf16 or fp32; weights [D], both bf16 or both fp32; s and y apart from every input (the
+    residual is not updated in place).  Asynchronous on `stream`."""
     if stream is not None:
         call = partial(norm_gate_fwd, x, weight, z, act, residual, alpha, next_weight, eps, s=s, y=y)
         return _on_stream(stream, call, x, weight, z, residual, next_weight)

@@ -334,7 +334,9 @@ KDA_API int kda_gdr_decode(const void* q, const void* k, const void* v, const vo
  * at least one of the two norms being there.  The gated norm of a delta rule's heads is (weight, z); a
  * residual add with the next block's norm is (residual, next_weight); a block normed on both sides has
  * all.  Rows are [B,H,T] places of strided tensors of dtype, any strides and alignment of the type;
- * weights are dense, of wdtype.  Sums and norms in fp32; y is taken from s before its rounding. */
+ * weights are dense, of wdtype.  An output may not hold one place twice, nor reach into the span of an input or of
+ * another output (so the residual is not updated in place).  Sums and norms in fp32; y is taken from s before its
+ * rounding. */
 #define KDA_NORM_MAX_D 16384
 
 typedef enum { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_act_t;
