@@ -144,3 +144,25 @@ def test_a_stream_of_its_own_device(name):
 
     with pytest.raises(ValueError, match="stream is on"):
         call(make_inputs(), Elsewhere())
+
+
+@pytest.mark.parametrize("name", ["chunk_fwd", "chunk_bwd", "gdr_chunk_fwd", "gdr_chunk_bwd", "norm_gate_bwd"])
+def test_captured_on_a_stream_that_forks_off(name):
+    """A call on a second stream inside a captured graph, replayed with eager work between."""
+    make_inputs, call = CALLS[name]
+    say(f"[case] {name} on a forked stream of a graph")
+    d = make_inputs()
+    ref = [x.clone() for x in call(d, None)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = call(d, side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(4):
+        for x in out:
+            x.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, ref)
+        assert same(call(d, None), ref)   # the program's own calls between replays
