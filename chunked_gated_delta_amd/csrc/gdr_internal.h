@@ -218,22 +218,9 @@ template <typename T> constexpr int in_frag() { return Frags<T>::in_planes * kPl
 template <typename T, int N> constexpr int op_frag() { return Frags<T>::planes(N) * kPlane; }
 
 __device__ __forceinline__ floatx4 mma(bf16x8 a, bf16x8 b, floatx4 c) { return mfma(a, b, c); }
-template <int N> __device__ __forceinline__ floatx4 mma(bf16x8 a, const Planes<N>& b, floatx4 c) {
-#pragma unroll
-  for (int i = N - 1; i >= 0; --i) c = mfma(a, b.p[i], c);
-  return c;
-}
 template <int N> __device__ __forceinline__ floatx4 mma(const Planes<N>& a, bf16x8 b, floatx4 c) {
 #pragma unroll
   for (int i = N - 1; i >= 0; --i) c = mfma(a.p[i], b, c);
-  return c;
-}
-// both in planes: the products that lie above the last plane's size
-template <int N> __device__ __forceinline__ floatx4 mma(const Planes<N>& a, const Planes<N>& b, floatx4 c) {
-#pragma unroll
-  for (int s = N - 1; s >= 0; --s)
-#pragma unroll
-    for (int i = 0; i <= s; ++i) c = mfma(a.p[i], b.p[s - i], c);
   return c;
 }
 __device__ __forceinline__ floatx4 mma(const float8v& a, const float8v& b, floatx4 c) {

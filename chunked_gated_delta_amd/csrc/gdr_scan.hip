@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kScanWaves = 2;   // wavefronts a SIMD that the registers are to allow
 
-__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ float value(float x) { return x; }
 
