@@ -2,7 +2,8 @@
 around a block.  Argument marshalling only, as in api.py: the computation is in the library's HIP kernels.
 
 Tensors may be strided views with a contiguous last dimension, so [B,T,H,D] projections are passed as
-x.transpose(1, 2) and slices of a fused projection as they are; nothing is copied.
+x.transpose(1, 2) and slices of a fused projection as they are; nothing is copied.  The rule's q, k, v, o and dO have
+their rows on 16-byte places and their tokens at most 32 MiB apart; the norms' rows may lie anywhere.
 
 A call with `stream` reads its inputs there: whoever wrote them on another stream lets `stream` wait for that
 one first, and whoever uses the results on another stream lets that one wait for `stream`."""
