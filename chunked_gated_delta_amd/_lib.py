@@ -67,6 +67,27 @@ class KdaNormGrads(ctypes.Structure):
         [(n, KdaStride) for n in ("sx", "sz", "sresidual")]
 
 
+class KdaLad(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "Hk", "Hv", "T", "dk", "dv", "n_seq")] + \
+        [("dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("w_per_head", ctypes.c_int32), ("g_min", ctypes.c_float),
+         ("scale", ctypes.c_float)] + [(n, KdaStride) for n in ("q", "k", "v", "w")]
+
+
+class KdaLadGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dq", "dk", "dv", "dw", "dS0")] + [(n, KdaStride) for n in ("sq", "sk", "sv", "sw")]
+
+
+class KdaQkNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "Hq", "Hk", "T", "D", "R")] + \
+        [(n, ctypes.c_int32) for n in ("dtype", "wdtype", "norm", "interleaved", "wide_positions")] + \
+        [(n, ctypes.c_float) for n in ("q_scale", "k_scale", "eps")] + [("pos_b", ctypes.c_int64), ("pos_t", ctypes.c_int64)] + \
+        [(n, KdaStride) for n in ("q", "k")]
+
+
+class KdaQkNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dq", "dk", "dq_weight", "dk_weight")] + [(n, KdaStride) for n in ("sq", "sk")]
+
+
 class KdaError(RuntimeError):
     def __init__(self, code: int, where: str, hip_text: str = ""):
         self.code = code
@@ -128,6 +149,21 @@ def load():
     lib.kda_norm_bwd.restype = i32
     lib.kda_norm_bwd_workspace_bytes.argtypes = [norm]
     lib.kda_norm_bwd_workspace_bytes.restype = sz
+    lad, qk = ctypes.POINTER(KdaLad), ctypes.POINTER(KdaQkNorm)
+    lib.kda_lad_chunk_fwd.argtypes = [vp] * 6 + [lad, vp, st, vp, vp, sz, vp]
+    lib.kda_lad_chunk_fwd.restype = i32
+    lib.kda_lad_chunk_bwd.argtypes = [vp] * 6 + [lad, vp, st, vp, ctypes.POINTER(KdaLadGrads), vp, sz, vp]
+    lib.kda_lad_chunk_bwd.restype = i32
+    lib.kda_lad_workspace_bytes.argtypes = [lad, i32]
+    lib.kda_lad_workspace_bytes.restype = sz
+    lib.kda_lad_decode.argtypes = [vp] * 5 + [i64, vp, lad, vp, st, vp]
+    lib.kda_lad_decode.restype = i32
+    lib.kda_qk_norm_fwd.argtypes = [vp] * 6 + [qk, vp, st, vp, st, vp]
+    lib.kda_qk_norm_fwd.restype = i32
+    lib.kda_qk_norm_bwd.argtypes = [vp] * 6 + [qk, vp, st, vp, st, ctypes.POINTER(KdaQkNormGrads), vp, sz, vp]
+    lib.kda_qk_norm_bwd.restype = i32
+    lib.kda_qk_norm_bwd_workspace_bytes.argtypes = [qk]
+    lib.kda_qk_norm_bwd_workspace_bytes.restype = sz
     lib.kda_strerror.argtypes = [i32]
     lib.kda_strerror.restype = ctypes.c_char_p
     lib.kda_last_hip_error.argtypes = []

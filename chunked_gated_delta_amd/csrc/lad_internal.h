@@ -1,0 +1,177 @@
+// Internal declarations of linear attention with a decay for each head.
+//
+// One walk does everything: with a state S (DX x DZ) and rows X, Y (DX values) and Z (DZ values),
+//     S <- e^{g_t} S + Y_t Z_t^T;   out_t = S^T X_t
+// is the forward with (X, Y, Z) = (q, k, v) and gives dq with (dO, v, k); backwards in time, with the
+// decay taken behind the output, it gives dk with (v, dO, q) and dv with (k, q, dO).  In chunks of C = 64 tokens
+// in the walk's order, P the prefix of the log-decays in the chunk (inclusive forwards, exclusive backwards):
+//     out_i = e^{P_i} X_i S + sum_{j <= i} e^{P_i - P_j} (X_i . Y_j) Z_j
+//     S <- e^{Ptot} S + sum_j e^{Ptot - P_j} Y_j Z_j^T
+// Every exponent is at most 0, and one decay a head keeps it out of the bf16 operands of X Y^T.
+//
+// Long sequences are cut into segments of L tokens that walk side by side: a first launch forms each segment's
+// state from zero, a second chains them (S entering segment i + 1 = e^{decay of i} S entering i + that state).
+#pragma once
+
+#include "gdr_internal.h"
+
+namespace kda {
+
+struct LadWalk {
+  const void *x, *y, *z, *dot;              // rows; dot (nullable): dots[t] = out_t . dot_t
+  kda_stride_t sx, sy, sz, sdot;
+  int grp_x, grp_y, grp_z, grp_dot;         // value heads that share a head of the tensor
+  void* out;
+  kda_stride_t so;
+  const float* entering;                    // per (slot, head) with by_slot, else per (sequence, head); null: zero
+  float* leaving;                           // per (slot, head) with leave_slot, else per (sequence, head), behind the walk's last segment; nullable
+  float* decay;                             // e^{the segment's decay} per (slot, head); nullable
+  float* dots;                              // [B, Hv, T]
+  float out_scale, in_scale;                // of the outputs, and of Z in outputs and state
+  int reverse, transposed, by_slot, leave_slot, out_f32, skip_end;   // transposed: states lie as [DZ][DX]; skip_end: no walk over the segment
+                                                         // behind which none comes
+};
+
+struct LadParams {
+  LadWalk walk[3];
+  int n_walks;
+  const void* w;
+  kda_stride_t sw;
+  int w_per_head, gate;
+  float g_min;
+  const int32_t* seq_start;                 // packed sequences: n_seq + 1 offsets; null: every batch row is one
+  int64_t T, L, n_seq, slots;
+  int Hv, grp;
+};
+
+// chains the segments' states: S (forwards) and its adjoint R (backwards)
+struct LadScan {
+  float *s, *r;                             // per (slot, head): in: the segment's own state; out: the one entering it (r: from behind)
+  const float *s_decay, *r_decay;
+  const float *S0, *dSf;                    // nullable
+  float *S_final, *dS0;                     // per (sequence, head); nullable
+  const int32_t* seq_start;
+  int64_t T, L, n_seq;
+  int Hv, size, first, dirs;                // size = dk dv; directions first .. first + dirs - 1 (0 forwards, 1 its adjoint)
+};
+
+// the log-decay's gradient from dots of q.dq and k.dk
+struct LadDecayGrad {
+  const float *qdq, *kdk;                   // [B, Hv, T]
+  const float *s, *r;                       // entering states of the segments (null: one segment a sequence)
+  const float *S_final, *dSf;               // per (sequence, head); dSf nullable
+  const void* w;
+  kda_stride_t sw, sdw;
+  void* dw;
+  double* partial;                          // per (slot, head), of w per head
+  const int32_t* seq_start;
+  int64_t T, L, n_seq, slots;
+  int Hv, size, w_per_head, gate, dtype;
+  float g_min;
+};
+
+// dq or dk from the value heads that share it
+struct LadSum {
+  const float* part[2];                     // [B, Hk, grp, T, D]
+  void* out[2];                             // dq, dk
+  kda_stride_t so[2];
+  const int32_t* seq_start;
+  int64_t B, T, n_seq;
+  int Hk, grp, D, dtype;
+};
+
+struct LadStepParams {
+  const void *q, *k, *v, *w;
+  kda_stride_t sq, sk, sv, sw, so;
+  const int32_t* slots;
+  float* S;
+  void* o;
+  int64_t B, T, n_slots;
+  int Hk, Hv, dk, dv;
+  int dtype, gate, w_per_head;
+  float g_min, scale;
+};
+
+struct QkNormParams {
+  const void *x[2], *weight[2], *dy[2];     // queries, keys
+  void *y[2], *dx[2], *dweight[2];
+  kda_stride_t sx[2], sy[2], sdy[2], sdx[2];
+  const void* positions;
+  const float* inv_freq;
+  int64_t pos_b, pos_t, B, T;
+  int H[2], D, R, dtype, wdtype, norm, interleaved, wide;
+  float scale[2], eps;
+  float* partial;
+};
+
+// segment length, and the number of slots that segments of it need
+int64_t lad_segment(int64_t B, int64_t T, int64_t n_seq, int Hv, bool packed, bool bwd);
+int64_t lad_slots(int64_t B, int64_t T, int64_t n_seq, int64_t L, bool packed);
+
+// the walks of p over every segment; states: only their states (no outputs)
+hipError_t launch_lad_fwd(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
+hipError_t launch_lad_bwd(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
+hipError_t launch_lad_states(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
+hipError_t launch_lad_scan(const LadScan& p, hipStream_t s);
+hipError_t launch_lad_decay_grad(const LadDecayGrad& p, hipStream_t s);
+hipError_t launch_lad_sum(const LadSum& p, hipStream_t s);
+hipError_t launch_lad_step(const LadStepParams& p, hipStream_t s);
+size_t qk_norm_bwd_workspace_bytes(const QkNormParams& p);
+hipError_t launch_qk_norm_fwd(const QkNormParams& p, hipStream_t s);
+hipError_t launch_qk_norm_bwd(const QkNormParams& p, hipStream_t s);
+
+// ---------------------------------------------------------------- segments
+
+struct LadSeg {
+  int64_t seq, row, t0, len, seg, n_seg, slot0;   // sequence, batch row, its first token, its tokens; segment of it, segments, first slot
+};
+
+// A sequence of len tokens has max(1, ceil(len / L)) segments; packed ones keep them at slot floor(start / L) +
+// sequence, which leaves room for every sequence's last one without a prefix sum over the lengths.  Offsets are
+// clamped into [0, T], so that offsets out of order address nothing out of range.
+__device__ __forceinline__ LadSeg lad_seq(const int32_t* seq_start, int64_t T, int64_t L, int64_t s) {
+  LadSeg q;
+  q.seq = s;
+  q.seg = 0;
+  if (!seq_start) {
+    q.row = s;
+    q.t0 = 0;
+    q.len = T;
+    q.n_seg = T > L ? (T + L - 1) / L : 1;
+    q.slot0 = s * q.n_seg;
+  } else {
+    const int64_t a = clamp_off(seq_start[s], 0, T), e = clamp_off(seq_start[s + 1], a, T);
+    q.row = 0;
+    q.t0 = a;
+    q.len = e - a;
+    q.n_seg = q.len > L ? (q.len + L - 1) / L : 1;
+    q.slot0 = a / L + s;
+  }
+  return q;
+}
+
+// the segment at this slot; false where the slot holds none
+__device__ __forceinline__ bool lad_find(const int32_t* seq_start, int64_t T, int64_t L, int64_t n_seq, int64_t slot, LadSeg* out) {
+  int64_t lo = 0;
+  if (!seq_start) {
+    lo = slot / (T > L ? (T + L - 1) / L : 1);
+  } else {
+    int64_t hi = n_seq - 1;   // the last sequence whose first slot is not behind this one
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) / 2;
+      if (clamp_off(seq_start[mid], 0, T) / L + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+  }
+  *out = lad_seq(seq_start, T, L, lo);
+  out->seg = slot - out->slot0;
+  return out->seg >= 0 && out->seg < out->n_seg;
+}
+
+// log-decay of one token
+template <typename T>
+__device__ __forceinline__ float lad_decay(const void* w, int per_head, kda_stride_t sw, int64_t row, int h, int64_t t, int gate, float g_min) {
+  const float x = per_head ? global_in<float>(w)[h] : get(global_in<T>(w) + row * sw.b + h * sw.h + t * sw.t);
+  return gdr_gate(x, gate, g_min);
+}
+
+}  // namespace kda

@@ -1,0 +1,456 @@
+// The walk of linear attention with a decay for each head over one segment (lad_internal.h has the mathematics).
+//
+// A workgroup owns one (segment, value head) and holds its whole state in registers, in fp32: DZ / 32 wavefronts
+// of 32 Z columns each.  Per chunk of 64 tokens, X, Y and Z rows go through LDS once; row tile i of X Y^T
+// is formed by wavefront i mod (DZ / 32), decayed, and shared through LDS as planes; then each wavefront forms its
+// 32 columns of the outputs and of the new state.
+//
+// Layouts (lane = 16 g + li).  Products give D tiles: rows 4g .. 4g + 3, column li.  They are formed transposed
+// (keys or Z columns along the rows, tokens along the columns), so that
+//  - the state's tiles (rows: X channels, columns: Z columns) are operands of the outputs as they lie in registers,
+//    with the contraction places of a step of 32 channels in the order {4g + r, 16 + 4g + r};
+//  - the tiles of Y X^T (rows: keys) are operands of the products with Z, lane by lane;
+//  - a lane has 8 consecutive Z columns of one token: tile c (0, 1) of a wavefront has column 8 (m / 4) + 4 c + m % 4
+//    at place m, one 16-byte access of bf16.
+// Key tile j has token 16 j + sigma(m) at place m, sigma(m) = 2 m (m < 8), 2 (m - 8) + 1 (m >= 8): with rows 4 banks
+// apart modulo 64, the 8 rows that half a wavefront's transposing read touches then lie on different banks.
+#pragma once
+
+#include "lad_internal.h"
+
+namespace kda {
+
+namespace lad {
+
+constexpr int kC = kGdrChunk;
+
+__device__ __forceinline__ int sigma(int m) { return m < 8 ? 2 * m : 2 * (m - 8) + 1; }
+__device__ __forceinline__ int zcol(int c, int m) { return 8 * (m >> 2) + 4 * c + (m & 3); }
+
+__device__ __forceinline__ floatx4 mac(bf16x8 a, bf16x8 b, floatx4 c) { return mfma(a, b, c); }
+__device__ __forceinline__ floatx4 mac(const float8v& a, const float8v& b, floatx4 c) { return mma(a, b, c); }
+
+// c[i] += a[i] b over planes of one side; the accumulators in turn, so that no product waits for the one before
+template <int N> __device__ __forceinline__ void mac2(const Planes<N> (&a)[2], bf16x8 b, floatx4 (&c)[2]) {
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = mfma(a[i].p[n], b, c[i]);
+}
+template <int N> __device__ __forceinline__ void mac2(const bf16x8 (&a)[2], const Planes<N>& b, floatx4 (&c)[2]) {
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = mfma(a[i], b.p[n], c[i]);
+}
+template <int N> __device__ __forceinline__ void mac2(bf16x8 a, const Planes<N> (&b)[2], floatx4 (&c)[2]) {
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = mfma(a, b[i].p[n], c[i]);
+}
+__device__ __forceinline__ void mac2(const float8v (&a)[2], const float8v& b, floatx4 (&c)[2]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[e], c[i], 0, 0, 0);
+}
+__device__ __forceinline__ void mac2(const float8v& a, const float8v (&b)[2], floatx4 (&c)[2]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[i][e], c[i], 0, 0, 0);
+}
+
+// A chunk's rows in LDS.
+template <typename T, int D> struct Tile {
+  static constexpr int kLd = sizeof(T) == 2 ? D + 8 : D + 4;
+  using In = typename Frags<T>::In;
+  T x[kC * kLd];
+  __device__ __forceinline__ void put8(int row, int c, const In& v) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<In*>(x + row * kLd + c) = v;
+    else {
+      *reinterpret_cast<floatx4*>(x + row * kLd + c) = floatx4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<floatx4*>(x + row * kLd + c + 4) = floatx4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  // row `row`, channels {32 ks + 4g + r, 32 ks + 16 + 4g + r}
+  __device__ __forceinline__ In row_frag(int row, int ks, int g) const {
+    const T* at = x + row * kLd + 32 * ks + 4 * g;
+    if constexpr (sizeof(T) == 2) {
+      const bf16x4 lo = ld4(at), hi = ld4(at + 16);
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const floatx4 a = *reinterpret_cast<const floatx4*>(at), b = *reinterpret_cast<const floatx4*>(at + 16);
+      return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+  }
+  // lane li has, at column col0 + 4 step (li / 4) + li % 4, the tokens of places 4g .. 4g + 3 of key tiles 2 ks, 2 ks + 1
+  template <int STEP> __device__ __forceinline__ In columns(int col0, int ks, int lane) const {
+    const int li = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+      typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+      const T* at = x + (32 * ks + sigma(4 * g + (li >> 2))) * kLd + col0 + 4 * STEP * (li & 3);
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)at);
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)(at + 16 * kLd));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      float8v f;
+      const T* at = x + (32 * ks + sigma(4 * g)) * kLd + col0 + 4 * STEP * (li >> 2) + (li & 3);   // sigma(4g + r) = sigma(4g) + 2r
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f[r] = at[2 * r * kLd];
+        f[4 + r] = at[(16 + 2 * r) * kLd];
+      }
+      return f;
+    }
+  }
+};
+
+struct Gates {
+  float hi[kC], lo[kC];     // the prefix as a sum of two floats: differences stay exact beside a reset
+  float oc[kC], uc[kC];     // e^{P} out_scale,  e^{Ptot - P} in_scale
+  float tot;                // e^{Ptot}
+};
+
+template <typename T, int DX, int DZ, bool OUT> struct Lds {
+  static constexpr int kWaves = DZ / 32;
+  Tile<T, DX> y;
+  Tile<T, DZ> z;
+  Gates gates[2];
+  struct Outs {
+    Tile<T, DX> x;
+    char p[4][2][op_frag<T, 2>()];
+    float dots[kWaves][kC];
+  };
+  struct None {};
+  std::conditional_t<OUT, Outs, None> o;
+};
+
+// one chunk's rows under way from memory
+template <typename T, int D, int THREADS> struct Rows8 {
+  static constexpr int kPieces = D / 8, kLoads = kC * kPieces / THREADS;
+  using In = typename Frags<T>::In;
+  In v[kLoads];
+  // `row0` the chunk's first row in memory, tokens at `stride` bytes; chunk rows `have` and more are zeros.  Backwards
+  // row0 is the chunk's last token in the walk's order.  have >= 1.
+  __device__ __forceinline__ void load(GlobalPtr<const T> row0, uint32_t stride, int have, int reverse, int tid) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int piece = i * THREADS + tid, row = piece / kPieces, c = piece % kPieces * 8;
+      const int in = row < have ? row : have - 1;
+      const uint32_t at = (uint32_t)(reverse ? have - 1 - in : in) * stride + c * (uint32_t)sizeof(T);
+      v[i] = load_row8(lane_at(row0, at));
+    }
+  }
+  __device__ __forceinline__ void leave(Tile<T, D>& t, int have, int tid) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int piece = i * THREADS + tid, row = piece / kPieces, c = piece % kPieces * 8;
+      In zero;
+      zero_frag(zero);
+      t.put8(row, c, row < have ? v[i] : zero);
+    }
+  }
+};
+
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end).
+__device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale, double* total) {
+  double p = g;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double up = __shfl_up(p, d);
+    if (lane >= d) p += up;
+  }
+  const double tot = __shfl(p, 63);
+  if (reverse) p -= (double)g;
+  const float hi = (float)p;
+  out.hi[lane] = hi;
+  out.lo[lane] = (float)(p - (double)hi);
+  out.oc[lane] = exp_fast(hi) * out_scale;
+  out.uc[lane] = exp_fast((float)(tot - p)) * in_scale;
+  if (lane == 0) out.tot = exp_fast((float)tot);
+  *total += tot;
+}
+
+}  // namespace lad
+
+// UP: planes of Z in the new state: three where it is a result in fp32, two where only outputs are taken from it.
+// OUT false: the segment's state from zero and nothing else.
+template <typename T, int DX, int DZ, int UP, bool OUT, int OCC>
+__global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
+  using namespace lad;
+  constexpr int THREADS = 2 * DZ, NW = DZ / 32, MT = DX / 16, KS = DX / 32;
+  using In = typename Frags<T>::In;
+  extern __shared__ __attribute__((aligned(16))) char raw[];
+  auto& lds = *reinterpret_cast<Lds<T, DX, DZ, OUT>*>(raw);
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, li = lane & 15, g = lane >> 4;
+
+  int64_t unit;
+  int part;
+  const int n_kh = p.Hv / p.grp;
+  if (!gdr_block(blockIdx.x, p.slots * n_kh, p.n_walks * p.grp, &unit, &part)) return;
+  const LadWalk& wk = p.walk[part / p.grp];
+  const int64_t slot = unit / n_kh;
+  const int h = (int)(unit % n_kh) * p.grp + part % p.grp;
+  LadSeg sg;
+  if (!lad_find(p.seq_start, p.T, p.L, p.n_seq, slot, &sg)) return;
+  const int reverse = wk.reverse;
+  const int64_t first = sg.seg * p.L;                                    // of the sequence
+  const int64_t len = sg.len - first < p.L ? sg.len - first : p.L;       // this segment's tokens
+  const bool end = reverse ? sg.seg == 0 : sg.seg == sg.n_seg - 1;       // no segment behind it in the walk's order
+  if (wk.skip_end && end) return;
+
+  const auto row_base = [&](const void* t, kda_stride_t s, int grp) { return global_in<T>(t) + sg.row * s.b + (h / grp) * s.h; };
+  const auto xb = OUT ? row_base(wk.x, wk.sx, wk.grp_x) : GlobalPtr<const T>(), yb = row_base(wk.y, wk.sy, wk.grp_y), zb = row_base(wk.z, wk.sz, wk.grp_z);
+  const uint32_t xs = (uint32_t)(wk.sx.t * (int64_t)sizeof(T)), ys = (uint32_t)(wk.sy.t * (int64_t)sizeof(T)), zs = (uint32_t)(wk.sz.t * (int64_t)sizeof(T));
+  // the first token in memory of chunk c, which has `have` tokens
+  const auto chunk_at = [&](int64_t c, int have) { return sg.t0 + first + (reverse ? len - kC * c - have : kC * c); };
+  const auto chunk_have = [&](int64_t c) { return (int)(len - kC * c < kC ? len - kC * c : kC); };
+
+  Rows8<T, DX, THREADS> rx, ry;
+  Rows8<T, DZ, THREADS> rz;
+  const auto fetch = [&](int64_t c) {
+    const int have = chunk_have(c);
+    const int64_t t = chunk_at(c, have);
+    if constexpr (OUT) rx.load(xb + t * wk.sx.t, xs, have, reverse, tid);
+    ry.load(yb + t * wk.sy.t, ys, have, reverse, tid);
+    rz.load(zb + t * wk.sz.t, zs, have, reverse, tid);
+  };
+  const auto gate_of = [&](int64_t c) {
+    const int have = chunk_have(c), in = lane < have ? lane : have - 1;
+    const int64_t t = chunk_at(c, have) + (reverse ? have - 1 - in : in);
+    const float x = lad_decay<T>(p.w, p.w_per_head, p.sw, sg.row, h, t, p.gate, p.g_min);
+    return lane < have ? x : 0.f;
+  };
+
+  const int64_t n_chunks = (len + kC - 1) / kC;
+  if (n_chunks > 0) fetch(0);
+
+  floatx4 S[MT][2];
+  {
+    const int64_t at = wk.by_slot ? slot * p.Hv + h : sg.seq * p.Hv + h;
+    const auto src = global_in<float>(wk.entering) + at * (DX * DZ);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int z = 32 * wave + zcol(c, li), x = 16 * m + 4 * g;
+        S[m][c] = floatx4{};
+        if (wk.entering) {
+          if (wk.transposed) S[m][c] = ld4f(src + z * DX + x);
+          else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[m][c][r] = src[(x + r) * DZ + z];
+          }
+        }
+      }
+  }
+
+  double total = 0.0;
+  if (wave == 0 && n_chunks > 0) put_gates(lds.gates[0], gate_of(0), lane, reverse, wk.out_scale, wk.in_scale, &total);
+
+  for (int64_t c = 0; c < n_chunks; ++c) {
+    const int have = chunk_have(c);
+    const Gates& gt = lds.gates[c & 1];
+    if constexpr (OUT) rx.leave(lds.o.x, have, tid);
+    ry.leave(lds.y, have, tid);
+    rz.leave(lds.z, have, tid);
+    block_barrier();
+    const int64_t next = c + 1 < n_chunks ? c + 1 : c;   // the last chunk asks for its own rows again
+    fetch(next);
+    float gn = 0.f;
+    if (wave == 0) gn = gate_of(next);
+
+    if constexpr (OUT) {
+      // this wavefront's row tiles of the decayed X Y^T, transposed: column li is token 16 i + li
+#pragma unroll
+      for (int ii = 0; ii < 4 / NW; ++ii) {
+        const int i = wave + ii * NW;
+        const float qh = gt.hi[16 * i + li], ql = gt.lo[16 * i + li];
+        floatx4 t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = floatx4{};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const In xf = lds.o.x.row_frag(16 * i + li, ks, g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[j] = mac(lds.y.row_frag(16 * j + sigma(li), ks, g), xf, t[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * j + sigma(4 * g + r);
+            const float e = exp_fast((qh - gt.hi[key]) + (ql - gt.lo[key])) * (wk.out_scale * wk.in_scale);
+            t[j][r] = key <= 16 * i + li ? t[j][r] * e : 0.f;
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const float8v f = {t[2 * ks][0], t[2 * ks][1], t[2 * ks][2], t[2 * ks][3], t[2 * ks + 1][0], t[2 * ks + 1][1], t[2 * ks + 1][2], t[2 * ks + 1][3]};
+          store_frag(lds.o.p[i][ks], lane, make_op<2>(f, T{}));
+        }
+      }
+    }
+    if (wave == 0) put_gates(lds.gates[(c + 1) & 1], c + 1 < n_chunks ? gn : 0.f, lane, reverse, wk.out_scale, wk.in_scale, &total);
+
+    floatx4 acc[4][2];
+    if constexpr (OUT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = floatx4{};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        typename Frags<T>::template Op<2> sp[2];
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const floatx4 a = S[2 * ks][cc], b = S[2 * ks + 1][cc];
+          sp[cc] = make_op<2>(float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, T{});
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mac2(sp, lds.o.x.row_frag(16 * i + li, ks, g), acc[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float oc = gt.oc[16 * i + li];
+        acc[i][0] *= oc;
+        acc[i][1] *= oc;
+      }
+      block_barrier();   // the tiles of X Y^T are there
+    }
+
+    // state and the rest of the outputs
+    const float tot = gt.tot;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) S[m][cc] *= tot;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      In zf[2];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
+      if constexpr (OUT) {
+#pragma unroll
+        for (int i = 2 * ks; i < 4; ++i) mac2(zf, load_frag<typename Frags<T>::template Op<2>>(lds.o.p[i][ks], lane), acc[i]);
+      }
+      typename Frags<T>::template Op<UP> zu[2];
+      float8v u;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        u[r] = gt.uc[32 * ks + sigma(4 * g + r)];
+        u[4 + r] = gt.uc[32 * ks + 16 + sigma(4 * g + r)];
+      }
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        float8v f;
+        if constexpr (sizeof(T) == 2) f = __builtin_convertvector(__builtin_bit_cast(bf16x8v, zf[cc]), float8v);
+        else f = zf[cc];
+        zu[cc] = make_op<UP>(f * u, T{});
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) mac2(lds.y.template columns<1>(16 * m, ks, lane), zu, S[m]);
+    }
+
+    if constexpr (OUT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) settle(acc[i][cc]);
+      const int64_t t0 = chunk_at(c, have);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * i + li;
+        const int in = row < have ? row : have - 1;
+        const int64_t t = t0 + (reverse ? have - 1 - in : in);
+        if (wk.dot) {
+          const auto f = load_row8(global_in<T>(wk.dot) + sg.row * wk.sdot.b + (h / wk.grp_dot) * wk.sdot.h + t * wk.sdot.t + 32 * wave + 8 * g);
+          float8v d;
+          if constexpr (sizeof(T) == 2) d = __builtin_convertvector(__builtin_bit_cast(bf16x8v, f), float8v);
+          else d = f;
+          float s = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s += acc[i][0][r] * d[r] + acc[i][1][r] * d[4 + r];
+          s += __shfl_xor(s, 16);
+          s += __shfl_xor(s, 32);
+          if (g == 0) lds.o.dots[wave][row] = s;
+        }
+        if (row < have) {
+          const int64_t at = sg.row * wk.so.b + h * wk.so.h + t * wk.so.t + 32 * wave + 8 * g;
+          if (wk.out_f32) {
+            store_row4(global_out<float>(wk.out) + at, acc[i][0]);
+            store_row4(global_out<float>(wk.out) + at + 4, acc[i][1]);
+          } else if constexpr (sizeof(T) == 2) {
+            *repoint<bf16x8>(global_out<uint16_t>(wk.out) + at) = pack2(acc[i][0], acc[i][1]);
+          } else {
+            store_row4(global_out<float>(wk.out) + at, acc[i][0]);
+            store_row4(global_out<float>(wk.out) + at + 4, acc[i][1]);
+          }
+        }
+      }
+    }
+    block_barrier();   // nobody reads this chunk's rows any more
+    if constexpr (OUT) {
+      if (wk.dot && tid < kC) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += lds.o.dots[w][tid];
+        if (tid < have) wk.dots[(sg.row * p.Hv + h) * p.T + chunk_at(c, have) + (reverse ? have - 1 - tid : tid)] = s;
+      }
+    }
+  }
+
+  if (wk.decay && tid == 0) wk.decay[slot * p.Hv + h] = exp_fast((float)total);
+  if (wk.leaving && (wk.leave_slot || end)) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) settle(S[m][c]);
+    const int64_t at = wk.leave_slot ? slot * p.Hv + h : sg.seq * p.Hv + h;
+    const auto dst = as_global(wk.leaving) + at * (DX * DZ);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int z = 32 * wave + zcol(c, li), x = 16 * m + 4 * g;
+        if (wk.transposed) *repoint<floatx4>(dst + z * DX + x) = S[m][c];
+        else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dst[(x + r) * DZ + z] = S[m][c][r];
+        }
+      }
+  }
+}
+
+template <typename T, int DX, int DZ, int UP, bool OUT>
+hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
+  constexpr int kLdsBytes = (int)sizeof(lad::Lds<T, DX, DZ, OUT>);
+  // two workgroups a compute unit where registers and LDS allow it
+  constexpr int OCC = sizeof(T) == 2 && DZ == 128 ? 2 : 1;
+  const auto kernel = lad_walk_kernel<T, DX, DZ, UP, OUT, OCC>;
+  static std::atomic<uint64_t> done;
+  const hipError_t set = set_dyn_lds(reinterpret_cast<const void*>(kernel), kLdsBytes, done);
+  if (set != hipSuccess) return set;
+  const int64_t grid = gdr_blocks(p.slots * (p.Hv / p.grp), p.n_walks * p.grp);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(2 * DZ), kLdsBytes, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, int UP, bool OUT>
+hipError_t launch_walk_dims(const LadParams& p, int dx, int dz, hipStream_t s) {
+  switch (dx * 256 + dz) {
+    case 32 * 256 + 32: return launch_walk_one<T, 32, 32, UP, OUT>(p, s);
+    case 32 * 256 + 64: return launch_walk_one<T, 32, 64, UP, OUT>(p, s);
+    case 32 * 256 + 128: return launch_walk_one<T, 32, 128, UP, OUT>(p, s);
+    case 64 * 256 + 32: return launch_walk_one<T, 64, 32, UP, OUT>(p, s);
+    case 64 * 256 + 64: return launch_walk_one<T, 64, 64, UP, OUT>(p, s);
+    case 64 * 256 + 128: return launch_walk_one<T, 64, 128, UP, OUT>(p, s);
+    case 128 * 256 + 32: return launch_walk_one<T, 128, 32, UP, OUT>(p, s);
+    case 128 * 256 + 64: return launch_walk_one<T, 128, 64, UP, OUT>(p, s);
+    default: return launch_walk_one<T, 128, 128, UP, OUT>(p, s);
+  }
+}
+
+}  // namespace kda

@@ -1,0 +1,339 @@
+// Norms of queries and keys for each head with the rotation by position, and their gradients, one pass over each row:
+//   n = x / rms(x) * weight,   y = scale * rot(n):  (a, b) -> (a cos - b sin, b cos + a sin) for the pairs of the first R
+// values.  Bound by HBM where there are many rows, by the call where there are few.
+//
+// NT lanes hold a row as 8 pairs each; a group of NT lanes keeps one token and walks its heads, so the sines of a
+// token's angles are formed once for all of them (64 pairs cost more than a row's trip through memory would).
+// Angles are products of the position and the fp32 frequency in double, reduced to turns there: a float's product is off
+// by 0.03 radians at position 10^6.
+//
+// The gradient recomputes the norm from the same row; the weights' gradients are summed in registers over the rows that a
+// workgroup takes, and a second kernel adds up the workgroups in a fixed order.
+#include "lad_internal.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kMaxBlocks = 512;   // workgroups a tensor of the gradient: rows of partial sums
+
+template <int NT, bool NEAR, bool VEC> struct Pairs {
+  int t, D, R;
+  __device__ __forceinline__ int pair(int j) const { return VEC ? 8 * t + j : j * NT + t; }
+  __device__ __forceinline__ bool has(int j) const { return pair(VEC ? 0 : j) < D / 2; }
+  // places of the pair's two values
+  __device__ __forceinline__ int a(int j) const {
+    const int p = pair(j);
+    return NEAR ? 2 * p : p < R / 2 ? p : R / 2 + p;
+  }
+  __device__ __forceinline__ int b(int j) const {
+    const int p = pair(j);
+    return NEAR ? 2 * p + 1 : p < R / 2 ? p + R / 2 : p + D / 2;
+  }
+};
+
+__device__ __forceinline__ float8v widen(bf16x8 f) { return __builtin_convertvector(__builtin_bit_cast(bf16x8v, f), float8v); }
+__device__ __forceinline__ float8v widen(const float8v& f) { return f; }
+
+template <typename T, int NT, bool NEAR, bool VEC>
+__device__ __forceinline__ void load_pairs(GlobalPtr<const T> row, Pairs<NT, NEAR, VEC> m, float (&a)[8], float (&b)[8]) {
+  if constexpr (VEC) {
+    const int at = m.has(0) ? m.t : 0;   // a lane behind the row reads its first values and drops them
+    const Pairs<NT, NEAR, VEC> in{at, m.D, m.R};
+    const int lo = in.a(0), hi = NEAR ? lo + 8 : in.b(0);
+    const float8v x = widen(load_row8(row + lo)), y = widen(load_row8(row + hi));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = NEAR ? (j < 4 ? x[2 * (j & 3)] : y[2 * (j & 3)]) : x[j];
+      b[j] = NEAR ? (j < 4 ? x[2 * (j & 3) + 1] : y[2 * (j & 3) + 1]) : y[j];
+      if (!m.has(0)) a[j] = b[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = b[j] = 0.f;
+      if (m.has(j)) {
+        a[j] = get(row + m.a(j));
+        b[j] = get(row + m.b(j));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store8(GlobalPtr<uint16_t> p, const float (&x)[8]) {
+  *repoint<bf16x8>(p) = pack2(floatx4{x[0], x[1], x[2], x[3]}, floatx4{x[4], x[5], x[6], x[7]});
+}
+__device__ __forceinline__ void store8(GlobalPtr<float> p, const float (&x)[8]) {
+  store_row4(p, floatx4{x[0], x[1], x[2], x[3]});
+  store_row4(p + 4, floatx4{x[4], x[5], x[6], x[7]});
+}
+
+template <typename T, int NT, bool NEAR, bool VEC>
+__device__ __forceinline__ void store_pairs(GlobalPtr<T> row, Pairs<NT, NEAR, VEC> m, const float (&a)[8], const float (&b)[8]) {
+  if constexpr (VEC) {
+    if (!m.has(0)) return;
+    if constexpr (NEAR) {
+      const float x[8] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]}, y[8] = {a[4], b[4], a[5], b[5], a[6], b[6], a[7], b[7]};
+      store8(row + m.a(0), x);
+      store8(row + m.a(0) + 8, y);
+    } else {
+      store8(row + m.a(0), a);
+      store8(row + m.b(0), b);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (m.has(j)) {
+        put(row + m.a(j), a[j]);
+        put(row + m.b(j), b[j]);
+      }
+  }
+}
+
+// cosines and sines of a token's angles; 1 and 0 for pairs that do not turn
+template <int NT, bool NEAR, bool VEC>
+__device__ __forceinline__ void angles(const QkNormParams& p, int64_t b, int64_t t, Pairs<NT, NEAR, VEC> m, float (&c)[8], float (&s)[8]) {
+  double pos = 0.0;
+  if (p.R > 0) {
+    const int64_t at = b * p.pos_b + t * p.pos_t;
+    pos = p.wide ? (double)global_in<int64_t>(p.positions)[at] : (double)global_in<int32_t>(p.positions)[at];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = m.pair(j);
+    c[j] = 1.f;
+    s[j] = 0.f;
+    if (i < p.R / 2) {
+      const double turns = pos * (double)global_in<float>(p.inv_freq)[i] * 0.15915494309189533577;   // 1 / (2 pi)
+      sincospif((float)(2.0 * (turns - rint(turns))), &s[j], &c[j]);
+    }
+  }
+}
+
+template <int NT> __device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int d = 1; d < NT; d <<= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+template <int NT, bool NEAR, bool VEC>
+__device__ __forceinline__ void load_weight(const void* w, int wdtype, Pairs<NT, NEAR, VEC> m, float (&a)[8], float (&b)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = b[j] = 1.f;
+  } else if (wdtype == KDA_DTYPE_BF16) load_pairs<uint16_t>(global_in<uint16_t>(w), m, a, b);
+  else load_pairs<float>(global_in<float>(w), m, a, b);
+}
+
+template <typename T> __device__ __forceinline__ GlobalPtr<T> row_of(const void* p, kda_stride_t s, int64_t b, int h, int64_t t) {
+  return (GlobalPtr<T>)p + b * s.b + h * s.h + t * s.t;
+}
+
+// One workgroup: 256 / NT tokens and up to `heads` heads of one tensor.  Blocks of the queries come first.
+template <typename T, int NT, bool NEAR, bool VEC>
+__global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkNormParams p, int heads, int parts_q, int parts) {
+  constexpr int TOK = 256 / NT;
+  const int part = blockIdx.x % parts, which = part >= parts_q;
+  const int h0 = (which ? part - parts_q : part) * heads, h1 = h0 + heads < p.H[which] ? h0 + heads : p.H[which];
+  const uint32_t row = (blockIdx.x / parts) * TOK + threadIdx.x / NT, T_ = (uint32_t)p.T;
+  if (row >= (uint32_t)(p.B * p.T)) return;
+  const int64_t b = row / T_, t = row - b * T_;
+  const Pairs<NT, NEAR, VEC> m{(int)(threadIdx.x % NT), p.D, p.R};
+  float wa[8], wb[8], c[8], s[8];
+  load_weight(p.weight[which], p.wdtype, m, wa, wb);
+  angles(p, b, t, m, c, s);
+  for (int h = h0; h < h1; ++h) {
+    float x[8], y[8];
+    load_pairs<T>(row_of<const T>(p.x[which], p.sx[which], b, h, t), m, x, y);
+    float r = p.scale[which];
+    if (p.norm) {
+      float q = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q += x[j] * x[j] + y[j] * y[j];
+      r *= rsqrtf(row_sum<NT>(q) / (float)p.D + p.eps);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float u = x[j] * wa[j] * r, v = y[j] * wb[j] * r;
+      x[j] = u * c[j] - v * s[j];
+      y[j] = v * c[j] + u * s[j];
+    }
+    store_pairs<T>(row_of<T>(p.y[which], p.sy[which], b, h, t), m, x, y);
+  }
+}
+
+// blocks_q workgroups walk the queries' (tokens, heads) items, the others the keys'
+template <typename T, int NT, bool NEAR, bool VEC>
+__global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkNormParams p, int heads, int blocks_q) {
+  constexpr int TOK = 256 / NT;
+  __shared__ float acc[4][NT * 16];
+  const int which = (int)blockIdx.x >= blocks_q;
+  const int block = which ? blockIdx.x - blocks_q : blockIdx.x, blocks = which ? gridDim.x - blocks_q : blocks_q;
+  const Pairs<NT, NEAR, VEC> m{(int)(threadIdx.x % NT), p.D, p.R};
+  const uint32_t rows = (uint32_t)(p.B * p.T), T_ = (uint32_t)p.T;
+  const int parts = (p.H[which] + heads - 1) / heads;
+  const int64_t items = (int64_t)((rows + TOK - 1) / TOK) * parts;
+  float wa[8], wb[8], da[8], db[8];
+  load_weight(p.weight[which], p.wdtype, m, wa, wb);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) da[j] = db[j] = 0.f;
+  for (int64_t item = block; item < items; item += blocks) {
+    const int h0 = (int)(item % parts) * heads, h1 = h0 + heads < p.H[which] ? h0 + heads : p.H[which];
+    const uint32_t row = (uint32_t)(item / parts) * TOK + threadIdx.x / NT;
+    if (row >= rows) continue;
+    const int64_t b = row / T_, t = row - b * T_;
+    float c[8], s[8];
+    angles(p, b, t, m, c, s);
+    for (int h = h0; h < h1; ++h) {
+      float x[8], y[8], u[8], v[8];
+      load_pairs<T>(row_of<const T>(p.x[which], p.sx[which], b, h, t), m, x, y);
+      load_pairs<T>(row_of<const T>(p.dy[which], p.sdy[which], b, h, t), m, u, v);
+      float r = 1.f;
+      if (p.norm) {
+        float q = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q += x[j] * x[j] + y[j] * y[j];
+        r = rsqrtf(row_sum<NT>(q) / (float)p.D + p.eps);
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float e = u[j] * p.scale[which], f = v[j] * p.scale[which];
+        u[j] = e * c[j] + f * s[j];
+        v[j] = f * c[j] - e * s[j];
+        x[j] *= r;
+        y[j] *= r;
+        da[j] += u[j] * x[j];
+        db[j] += v[j] * y[j];
+        u[j] *= wa[j];
+        v[j] *= wb[j];
+        dot += u[j] * x[j] + v[j] * y[j];
+      }
+      if (p.norm) {
+        dot = row_sum<NT>(dot) / (float)p.D;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          u[j] = r * (u[j] - x[j] * dot);
+          v[j] = r * (v[j] - y[j] * dot);
+        }
+      }
+      store_pairs<T>(row_of<T>(p.dx[which], p.sdx[which], b, h, t), m, u, v);
+    }
+  }
+  if (!p.dweight[which]) return;
+  // the wavefront's tokens, then the wavefronts
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int d = NT; d < 64; d <<= 1) {
+      da[j] += __shfl_xor(da[j], d);
+      db[j] += __shfl_xor(db[j], d);
+    }
+  }
+  if ((threadIdx.x & 63) < NT) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      acc[threadIdx.x >> 6][m.t * 16 + j] = da[j];
+      acc[threadIdx.x >> 6][m.t * 16 + 8 + j] = db[j];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < NT) {
+    const auto out = as_global(p.partial) + ((int64_t)which * kMaxBlocks + block) * p.D;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!m.has(j)) continue;
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        a += acc[w][m.t * 16 + j];
+        b += acc[w][m.t * 16 + 8 + j];
+      }
+      out[m.a(j)] = a;
+      out[m.b(j)] = b;
+    }
+  }
+}
+
+// adds up the workgroups' sums: 16 columns a workgroup, 64 threads along the workgroups of each
+__global__ __launch_bounds__(1024) void qk_norm_weight_kernel(QkNormParams p, int blocks_q, int blocks_k) {
+  __shared__ float part[64][17];
+  const int c = threadIdx.x & 15, y = threadIdx.x >> 4, col = blockIdx.x * 16 + c, which = blockIdx.y;
+  if (!p.dweight[which]) return;
+  const int blocks = which ? blocks_k : blocks_q;
+  const auto in = global_in<float>(p.partial) + (int64_t)which * kMaxBlocks * p.D;
+  float s = 0.f;
+  if (col < p.D) {
+#pragma unroll 8
+    for (int i = y; i < blocks; i += 64) s += in[(int64_t)i * p.D + col];
+  }
+  part[y][c] = s;
+  __syncthreads();
+  if (y == 0 && col < p.D) {
+    s = 0.f;
+    for (int i = 0; i < 64; ++i) s += part[i][c];
+    if (p.wdtype == KDA_DTYPE_BF16) put(global_out<uint16_t>(p.dweight[which]) + col, s);
+    else put(global_out<float>(p.dweight[which]) + col, s);
+  }
+}
+
+template <typename T, int NT, bool NEAR, bool VEC>
+hipError_t launch_one(const QkNormParams& p, hipStream_t s, bool bwd) {
+  constexpr int TOK = 256 / NT;
+  const int64_t groups = (p.B * p.T + TOK - 1) / TOK;
+  // heads a workgroup walks with one set of angles: as many as leave 8 workgroups a compute unit
+  const int64_t all = groups * (p.H[0] + p.H[1]), most = p.H[0] > p.H[1] ? p.H[0] : p.H[1];
+  const int heads = (int)(all / 2048 < 1 ? 1 : all / 2048 < most ? all / 2048 : most);
+  const int64_t parts_q = (p.H[0] + heads - 1) / heads, parts_k = (p.H[1] + heads - 1) / heads;
+  if (!bwd) {
+    const int64_t grid = groups * (parts_q + parts_k);
+    if (grid > 0)
+      hipLaunchKernelGGL((qk_norm_fwd_kernel<T, NT, NEAR, VEC>), dim3((unsigned)grid), dim3(256), 0, s, p, heads, (int)parts_q, (int)(parts_q + parts_k));
+    return hipGetLastError();
+  }
+  const auto blocks = [&](int64_t items) { return (int)(items < kMaxBlocks ? items : kMaxBlocks); };
+  const int blocks_q = blocks(groups * parts_q), blocks_k = blocks(groups * parts_k);
+  if (blocks_q + blocks_k > 0)
+    hipLaunchKernelGGL((qk_norm_bwd_kernel<T, NT, NEAR, VEC>), dim3(blocks_q + blocks_k), dim3(256), 0, s, p, heads, blocks_q);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!p.dweight[0] && !p.dweight[1])) return e;
+  hipLaunchKernelGGL(qk_norm_weight_kernel, dim3((unsigned)((p.D + 15) / 16), 2), dim3(1024), 0, s, p, blocks_q, blocks_k);
+  return hipGetLastError();
+}
+
+template <typename T, bool NEAR, bool VEC>
+hipError_t launch_d(const QkNormParams& p, hipStream_t s, bool bwd) {
+  if (p.D <= 64) return launch_one<T, 4, NEAR, VEC>(p, s, bwd);
+  if (p.D <= 128) return launch_one<T, 8, NEAR, VEC>(p, s, bwd);
+  if (p.D <= 256) return launch_one<T, 16, NEAR, VEC>(p, s, bwd);
+  return launch_one<T, 64, NEAR, VEC>(p, s, bwd);
+}
+
+bool rows16(const void* ptr, kda_stride_t s, int esz) {
+  if (!ptr) return true;
+  const int64_t per = 16 / esz;
+  return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0 && s.b % per == 0 && s.h % per == 0 && s.t % per == 0;
+}
+
+template <typename T> hipError_t launch_t(const QkNormParams& p, hipStream_t s, bool bwd) {
+  const kda_stride_t none = {0, 0, 0};
+  // whole 16-byte pieces: a lane's 8 pairs are all turned or all not, unless they are neighbours
+  bool vec = p.D % 16 == 0 && (p.interleaved || (p.R % 16 == 0));
+  for (int i = 0; i < 2; ++i)
+    vec = vec && rows16(p.x[i], p.sx[i], sizeof(T)) && rows16(p.y[i], p.sy[i], sizeof(T)) && rows16(p.dy[i], p.sdy[i], sizeof(T)) &&
+          rows16(p.dx[i], p.sdx[i], sizeof(T)) && rows16(p.weight[i], none, 4);
+  if (p.interleaved) return vec ? launch_d<T, true, true>(p, s, bwd) : launch_d<T, true, false>(p, s, bwd);
+  return vec ? launch_d<T, false, true>(p, s, bwd) : launch_d<T, false, false>(p, s, bwd);
+}
+
+}  // namespace
+
+size_t qk_norm_bwd_workspace_bytes(const QkNormParams& p) { return (size_t)2 * kMaxBlocks * p.D * 4; }
+hipError_t launch_qk_norm_fwd(const QkNormParams& p, hipStream_t s) {
+  return p.dtype == KDA_DTYPE_BF16 ? launch_t<uint16_t>(p, s, false) : launch_t<float>(p, s, false);
+}
+hipError_t launch_qk_norm_bwd(const QkNormParams& p, hipStream_t s) {
+  return p.dtype == KDA_DTYPE_BF16 ? launch_t<uint16_t>(p, s, true) : launch_t<float>(p, s, true);
+}
+
+}  // namespace kda

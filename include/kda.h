@@ -368,6 +368,103 @@ KDA_API int kda_norm_bwd(const void* x, const void* weight, const void* z, const
 
 KDA_API size_t kda_norm_bwd_workspace_bytes(const kda_norm_t* desc);
 
+/* ------------------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the recurrence of the head-gated rule without its
+ * correction.  Per sequence and value head h, with query/key head h / (Hv / Hk):
+ *
+ *     S <- e^{g_t} S + k_t v_t^T;   o_t = scale S^T q_t
+ *
+ * with g from w by desc->gate as above.  w [B,Hv,T] is of dtype; with desc->w_per_head it is [Hv], dense and
+ * fp32: one decay for each head (desc->w is not read then), and so is its gradient.
+ * Tensors, strides, packed sequences, aliasing and their limits are those of the head-gated rule above (there is no
+ * beta).  Evaluated in chunks of 64 tokens, long sequences in segments side by side: a NaN or infinity in a token may
+ * reach the other tokens of its chunk and segment and every later one (in the gradients every earlier one too), never
+ * another sequence.  bf16: inputs are exact operands; what is computed is carried as a sum of two or three, so a result
+ * is off by its own rounding and states are fp32's. */
+typedef struct {
+  int64_t B, Hk, Hv, T, dk, dv; /* Hk divides Hv; dk, dv in {32, 64, 128}; 0 <= T < 2^31 */
+  int64_t n_seq;                /* packed sequences (0 without seq_start) */
+  int32_t dtype;                /* a kda_dtype_t */
+  int32_t gate;                 /* a kda_gate_t */
+  int32_t w_per_head;           /* 0: w [B,Hv,T] of dtype; 1: w [Hv], fp32 */
+  float g_min;                  /* KDA_GATE_BOUNDED only */
+  float scale;                  /* of the outputs, finite */
+  kda_stride_t q, k, v, w;
+} kda_lad_t;
+
+/* Gradients, in the inputs' type (dw of a w per head and dS0 fp32); dw, dS0 NULL: not wanted. */
+typedef struct {
+  void *dq, *dk, *dv, *dw;
+  float* dS0;
+  kda_stride_t sq, sk, sv, sw;
+} kda_lad_grads_t;
+
+/* Chunked forward: o, and S_final unless it is NULL (which may be S0, in place).  S0 NULL: zero states. */
+KDA_API int kda_lad_chunk_fwd(const void* q, const void* k, const void* v, const void* w, const float* S0,
+                              const int32_t* seq_start, const kda_lad_t* desc, void* o, const kda_stride_t* o_stride,
+                              float* S_final, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients, given dO = dL/do and dS_final = dL/dS_final (NULL: zero).  Value heads that share a
+ * query/key head add up in dq and dk, in a fixed order; so do the tokens in a dw per head. */
+KDA_API int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w, const float* S0,
+                              const int32_t* seq_start, const kda_lad_t* desc, const void* dO,
+                              const kda_stride_t* dO_stride, const float* dS_final, const kda_lad_grads_t* grads,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch of the two (backward != 0: of kda_lad_chunk_bwd); (size_t)-1 for an invalid descriptor. */
+KDA_API size_t kda_lad_workspace_bytes(const kda_lad_t* desc, int backward);
+
+/* Recurrent step: advances states of the pool S [n_slots,Hv,dk,dv] in place by the T tokens of each of B
+ * rows, one after another.  slots (device, int32 [B], or NULL: row b uses state b) names each row's state; a
+ * slot outside [0, n_slots) marks a padding row: its outputs are zeros and no state is touched.  Rows that
+ * name the same slot are successive tokens of that state, in row order. */
+KDA_API int kda_lad_decode(const void* q, const void* k, const void* v, const void* w, float* S, int64_t n_slots,
+                           const int32_t* slots, const kda_lad_t* desc, void* o, const kda_stride_t* o_stride,
+                           void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Norms of queries and keys for each head with the rotation by position, what stands before a rule or an
+ * attention.  Per row x of D values of q or k, at its token's position p:
+ *     n = x / rms(x) * weight            (desc->norm 0: n = x * weight; weight NULL: without it)
+ *     y = scale * (n, its first R values rotated in pairs by the angles p * inv_freq[i], i < R / 2)
+ *     (a, b) -> (a cos - b sin, b cos + a sin);  rms(t) = sqrt(mean(t^2) + eps)
+ * Pair i is values i and i + R/2, or 2i and 2i + 1 with desc->interleaved.  R = 0: no rotation (positions and
+ * inv_freq are not read).  Angles are products in 64 bits, so far positions keep their accuracy.
+ * q, q_out [B,Hq,T,D], k, k_out [B,Hk,T,D]: of dtype, any strides with the last dimension contiguous (Hk may be
+ * 0: no keys); weights dense [D] of wdtype; positions [B,T], int32 or int64 with strides in elements;
+ * inv_freq dense fp32 [R/2].  D even, at most KDA_QK_NORM_MAX_D; R even, at most D.  An output may not hold
+ * one place twice, nor reach into the span of an input or another output. */
+#define KDA_QK_NORM_MAX_D 1024
+
+typedef struct {
+  int64_t B, Hq, Hk, T, D, R;
+  int32_t dtype, wdtype;         /* kda_dtype_t of the rows and of the weights */
+  int32_t norm, interleaved;     /* truth values */
+  int32_t wide_positions;        /* 0: int32, 1: int64 */
+  float q_scale, k_scale, eps;   /* finite, eps >= 0 */
+  int64_t pos_b, pos_t;          /* elements between the positions' batch rows and tokens, >= 0 */
+  kda_stride_t q, k;
+} kda_qk_norm_t;
+
+typedef struct {
+  void *dq, *dk;                 /* of dtype */
+  void *dq_weight, *dk_weight;   /* [D], of wdtype, where the weights are given */
+  kda_stride_t sq, sk;
+} kda_qk_norm_grads_t;
+
+KDA_API int kda_qk_norm_fwd(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                            const void* positions, const float* inv_freq, const kda_qk_norm_t* desc, void* q_out,
+                            const kda_stride_t* q_out_stride, void* k_out, const kda_stride_t* k_out_stride, void* stream);
+
+/* Gradients given dq_out = dL/dq_out and dk_out = dL/dk_out.  The weights' gradients are sums over the rows in
+ * a fixed order; the workspace is needed where there are weights. */
+KDA_API int kda_qk_norm_bwd(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                            const void* positions, const float* inv_freq, const kda_qk_norm_t* desc, const void* dq_out,
+                            const kda_stride_t* dq_out_stride, const void* dk_out, const kda_stride_t* dk_out_stride,
+                            const kda_qk_norm_grads_t* grads, void* workspace, size_t workspace_bytes, void* stream);
+
+KDA_API size_t kda_qk_norm_bwd_workspace_bytes(const kda_qk_norm_t* desc);
+
 /* Static description of an error code. Host-only. */
 KDA_API const char* kda_strerror(int code);
 
