@@ -73,7 +73,7 @@ Span w_span(const kda_lad_t* d, const void* w) {
 // workspace sections
 struct Work {
   char *s, *r, *s_decay, *r_decay, *s_final;   // the chain over the segments
-  char *qdq, *kdk, *partial;                   // of the decay's gradient
+  char *qdq, *kdk, *partial;                   // of the decay's gradient; qdq and kdk twice [B, Hv, T]
   char *dq, *dk;                               // gradients by value head, where heads share q and k
 };
 
@@ -93,8 +93,8 @@ size_t layout(Work& w, void* base, const kda_lad_t* d, const Plan& p, bool bwd) 
   take(w.r, per_slot * size);
   take(w.r_decay, per_slot * 4);
   take(w.s_final, (double)p.n_seq * d->Hv * size);
-  take(w.qdq, rows);
-  take(w.kdk, rows);
+  take(w.qdq, rows * 4);   // two of doubles
+  take(w.kdk, rows * 4);
   take(w.partial, per_slot * 8);
   if (p.grp > 1) {
     take(w.dq, rows * d->dk);
@@ -278,19 +278,23 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     b.in_scale = c.in_scale = desc->scale;
     b.entering = c.entering = backwards ? floats(ws.r) : dS_final;
     b.by_slot = c.by_slot = backwards;
+    const auto set_dots = [&](LadWalk& x, char* at) {
+      x.dots[0] = reinterpret_cast<double*>(at);
+      x.dots[1] = x.dots[0] + B * Hv * T;
+    };
     if (grads->dw) {
-      a.dot = q; a.sdot = desc->q; a.grp_dot = pl.grp; a.dots = floats(ws.qdq);
-      b.dot = k; b.sdot = desc->k; b.grp_dot = pl.grp; b.dots = floats(ws.kdk);
+      a.dot = q; a.sdot = desc->q; a.grp_dot = pl.grp; set_dots(a, ws.qdq);
+      b.dot = k; b.sdot = desc->k; b.grp_dot = pl.grp; set_dots(b, ws.kdk);
     }
     p.walk[0] = a;
     p.walk[1] = b;
     p.walk[2] = c;
     p.n_walks = dk == dv ? 3 : 2;
-    if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, s))) != KDA_OK) return rc;
+    if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, per_head && grads->dw, s))) != KDA_OK) return rc;
     if (dk != dv) {
       p.walk[0] = c;
       p.n_walks = 1;
-      if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dk, (int)dv, s))) != KDA_OK) return rc;
+      if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dk, (int)dv, false, s))) != KDA_OK) return rc;
     }
     if (shared) {
       LadSum sm{};
@@ -302,7 +306,11 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
   }
   if (!grads->dw || (T == 0 && !per_head)) return KDA_OK;
   LadDecayGrad g{};
-  g.qdq = floats(ws.qdq); g.kdk = floats(ws.kdk); g.s = floats(ws.s); g.r = floats(ws.r);
+  for (int i = 0; i < 2; ++i) {
+    g.qdq[i] = reinterpret_cast<const double*>(ws.qdq) + i * B * Hv * T;
+    g.kdk[i] = reinterpret_cast<const double*>(ws.kdk) + i * B * Hv * T;
+  }
+  g.s = floats(ws.s); g.r = floats(ws.r);
   g.S_final = floats(ws.s_final); g.dSf = dS_final; g.w = w; g.sw = desc->w; g.dw = grads->dw; g.sdw = grads->sw;
   g.partial = reinterpret_cast<double*>(ws.partial); g.seq_start = seq_start;
   g.T = T; g.L = pl.L; g.n_seq = pl.n_seq; g.slots = pl.slots; g.Hv = (int)Hv; g.size = (int)(dk * dv);

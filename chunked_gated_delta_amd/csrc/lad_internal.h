@@ -18,7 +18,7 @@
 namespace kda {
 
 struct LadWalk {
-  const void *x, *y, *z, *dot;              // rows; dot (nullable): dots[t] = out_t . dot_t
+  const void *x, *y, *z, *dot;              // rows; dot nullable
   kda_stride_t sx, sy, sz, sdot;
   int grp_x, grp_y, grp_z, grp_dot;         // value heads that share a head of the tensor
   void* out;
@@ -26,7 +26,7 @@ struct LadWalk {
   const float* entering;                    // per (slot, head) with by_slot, else per (sequence, head); null: zero
   float* leaving;                           // per (slot, head) with leave_slot, else per (sequence, head), behind the walk's last segment; nullable
   float* decay;                             // e^{the segment's decay} per (slot, head); nullable
-  float* dots;                              // [B, Hv, T]
+  double* dots[2];                          // [B, Hv, T]: out_t . dot_t of what came from the state, and of all of it
   float out_scale, in_scale;                // of the outputs, and of Z in outputs and state
   int reverse, transposed, by_slot, leave_slot, out_f32, skip_end;   // transposed: states lie as [DZ][DX]; skip_end: no walk over the segment
                                                          // behind which none comes
@@ -57,7 +57,7 @@ struct LadScan {
 
 // the log-decay's gradient from dots of q.dq and k.dk
 struct LadDecayGrad {
-  const float *qdq, *kdk;                   // [B, Hv, T]
+  const double *qdq[2], *kdk[2];            // [B, Hv, T]: from other chunks, and all
   const float *s, *r;                       // entering states of the segments (null: one segment a sequence)
   const float *S_final, *dSf;               // per (sequence, head); dSf nullable
   const void* w;
@@ -110,7 +110,9 @@ int64_t lad_slots(int64_t B, int64_t T, int64_t n_seq, int64_t L, bool packed);
 
 // the walks of p over every segment; states: only their states (no outputs)
 hipError_t launch_lad_fwd(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
-hipError_t launch_lad_bwd(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
+// exact: with fp32's accuracy up to the results' own rounding
+hipError_t launch_lad_bwd(const LadParams& p, int dtype, int dx, int dz, bool exact, hipStream_t s);
+hipError_t launch_lad_bwd_exact(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
 hipError_t launch_lad_states(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
 hipError_t launch_lad_scan(const LadScan& p, hipStream_t s);
 hipError_t launch_lad_decay_grad(const LadDecayGrad& p, hipStream_t s);

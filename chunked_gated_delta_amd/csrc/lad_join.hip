@@ -47,12 +47,17 @@ __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
   if (out) *repoint<floatx4>(as_global(out) + whole) = x;
 }
 
-// dg_t = sum over the segment's tokens s >= t of (q.dq - k.dk)_s + <S, R> at the segment's end, in double: the terms
-// cancel.  256 threads take consecutive tokens each.
+// The log-decay's gradient is a sum over pairs of tokens, dg_t = sum of c_ij over i >= t > j; with B_c the sum over the
+// pairs on both sides of chunk c's start (= <S, R> there), and the dots d_i = q_i . dq_i = sum of c_ij over j <= i,
+// e_j = k_j . dk_j = sum of c_ij over i >= j, each also without its chunk's own pairs (d', e'):
+//     dg_t = B_{c+1} + sum over t' >= t of the chunk (d - e),   B_c = B_{c+1} + sum over the chunk (d' - e')
+// A chunk's own pairs cancel in its d and e; left out of B they leave no rounding there, which would come from as many
+// tokens as the segment has and be large beside the gradient of a head that soon forgets.  B at the segment's end is the product
+// of states.  All in double; a wavefront takes a chunk, from the last one down.
 template <typename T>
 __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
-  __shared__ double part[256];
-  const int tid = threadIdx.x;
+  __shared__ double part[4];
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   const int64_t slot = blockIdx.x / p.Hv;
   const int h = (int)(blockIdx.x % p.Hv);
   LadSeg sg;
@@ -61,6 +66,11 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
     return;
   }
   const int64_t first = sg.seg * p.L, len = sg.len - first < p.L ? sg.len - first : p.L;
+  const auto wave_sum = [](double x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    return x;
+  };
   // <S, R> where the segment ends
   const bool last = sg.seg == sg.n_seg - 1;
   const float *S = nullptr, *R = nullptr;
@@ -78,46 +88,51 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) dot += (double)a[r] * (double)b[r];
     }
-  const auto qd = global_in<float>(p.qdq) + (sg.row * p.Hv + h) * p.T + sg.t0 + first, kd = global_in<float>(p.kdk) + (sg.row * p.Hv + h) * p.T + sg.t0 + first;
-  const int64_t per = (len + 255) / 256, lo = tid * per < len ? tid * per : len, hi = lo + per < len ? lo + per : len;
-  double sum = 0.0;
-  for (int64_t t = lo; t < hi; ++t) sum += (double)qd[t] - (double)kd[t];
-  // the sum of every thread's products, then what lies behind this thread's tokens
-  part[tid] = dot;
+  dot = wave_sum(dot);
+  if (lane == 0) part[wave] = dot;
   __syncthreads();
-  for (int d = 128; d > 0; d >>= 1) {
-    if (tid < d) part[tid] += part[tid + d];
+  double B = part[0] + part[1] + part[2] + part[3];   // behind the chunks taken so far
+  const int64_t at = (sg.row * p.Hv + h) * p.T + sg.t0 + first;
+  const int64_t n_chunks = (len + kGdrChunk - 1) / kGdrChunk;
+  double total = 0.0;
+  for (int64_t done = 0; done < n_chunks; done += 4) {
+    const int64_t c = n_chunks - 1 - done - wave, t = kGdrChunk * c + lane;
+    const bool live = c >= 0 && t < len;
+    double own = 0.0, across = 0.0;
+    if (live) {
+      own = p.qdq[1][at + t] - p.kdk[1][at + t];
+      across = p.qdq[0][at + t] - p.kdk[0][at + t];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double more = __shfl_down(own, d);
+      if (lane + d < 64) own += more;
+    }
+    across = wave_sum(across);
+    __syncthreads();   // the values of the turn before have been read
+    if (lane == 0) part[wave] = across;
     __syncthreads();
-  }
-  const double end = part[0];
-  __syncthreads();
-  part[tid] = sum;
-  __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const double more = tid + d < 256 ? part[tid + d] : 0.0;
-    __syncthreads();
-    part[tid] += more;
-    __syncthreads();
-  }
-  double run = end + (tid < 255 ? part[tid + 1] : 0.0), total = 0.0;
-  for (int64_t t = hi - 1; t >= lo; --t) {
-    run += (double)qd[t] - (double)kd[t];
-    if (p.w_per_head) total += run;
+    double mine = B;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) mine += part[w];
+      B += part[w];
+    }
+    if (!live) continue;
+    const double dg = mine + own;
+    if (p.w_per_head) total += dg;
     else {
       const int64_t tok = sg.t0 + first + t;
       const float w = get(global_in<T>(p.w) + sg.row * p.sw.b + h * p.sw.h + tok * p.sw.t);
-      put(global_out<T>(p.dw) + sg.row * p.sdw.b + h * p.sdw.h + tok * p.sdw.t, (float)(run * (double)gdr_gate_grad(w, p.gate, p.g_min)));
+      put(global_out<T>(p.dw) + sg.row * p.sdw.b + h * p.sdw.h + tok * p.sdw.t, (float)(dg * (double)gdr_gate_grad(w, p.gate, p.g_min)));
     }
   }
   if (!p.w_per_head) return;
+  total = wave_sum(total);
   __syncthreads();
-  part[tid] = total;
+  if (lane == 0) part[wave] = total;
   __syncthreads();
-  for (int d = 128; d > 0; d >>= 1) {
-    if (tid < d) part[tid] += part[tid + d];
-    __syncthreads();
-  }
-  if (tid == 0) p.partial[slot * p.Hv + h] = part[0];
+  if (tid == 0) p.partial[slot * p.Hv + h] = part[0] + part[1] + part[2] + part[3];
 }
 
 // dw of a w per head: the segments' sums, in a fixed order

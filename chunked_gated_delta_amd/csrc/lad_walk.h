@@ -113,15 +113,15 @@ struct Gates {
   float tot;                // e^{Ptot}
 };
 
-template <typename T, int DX, int DZ, bool OUT> struct Lds {
+template <typename T, int DX, int DZ, int PL, bool OUT> struct Lds {
   static constexpr int kWaves = DZ / 32;
   Tile<T, DX> y;
   Tile<T, DZ> z;
   Gates gates[2];
   struct Outs {
     Tile<T, DX> x;
-    char p[4][2][op_frag<T, 2>()];
-    float dots[kWaves][kC];
+    char p[4][2][op_frag<T, PL>()];
+    double dots[2][kWaves][kC];
   };
   struct None {};
   std::conditional_t<OUT, Outs, None> o;
@@ -177,15 +177,16 @@ __device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int rev
 
 }  // namespace lad
 
-// UP: planes of Z in the new state: three where it is a result in fp32, two where only outputs are taken from it.
+// PL: planes of the state and of X Y^T in the outputs; UP: of Z in the new state.  Two (off by 2^-17) where only results
+// in bf16 are taken from them, three (fp32's accuracy) for states and decays' gradients in fp32.
 // OUT false: the segment's state from zero and nothing else.
-template <typename T, int DX, int DZ, int UP, bool OUT, int OCC>
+template <typename T, int DX, int DZ, int UP, int PL, bool OUT, int OCC>
 __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   using namespace lad;
   constexpr int THREADS = 2 * DZ, NW = DZ / 32, MT = DX / 16, KS = DX / 32;
   using In = typename Frags<T>::In;
   extern __shared__ __attribute__((aligned(16))) char raw[];
-  auto& lds = *reinterpret_cast<Lds<T, DX, DZ, OUT>*>(raw);
+  auto& lds = *reinterpret_cast<Lds<T, DX, DZ, PL, OUT>*>(raw);
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, li = lane & 15, g = lane >> 4;
 
   int64_t unit;
@@ -206,27 +207,30 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   const auto row_base = [&](const void* t, kda_stride_t s, int grp) { return global_in<T>(t) + sg.row * s.b + (h / grp) * s.h; };
   const auto xb = OUT ? row_base(wk.x, wk.sx, wk.grp_x) : GlobalPtr<const T>(), yb = row_base(wk.y, wk.sy, wk.grp_y), zb = row_base(wk.z, wk.sz, wk.grp_z);
   const uint32_t xs = (uint32_t)(wk.sx.t * (int64_t)sizeof(T)), ys = (uint32_t)(wk.sy.t * (int64_t)sizeof(T)), zs = (uint32_t)(wk.sz.t * (int64_t)sizeof(T));
-  // the first token in memory of chunk c, which has `have` tokens
-  const auto chunk_at = [&](int64_t c, int have) { return sg.t0 + first + (reverse ? len - kC * c - have : kC * c); };
-  const auto chunk_have = [&](int64_t c) { return (int)(len - kC * c < kC ? len - kC * c : kC); };
+  // chunk c of the walk: its first token in memory, and its tokens.  Backwards the chunks are the same ones.
+  const int64_t n_chunks = (len + kC - 1) / kC;
+  const auto chunk_at = [&](int64_t c) { return sg.t0 + first + kC * (reverse ? n_chunks - 1 - c : c); };
+  const auto chunk_have = [&](int64_t c) {
+    const int64_t left = len - kC * (reverse ? n_chunks - 1 - c : c);
+    return (int)(left < kC ? left : kC);
+  };
 
   Rows8<T, DX, THREADS> rx, ry;
   Rows8<T, DZ, THREADS> rz;
   const auto fetch = [&](int64_t c) {
     const int have = chunk_have(c);
-    const int64_t t = chunk_at(c, have);
+    const int64_t t = chunk_at(c);
     if constexpr (OUT) rx.load(xb + t * wk.sx.t, xs, have, reverse, tid);
     ry.load(yb + t * wk.sy.t, ys, have, reverse, tid);
     rz.load(zb + t * wk.sz.t, zs, have, reverse, tid);
   };
   const auto gate_of = [&](int64_t c) {
     const int have = chunk_have(c), in = lane < have ? lane : have - 1;
-    const int64_t t = chunk_at(c, have) + (reverse ? have - 1 - in : in);
+    const int64_t t = chunk_at(c) + (reverse ? have - 1 - in : in);
     const float x = lad_decay<T>(p.w, p.w_per_head, p.sw, sg.row, h, t, p.gate, p.g_min);
     return lane < have ? x : 0.f;
   };
 
-  const int64_t n_chunks = (len + kC - 1) / kC;
   if (n_chunks > 0) fetch(0);
 
   floatx4 S[MT][2];
@@ -248,6 +252,27 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         }
       }
   }
+
+  // this wavefront's part of out . dot for every token of the chunk
+  using Dot = std::conditional_t<sizeof(T) == 4 || PL == 3, double, float>;
+  const auto row_dots = [&](int64_t c, const floatx4 (&acc)[4][2], double* out) {
+    const int have = chunk_have(c);
+    const auto base = global_in<T>(wk.dot) + sg.row * wk.sdot.b + (h / wk.grp_dot) * wk.sdot.h + 32 * wave + 8 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * i + li, in = row < have ? row : have - 1;
+      const auto f = load_row8(base + (chunk_at(c) + (reverse ? have - 1 - in : in)) * wk.sdot.t);
+      float8v d;
+      if constexpr (sizeof(T) == 2) d = __builtin_convertvector(__builtin_bit_cast(bf16x8v, f), float8v);
+      else d = f;
+      Dot s = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s += (Dot)acc[i][0][r] * (Dot)d[r] + (Dot)acc[i][1][r] * (Dot)d[4 + r];
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (g == 0) out[row] = s;
+    }
+  };
 
   double total = 0.0;
   if (wave == 0 && n_chunks > 0) put_gates(lds.gates[0], gate_of(0), lane, reverse, wk.out_scale, wk.in_scale, &total);
@@ -291,7 +316,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           const float8v f = {t[2 * ks][0], t[2 * ks][1], t[2 * ks][2], t[2 * ks][3], t[2 * ks + 1][0], t[2 * ks + 1][1], t[2 * ks + 1][2], t[2 * ks + 1][3]};
-          store_frag(lds.o.p[i][ks], lane, make_op<2>(f, T{}));
+          store_frag(lds.o.p[i][ks], lane, make_op<PL>(f, T{}));
         }
       }
     }
@@ -303,11 +328,11 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = floatx4{};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        typename Frags<T>::template Op<2> sp[2];
+        typename Frags<T>::template Op<PL> sp[2];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const floatx4 a = S[2 * ks][cc], b = S[2 * ks + 1][cc];
-          sp[cc] = make_op<2>(float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, T{});
+          sp[cc] = make_op<PL>(float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, T{});
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) mac2(sp, lds.o.x.row_frag(16 * i + li, ks, g), acc[i]);
@@ -318,6 +343,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         acc[i][0] *= oc;
         acc[i][1] *= oc;
       }
+      if (wk.dot) row_dots(c, acc, lds.o.dots[0][wave]);
       block_barrier();   // the tiles of X Y^T are there
     }
 
@@ -334,7 +360,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
       if constexpr (OUT) {
 #pragma unroll
-        for (int i = 2 * ks; i < 4; ++i) mac2(zf, load_frag<typename Frags<T>::template Op<2>>(lds.o.p[i][ks], lane), acc[i]);
+        for (int i = 2 * ks; i < 4; ++i) mac2(zf, load_frag<typename Frags<T>::template Op<PL>>(lds.o.p[i][ks], lane), acc[i]);
       }
       typename Frags<T>::template Op<UP> zu[2];
       float8v u;
@@ -359,24 +385,13 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) settle(acc[i][cc]);
-      const int64_t t0 = chunk_at(c, have);
+      if (wk.dot) row_dots(c, acc, lds.o.dots[1][wave]);
+      const int64_t t0 = chunk_at(c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = 16 * i + li;
         const int in = row < have ? row : have - 1;
         const int64_t t = t0 + (reverse ? have - 1 - in : in);
-        if (wk.dot) {
-          const auto f = load_row8(global_in<T>(wk.dot) + sg.row * wk.sdot.b + (h / wk.grp_dot) * wk.sdot.h + t * wk.sdot.t + 32 * wave + 8 * g);
-          float8v d;
-          if constexpr (sizeof(T) == 2) d = __builtin_convertvector(__builtin_bit_cast(bf16x8v, f), float8v);
-          else d = f;
-          float s = 0.f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s += acc[i][0][r] * d[r] + acc[i][1][r] * d[4 + r];
-          s += __shfl_xor(s, 16);
-          s += __shfl_xor(s, 32);
-          if (g == 0) lds.o.dots[wave][row] = s;
-        }
         if (row < have) {
           const int64_t at = sg.row * wk.so.b + h * wk.so.h + t * wk.so.t + 32 * wave + 8 * g;
           if (wk.out_f32) {
@@ -393,11 +408,15 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     }
     block_barrier();   // nobody reads this chunk's rows any more
     if constexpr (OUT) {
-      if (wk.dot && tid < kC) {
-        float s = 0.f;
+      if (wk.dot && tid < kC && tid < have) {
+        const int64_t at = (sg.row * p.Hv + h) * p.T + chunk_at(c) + (reverse ? have - 1 - tid : tid);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) s += lds.o.dots[w][tid];
-        if (tid < have) wk.dots[(sg.row * p.Hv + h) * p.T + chunk_at(c, have) + (reverse ? have - 1 - tid : tid)] = s;
+        for (int k = 0; k < 2; ++k) {
+          double s = 0.0;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) s += lds.o.dots[k][w][tid];
+          wk.dots[k][at] = s;
+        }
       }
     }
   }
@@ -424,12 +443,12 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   }
 }
 
-template <typename T, int DX, int DZ, int UP, bool OUT>
+template <typename T, int DX, int DZ, int UP, int PL, bool OUT>
 hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
-  constexpr int kLdsBytes = (int)sizeof(lad::Lds<T, DX, DZ, OUT>);
+  constexpr int kLdsBytes = (int)sizeof(lad::Lds<T, DX, DZ, PL, OUT>);
   // two workgroups a compute unit where registers and LDS allow it
   constexpr int OCC = sizeof(T) == 2 && DZ == 128 ? 2 : 1;
-  const auto kernel = lad_walk_kernel<T, DX, DZ, UP, OUT, OCC>;
+  const auto kernel = lad_walk_kernel<T, DX, DZ, UP, PL, OUT, OCC>;
   static std::atomic<uint64_t> done;
   const hipError_t set = set_dyn_lds(reinterpret_cast<const void*>(kernel), kLdsBytes, done);
   if (set != hipSuccess) return set;
@@ -438,18 +457,18 @@ hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int UP, bool OUT>
+template <typename T, int UP, int PL, bool OUT>
 hipError_t launch_walk_dims(const LadParams& p, int dx, int dz, hipStream_t s) {
   switch (dx * 256 + dz) {
-    case 32 * 256 + 32: return launch_walk_one<T, 32, 32, UP, OUT>(p, s);
-    case 32 * 256 + 64: return launch_walk_one<T, 32, 64, UP, OUT>(p, s);
-    case 32 * 256 + 128: return launch_walk_one<T, 32, 128, UP, OUT>(p, s);
-    case 64 * 256 + 32: return launch_walk_one<T, 64, 32, UP, OUT>(p, s);
-    case 64 * 256 + 64: return launch_walk_one<T, 64, 64, UP, OUT>(p, s);
-    case 64 * 256 + 128: return launch_walk_one<T, 64, 128, UP, OUT>(p, s);
-    case 128 * 256 + 32: return launch_walk_one<T, 128, 32, UP, OUT>(p, s);
-    case 128 * 256 + 64: return launch_walk_one<T, 128, 64, UP, OUT>(p, s);
-    default: return launch_walk_one<T, 128, 128, UP, OUT>(p, s);
+    case 32 * 256 + 32: return launch_walk_one<T, 32, 32, UP, PL, OUT>(p, s);
+    case 32 * 256 + 64: return launch_walk_one<T, 32, 64, UP, PL, OUT>(p, s);
+    case 32 * 256 + 128: return launch_walk_one<T, 32, 128, UP, PL, OUT>(p, s);
+    case 64 * 256 + 32: return launch_walk_one<T, 64, 32, UP, PL, OUT>(p, s);
+    case 64 * 256 + 64: return launch_walk_one<T, 64, 64, UP, PL, OUT>(p, s);
+    case 64 * 256 + 128: return launch_walk_one<T, 64, 128, UP, PL, OUT>(p, s);
+    case 128 * 256 + 32: return launch_walk_one<T, 128, 32, UP, PL, OUT>(p, s);
+    case 128 * 256 + 64: return launch_walk_one<T, 128, 64, UP, PL, OUT>(p, s);
+    default: return launch_walk_one<T, 128, 128, UP, PL, OUT>(p, s);
   }
 }
 
