@@ -23,6 +23,7 @@ namespace kda {
 namespace lad {
 
 constexpr int kC = kGdrChunk;
+enum { kStates, kOuts, kDots, kParts };
 
 __device__ __forceinline__ int sigma(int m) { return m < 8 ? 2 * m : 2 * (m - 8) + 1; }
 __device__ __forceinline__ int zcol(int c, int m) { return 8 * (m >> 2) + 4 * c + (m & 3); }
@@ -107,86 +108,112 @@ template <typename T, int D> struct Tile {
   }
 };
 
+// place of a chunk's token in the order of key tiles
+__device__ __forceinline__ int key_place(int t) { return (t & 48) + ((t & 15) >> 1) + ((t & 1) << 3); }
+
+// by key_place of the chunk's tokens
 struct Gates {
   float hi[kC], lo[kC];     // the prefix as a sum of two floats: differences stay exact beside a reset
   float oc[kC], uc[kC];     // e^{P} out_scale,  e^{Ptot - P} in_scale
   float tot;                // e^{Ptot}
 };
 
-template <typename T, int DX, int DZ, int PL, bool OUT> struct Lds {
+template <typename T, int DX, int DZ, int PL, int MODE> struct Lds {
   static constexpr int kWaves = DZ / 32;
+  using Dot = std::conditional_t<sizeof(T) == 4 || PL == 3, double, float>;
   Tile<T, DX> y;
   Tile<T, DZ> z;
-  Gates gates[2];
+  Gates gates[2][kWaves];
+  double total[kWaves];
   struct Outs {
     Tile<T, DX> x;
     char p[4][2][op_frag<T, PL>()];
-    double dots[2][kWaves][kC];
   };
   struct None {};
-  std::conditional_t<OUT, Outs, None> o;
+  std::conditional_t<MODE != kStates, Outs, None> o;
+  Dot dots[MODE >= kDots ? 2 : 0][kWaves][kC];
 };
+
+// Memory is read and written through buffer descriptors over a chunk's rows: an offset behind them reads zeros and writes
+// nothing, so that rows behind a sequence's end need no branch, and the waits for loads under way count exactly
+// what lies behind them.  A chunk's rows lie within 2^31 bytes.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+typedef unsigned int u32x4v __attribute__((ext_vector_type(4)));
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ Buffer buffer(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
+}
+__device__ __forceinline__ bf16x8 buffer_row8(Buffer b, uint32_t at, uint16_t) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
+}
+__device__ __forceinline__ float8v buffer_row8(Buffer b, uint32_t at, float) {
+  const floatx4 lo = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
+  const floatx4 hi = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 16, 0));
+  return float8v{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+__device__ __forceinline__ uint16_t buffer_one(Buffer b, uint32_t at, uint16_t) { return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, (int)at, 0, 0); }
+__device__ __forceinline__ float buffer_one(Buffer b, uint32_t at, float) { return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, (int)at, 0, 0)); }
+template <typename V> __device__ __forceinline__ void buffer_put16(Buffer b, uint32_t at, V x, int more = 0) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, x), b, (int)at, more, 0);
+}
 
 // one chunk's rows under way from memory
 template <typename T, int D, int THREADS> struct Rows8 {
-  static constexpr int kPieces = D / 8, kLoads = kC * kPieces / THREADS;
+  static constexpr int kPieces = D / 8, kLoads = kC * kPieces / THREADS, kStep = THREADS / kPieces;
+  static_assert(THREADS % kPieces == 0 && kLoads * kStep == kC, "whole rows");
   using In = typename Frags<T>::In;
   In v[kLoads];
-  // `row0` the chunk's first row in memory, tokens at `stride` bytes; chunk rows `have` and more are zeros.  Backwards
-  // row0 is the chunk's last token in the walk's order.  have >= 1.
-  __device__ __forceinline__ void load(GlobalPtr<const T> row0, uint32_t stride, int have, int reverse, int tid) {
+  // chunk row `row` is memory row `row`, or have - 1 - row backwards; rows `have` and more are zeros
+  __device__ __forceinline__ void load(Buffer b, uint32_t stride, int have, int reverse, int tid) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int piece = i * THREADS + tid, row = piece / kPieces, c = piece % kPieces * 8;
-      const int in = row < have ? row : have - 1;
-      const uint32_t at = (uint32_t)(reverse ? have - 1 - in : in) * stride + c * (uint32_t)sizeof(T);
-      v[i] = load_row8(lane_at(row0, at));
+      const int row = i * kStep + tid / kPieces;
+      const uint32_t at = (uint32_t)(reverse ? have - 1 - row : row) * stride + (tid % kPieces) * 8 * (uint32_t)sizeof(T);
+      v[i] = buffer_row8(b, row < have ? at : kNowhere, T{});
     }
   }
-  __device__ __forceinline__ void leave(Tile<T, D>& t, int have, int tid) {
+  __device__ __forceinline__ void leave(Tile<T, D>& t, int tid) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int piece = i * THREADS + tid, row = piece / kPieces, c = piece % kPieces * 8;
-      In zero;
-      zero_frag(zero);
-      t.put8(row, c, row < have ? v[i] : zero);
-    }
+    for (int i = 0; i < kLoads; ++i) t.put8(i * kStep + tid / kPieces, tid % kPieces * 8, v[i]);
   }
 };
 
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end).
-__device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale, double* total) {
+// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end); returns their sum.
+__device__ __forceinline__ double put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale) {
   double p = g;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const double up = __shfl_up(p, d);
-    if (lane >= d) p += up;
+    p += lane >= d ? up : 0.0;
   }
   const double tot = __shfl(p, 63);
-  if (reverse) p -= (double)g;
-  const float hi = (float)p;
-  out.hi[lane] = hi;
-  out.lo[lane] = (float)(p - (double)hi);
-  out.oc[lane] = exp_fast(hi) * out_scale;
-  out.uc[lane] = exp_fast((float)(tot - p)) * in_scale;
-  if (lane == 0) out.tot = exp_fast((float)tot);
-  *total += tot;
+  p -= reverse ? (double)g : 0.0;
+  const float hi = (float)p, lo = (float)(p - (double)hi);
+  const int place = key_place(lane);
+  out.hi[place] = hi;
+  out.lo[place] = lo;
+  out.oc[place] = exp_fast(hi) * out_scale;
+  out.uc[place] = exp_fast((float)(tot - p)) * in_scale;
+  out.tot = exp_fast((float)tot);
+  return tot;
 }
 
 }  // namespace lad
 
 // PL: planes of the state and of X Y^T in the outputs; UP: of Z in the new state.  Two (off by 2^-17) where only results
 // in bf16 are taken from them, three (fp32's accuracy) for states and decays' gradients in fp32.
-// OUT false: the segment's state from zero and nothing else.
-template <typename T, int DX, int DZ, int UP, int PL, bool OUT, int OCC>
+// MODE: what a walk leaves behind.  kStates: the segment's state from zero and nothing else; kOuts: outputs of type T;
+// kDots: also their products with rows of another tensor; kParts: the same with outputs that may be in fp32.
+template <typename T, int DX, int DZ, int UP, int PL, int MODE, int OCC>
 __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   using namespace lad;
+  constexpr bool OUT = MODE != kStates, DOTS = MODE >= kDots;
   constexpr int THREADS = 2 * DZ, NW = DZ / 32, MT = DX / 16, KS = DX / 32;
   using In = typename Frags<T>::In;
   extern __shared__ __attribute__((aligned(16))) char raw[];
-  auto& lds = *reinterpret_cast<Lds<T, DX, DZ, PL, OUT>*>(raw);
+  auto& lds = *reinterpret_cast<Lds<T, DX, DZ, PL, MODE>*>(raw);
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, li = lane & 15, g = lane >> 4;
 
   int64_t unit;
@@ -204,9 +231,6 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   const bool end = reverse ? sg.seg == 0 : sg.seg == sg.n_seg - 1;       // no segment behind it in the walk's order
   if (wk.skip_end && end) return;
 
-  const auto row_base = [&](const void* t, kda_stride_t s, int grp) { return global_in<T>(t) + sg.row * s.b + (h / grp) * s.h; };
-  const auto xb = OUT ? row_base(wk.x, wk.sx, wk.grp_x) : GlobalPtr<const T>(), yb = row_base(wk.y, wk.sy, wk.grp_y), zb = row_base(wk.z, wk.sz, wk.grp_z);
-  const uint32_t xs = (uint32_t)(wk.sx.t * (int64_t)sizeof(T)), ys = (uint32_t)(wk.sy.t * (int64_t)sizeof(T)), zs = (uint32_t)(wk.sz.t * (int64_t)sizeof(T));
   // chunk c of the walk: its first token in memory, and its tokens.  Backwards the chunks are the same ones.
   const int64_t n_chunks = (len + kC - 1) / kC;
   const auto chunk_at = [&](int64_t c) { return sg.t0 + first + kC * (reverse ? n_chunks - 1 - c : c); };
@@ -214,24 +238,46 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     const int64_t left = len - kC * (reverse ? n_chunks - 1 - c : c);
     return (int)(left < kC ? left : kC);
   };
+  // the first token of the sequence's part of a tensor; a chunk's rows from there
+  const auto rows_of = [&](const void* t, kda_stride_t s, int grp) { return static_cast<const T*>(t) + sg.row * s.b + (h / grp) * s.h; };
+  const T* xb = OUT ? rows_of(wk.x, wk.sx, wk.grp_x) : nullptr;
+  const T *yb = rows_of(wk.y, wk.sy, wk.grp_y), *zb = rows_of(wk.z, wk.sz, wk.grp_z);
+  const int64_t xs = wk.sx.t, ys = wk.sy.t, zs = wk.sz.t;
+  constexpr uint32_t E = sizeof(T);
 
   Rows8<T, DX, THREADS> rx, ry;
   Rows8<T, DZ, THREADS> rz;
   const auto fetch = [&](int64_t c) {
     const int have = chunk_have(c);
     const int64_t t = chunk_at(c);
-    if constexpr (OUT) rx.load(xb + t * wk.sx.t, xs, have, reverse, tid);
-    ry.load(yb + t * wk.sy.t, ys, have, reverse, tid);
-    rz.load(zb + t * wk.sz.t, zs, have, reverse, tid);
+    if constexpr (OUT) rx.load(buffer(xb + t * xs), (uint32_t)xs * E, have, reverse, tid);
+    ry.load(buffer(yb + t * ys), (uint32_t)ys * E, have, reverse, tid);
+    rz.load(buffer(zb + t * zs), (uint32_t)zs * E, have, reverse, tid);
   };
-  const auto gate_of = [&](int64_t c) {
-    const int have = chunk_have(c), in = lane < have ? lane : have - 1;
-    const int64_t t = chunk_at(c) + (reverse ? have - 1 - in : in);
-    const float x = lad_decay<T>(p.w, p.w_per_head, p.sw, sg.row, h, t, p.gate, p.g_min);
-    return lane < have ? x : 0.f;
+  // Each wavefront forms the gates of one chunk in NW, all at the same time; their values of w are asked for as many
+  // chunks before.
+  const float head_w = p.w_per_head && p.w ? global_in<float>(p.w)[h] : 0.f;
+  const T* wb = static_cast<const T*>(p.w) + (p.w_per_head ? 0 : sg.row * p.sw.b + h * p.sw.h);
+  const auto gate_ask = [&](int64_t c) {
+    const int have = c < n_chunks ? chunk_have(c) : 0;
+    const int64_t t = c < n_chunks ? chunk_at(c) : 0;
+    const uint32_t at = (uint32_t)(reverse ? have - 1 - lane : lane) * ((uint32_t)p.sw.t * E);
+    return buffer_one(buffer(wb + (p.w_per_head ? 0 : t * p.sw.t)), p.w_per_head || lane >= have ? kNowhere : at, T{});
+  };
+  const auto gate_of = [&](int64_t c, T asked) {
+    float x;
+    if constexpr (sizeof(T) == 2) x = bf16_to_f32(asked);
+    else x = asked;
+    const float g = gdr_gate(p.w_per_head ? head_w : x, p.gate, p.g_min);
+    return c < n_chunks && lane < chunk_have(c) ? g : 0.f;
   };
 
-  if (n_chunks > 0) fetch(0);
+  double total = 0.0;
+  T asked{};
+  if (n_chunks > 0) {
+    asked = gate_ask(wave);
+    fetch(0);
+  }
 
   floatx4 S[MT][2];
   {
@@ -254,47 +300,58 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   }
 
   // this wavefront's part of out . dot for every token of the chunk
-  using Dot = std::conditional_t<sizeof(T) == 4 || PL == 3, double, float>;
-  const auto row_dots = [&](int64_t c, const floatx4 (&acc)[4][2], double* out) {
+  using Dot = typename Lds<T, DX, DZ, PL, MODE>::Dot;
+  In dots[DOTS ? 4 : 1];
+  const auto ask_dots = [&](int64_t c) {
     const int have = chunk_have(c);
-    const auto base = global_in<T>(wk.dot) + sg.row * wk.sdot.b + (h / wk.grp_dot) * wk.sdot.h + 32 * wave + 8 * g;
+    const Buffer b = buffer(rows_of(wk.dot, wk.sdot, wk.grp_dot) + chunk_at(c) * wk.sdot.t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = 16 * i + li, in = row < have ? row : have - 1;
-      const auto f = load_row8(base + (chunk_at(c) + (reverse ? have - 1 - in : in)) * wk.sdot.t);
+      const int row = 16 * i + li;
+      const uint32_t at = (uint32_t)(reverse ? have - 1 - row : row) * ((uint32_t)wk.sdot.t * E) + (32 * wave + 8 * g) * E;
+      dots[i] = buffer_row8(b, wk.dot && row < have ? at : kNowhere, T{});
+    }
+  };
+  const auto row_dots = [&](const floatx4 (&acc)[4][2], Dot* out) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       float8v d;
-      if constexpr (sizeof(T) == 2) d = __builtin_convertvector(__builtin_bit_cast(bf16x8v, f), float8v);
-      else d = f;
+      if constexpr (sizeof(T) == 2) d = __builtin_convertvector(__builtin_bit_cast(bf16x8v, dots[i]), float8v);
+      else d = dots[i];
       Dot s = 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) s += (Dot)acc[i][0][r] * (Dot)d[r] + (Dot)acc[i][1][r] * (Dot)d[4 + r];
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
-      if (g == 0) out[row] = s;
+      if (g == 0) out[16 * i + li] = s;
     }
   };
 
-  double total = 0.0;
-  if (wave == 0 && n_chunks > 0) put_gates(lds.gates[0], gate_of(0), lane, reverse, wk.out_scale, wk.in_scale, &total);
+  if (n_chunks > 0) {
+    total += put_gates(lds.gates[0][wave], gate_of(wave, asked), lane, reverse, wk.out_scale, wk.in_scale);
+    asked = gate_ask(NW + wave);
+    if constexpr (OUT) rx.leave(lds.o.x, tid);
+    ry.leave(lds.y, tid);
+    rz.leave(lds.z, tid);
+  }
+  block_barrier();
 
   for (int64_t c = 0; c < n_chunks; ++c) {
     const int have = chunk_have(c);
-    const Gates& gt = lds.gates[c & 1];
-    if constexpr (OUT) rx.leave(lds.o.x, have, tid);
-    ry.leave(lds.y, have, tid);
-    rz.leave(lds.z, have, tid);
-    block_barrier();
-    const int64_t next = c + 1 < n_chunks ? c + 1 : c;   // the last chunk asks for its own rows again
-    fetch(next);
-    float gn = 0.f;
-    if (wave == 0) gn = gate_of(next);
+    const Gates& gt = lds.gates[c / NW & 1][c % NW];
+    if (c % NW == NW - 1) {   // the gates of the next NW chunks
+      const int64_t mine = c + 1 + wave;
+      total += put_gates(lds.gates[(c + 1) / NW & 1][wave], gate_of(mine, asked), lane, reverse, wk.out_scale, wk.in_scale);
+      asked = gate_ask(mine + NW);
+    }
+    fetch(c + 1 < n_chunks ? c + 1 : c);   // the last chunk asks for its own rows again
 
     if constexpr (OUT) {
       // this wavefront's row tiles of the decayed X Y^T, transposed: column li is token 16 i + li
 #pragma unroll
       for (int ii = 0; ii < 4 / NW; ++ii) {
         const int i = wave + ii * NW;
-        const float qh = gt.hi[16 * i + li], ql = gt.lo[16 * i + li];
+        const float qh = gt.hi[16 * i + key_place(li)], ql = gt.lo[16 * i + key_place(li)];
         floatx4 t[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) t[j] = floatx4{};
@@ -306,11 +363,12 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          // exponents of later keys are put where the exponential is 0: selecting the product would put it behind a branch
+          const floatx4 kh = *reinterpret_cast<const floatx4*>(gt.hi + 16 * j + 4 * g), kl = *reinterpret_cast<const floatx4*>(gt.lo + 16 * j + 4 * g);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int key = 16 * j + sigma(4 * g + r);
-            const float e = exp_fast((qh - gt.hi[key]) + (ql - gt.lo[key])) * (wk.out_scale * wk.in_scale);
-            t[j][r] = key <= 16 * i + li ? t[j][r] * e : 0.f;
+            const float e = (qh - kh[r]) + (ql - kl[r]);
+            t[j][r] *= exp_fast(16 * j + sigma(4 * g + r) <= 16 * i + li ? e : -1e30f) * (wk.out_scale * wk.in_scale);
           }
         }
 #pragma unroll
@@ -320,8 +378,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         }
       }
     }
-    if (wave == 0) put_gates(lds.gates[(c + 1) & 1], c + 1 < n_chunks ? gn : 0.f, lane, reverse, wk.out_scale, wk.in_scale, &total);
-
+    if constexpr (DOTS) ask_dots(c);
     floatx4 acc[4][2];
     if constexpr (OUT) {
 #pragma unroll
@@ -339,11 +396,11 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float oc = gt.oc[16 * i + li];
+        const float oc = gt.oc[16 * i + key_place(li)];
         acc[i][0] *= oc;
         acc[i][1] *= oc;
       }
-      if (wk.dot) row_dots(c, acc, lds.o.dots[0][wave]);
+      if constexpr (DOTS) row_dots(acc, lds.dots[0][wave]);
       block_barrier();   // the tiles of X Y^T are there
     }
 
@@ -363,12 +420,8 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         for (int i = 2 * ks; i < 4; ++i) mac2(zf, load_frag<typename Frags<T>::template Op<PL>>(lds.o.p[i][ks], lane), acc[i]);
       }
       typename Frags<T>::template Op<UP> zu[2];
-      float8v u;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        u[r] = gt.uc[32 * ks + sigma(4 * g + r)];
-        u[4 + r] = gt.uc[32 * ks + 16 + sigma(4 * g + r)];
-      }
+      const floatx4 u0 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 4 * g), u1 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 16 + 4 * g);
+      const float8v u = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         float8v f;
@@ -385,43 +438,50 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) settle(acc[i][cc]);
-      if (wk.dot) row_dots(c, acc, lds.o.dots[1][wave]);
-      const int64_t t0 = chunk_at(c);
+      if constexpr (DOTS) row_dots(acc, lds.dots[1][wave]);
+      const int64_t out_row = sg.row * wk.so.b + h * wk.so.h + chunk_at(c) * wk.so.t;
+      const bool wide = MODE == kParts && wk.out_f32;
+      const uint32_t esz = wide ? 4 : E, ostep = (uint32_t)wk.so.t * esz;
+      const Buffer ob = buffer(static_cast<char*>(wk.out) + out_row * esz);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = 16 * i + li;
-        const int in = row < have ? row : have - 1;
-        const int64_t t = t0 + (reverse ? have - 1 - in : in);
-        if (row < have) {
-          const int64_t at = sg.row * wk.so.b + h * wk.so.h + t * wk.so.t + 32 * wave + 8 * g;
-          if (wk.out_f32) {
-            store_row4(global_out<float>(wk.out) + at, acc[i][0]);
-            store_row4(global_out<float>(wk.out) + at + 4, acc[i][1]);
-          } else if constexpr (sizeof(T) == 2) {
-            *repoint<bf16x8>(global_out<uint16_t>(wk.out) + at) = pack2(acc[i][0], acc[i][1]);
-          } else {
-            store_row4(global_out<float>(wk.out) + at, acc[i][0]);
-            store_row4(global_out<float>(wk.out) + at + 4, acc[i][1]);
-          }
+        const uint32_t at = row < have ? (uint32_t)(reverse ? have - 1 - row : row) * ostep + (32 * wave + 8 * g) * esz : kNowhere;
+        if constexpr (sizeof(T) == 2) buffer_put16(ob, wide ? kNowhere : at, pack2(acc[i][0], acc[i][1]));
+        if constexpr (sizeof(T) == 4 || MODE == kParts) {
+          buffer_put16(ob, sizeof(T) == 4 || wide ? at : kNowhere, acc[i][0]);
+          buffer_put16(ob, sizeof(T) == 4 || wide ? at : kNowhere, acc[i][1], 16);
         }
       }
     }
     block_barrier();   // nobody reads this chunk's rows any more
-    if constexpr (OUT) {
+    if constexpr (OUT) rx.leave(lds.o.x, tid);
+    ry.leave(lds.y, tid);
+    rz.leave(lds.z, tid);
+    if constexpr (DOTS) {
       if (wk.dot && tid < kC && tid < have) {
         const int64_t at = (sg.row * p.Hv + h) * p.T + chunk_at(c) + (reverse ? have - 1 - tid : tid);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           double s = 0.0;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) s += lds.o.dots[k][w][tid];
+          for (int w = 0; w < NW; ++w) s += lds.dots[k][w][tid];
           wk.dots[k][at] = s;
         }
       }
     }
+    block_barrier();
   }
 
-  if (wk.decay && tid == 0) wk.decay[slot * p.Hv + h] = exp_fast((float)total);
+  if (wk.decay) {
+    lds.total[wave] = total;
+    block_barrier();
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 1; w < NW; ++w) total += lds.total[w];
+      wk.decay[slot * p.Hv + h] = exp_fast((float)total);
+    }
+  }
   if (wk.leaving && (wk.leave_slot || end)) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -443,12 +503,12 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   }
 }
 
-template <typename T, int DX, int DZ, int UP, int PL, bool OUT>
+template <typename T, int DX, int DZ, int UP, int PL, int MODE>
 hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
-  constexpr int kLdsBytes = (int)sizeof(lad::Lds<T, DX, DZ, PL, OUT>);
+  constexpr int kLdsBytes = (int)sizeof(lad::Lds<T, DX, DZ, PL, MODE>);
   // two workgroups a compute unit where registers and LDS allow it
-  constexpr int OCC = sizeof(T) == 2 && DZ == 128 ? 2 : 1;
-  const auto kernel = lad_walk_kernel<T, DX, DZ, UP, PL, OUT, OCC>;
+  constexpr int OCC = sizeof(T) == 2 && DZ == 128 && PL == 2 ? 2 : 1;
+  const auto kernel = lad_walk_kernel<T, DX, DZ, UP, PL, MODE, OCC>;
   static std::atomic<uint64_t> done;
   const hipError_t set = set_dyn_lds(reinterpret_cast<const void*>(kernel), kLdsBytes, done);
   if (set != hipSuccess) return set;
@@ -457,18 +517,18 @@ hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int UP, int PL, bool OUT>
+template <typename T, int UP, int PL, int MODE>
 hipError_t launch_walk_dims(const LadParams& p, int dx, int dz, hipStream_t s) {
   switch (dx * 256 + dz) {
-    case 32 * 256 + 32: return launch_walk_one<T, 32, 32, UP, PL, OUT>(p, s);
-    case 32 * 256 + 64: return launch_walk_one<T, 32, 64, UP, PL, OUT>(p, s);
-    case 32 * 256 + 128: return launch_walk_one<T, 32, 128, UP, PL, OUT>(p, s);
-    case 64 * 256 + 32: return launch_walk_one<T, 64, 32, UP, PL, OUT>(p, s);
-    case 64 * 256 + 64: return launch_walk_one<T, 64, 64, UP, PL, OUT>(p, s);
-    case 64 * 256 + 128: return launch_walk_one<T, 64, 128, UP, PL, OUT>(p, s);
-    case 128 * 256 + 32: return launch_walk_one<T, 128, 32, UP, PL, OUT>(p, s);
-    case 128 * 256 + 64: return launch_walk_one<T, 128, 64, UP, PL, OUT>(p, s);
-    default: return launch_walk_one<T, 128, 128, UP, PL, OUT>(p, s);
+    case 32 * 256 + 32: return launch_walk_one<T, 32, 32, UP, PL, MODE>(p, s);
+    case 32 * 256 + 64: return launch_walk_one<T, 32, 64, UP, PL, MODE>(p, s);
+    case 32 * 256 + 128: return launch_walk_one<T, 32, 128, UP, PL, MODE>(p, s);
+    case 64 * 256 + 32: return launch_walk_one<T, 64, 32, UP, PL, MODE>(p, s);
+    case 64 * 256 + 64: return launch_walk_one<T, 64, 64, UP, PL, MODE>(p, s);
+    case 64 * 256 + 128: return launch_walk_one<T, 64, 128, UP, PL, MODE>(p, s);
+    case 128 * 256 + 32: return launch_walk_one<T, 128, 32, UP, PL, MODE>(p, s);
+    case 128 * 256 + 64: return launch_walk_one<T, 128, 64, UP, PL, MODE>(p, s);
+    default: return launch_walk_one<T, 128, 128, UP, PL, MODE>(p, s);
   }
 }
 
