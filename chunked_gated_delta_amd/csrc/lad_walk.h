@@ -22,6 +22,7 @@ namespace kda {
 
 namespace lad {
 
+typedef short short8 __attribute__((ext_vector_type(8)));
 constexpr int kC = kGdrChunk;
 enum { kStates, kOuts, kDots, kParts };
 
@@ -30,6 +31,10 @@ __device__ __forceinline__ int zcol(int c, int m) { return 8 * (m >> 2) + 4 * c 
 
 __device__ __forceinline__ floatx4 mac(bf16x8 a, bf16x8 b, floatx4 c) { return mfma(a, b, c); }
 __device__ __forceinline__ floatx4 mac(const float8v& a, const float8v& b, floatx4 c) { return mma(a, b, c); }
+
+// The compiler's schedule puts an LDS read right in front of its use, whose latency a wavefront then waits for (45 times a
+// chunk): reads are asked for a step ahead, and nothing crosses this.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // c[i] += a[i] b over planes of one side; the accumulators in turn, so that no product waits for the one before
 template <int N> __device__ __forceinline__ void mac2(const Planes<N> (&a)[2], bf16x8 b, floatx4 (&c)[2]) {
@@ -63,6 +68,40 @@ __device__ __forceinline__ void mac2(const float8v& a, const float8v (&b)[2], fl
     for (int i = 0; i < 2; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[i][e], c[i], 0, 0, 0);
 }
 
+// Values as planes of bf16, two at a time: a wider conversion compiles to one instruction a value.
+template <int N> __device__ __forceinline__ Planes<N> planes_of(const float8v& x, uint16_t) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 p[N];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t h = pk_bf16(a, b);
+      p[n][i] = h;
+      if (n + 1 < N) {
+        a -= lo_bf16(h);
+        b -= hi_bf16(h);
+      }
+    }
+  }
+  Planes<N> r;
+#pragma unroll
+  for (int n = 0; n < N; ++n) r.p[n] = __builtin_bit_cast(bf16x8, p[n]);
+  return r;
+}
+template <int N> __device__ __forceinline__ float8v planes_of(const float8v& x, float) { return x; }
+__device__ __forceinline__ bf16x8 round8(floatx4 a, floatx4 b) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(bf16x8, u32x4{pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(b[0], b[1]), pk_bf16(b[2], b[3])});
+}
+__device__ __forceinline__ float8v widen(bf16x8 f, uint16_t) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 w = __builtin_bit_cast(u32x4, f);
+  return float8v{lo_bf16(w[0]), hi_bf16(w[0]), lo_bf16(w[1]), hi_bf16(w[1]), lo_bf16(w[2]), hi_bf16(w[2]), lo_bf16(w[3]), hi_bf16(w[3])};
+}
+__device__ __forceinline__ float8v widen(const float8v& f, float) { return f; }
+
 // A chunk's rows in LDS.
 template <typename T, int D> struct Tile {
   static constexpr int kLd = sizeof(T) == 2 ? D + 8 : D + 4;
@@ -74,6 +113,21 @@ template <typename T, int D> struct Tile {
       *reinterpret_cast<floatx4*>(x + row * kLd + c) = floatx4{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<floatx4*>(x + row * kLd + c + 4) = floatx4{v[4], v[5], v[6], v[7]};
     }
+  }
+  // The same for rows that are read by row_pair only: bf16 values {4g + r, 16 + 4g + r} of 32 lie side by side, one read in
+  // place of two with addresses of their own.
+  __device__ __forceinline__ void put8_paired(int row, int c, const In& v) {
+    if constexpr (sizeof(T) == 2) {
+      T* at = x + row * kLd + (c & ~31) + (c & 8) * 2 + (c & 16) / 4;
+      const bf16x4 lo = __builtin_shufflevector(__builtin_bit_cast(short8, v), __builtin_bit_cast(short8, v), 0, 1, 2, 3);
+      const bf16x4 hi = __builtin_shufflevector(__builtin_bit_cast(short8, v), __builtin_bit_cast(short8, v), 4, 5, 6, 7);
+      *reinterpret_cast<bf16x4*>(at) = lo;
+      *reinterpret_cast<bf16x4*>(at + 8) = hi;
+    } else put8(row, c, v);
+  }
+  __device__ __forceinline__ In row_pair(int row, int ks, int g) const {
+    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const In*>(x + row * kLd + 32 * ks + 8 * g);
+    else return row_frag(row, ks, g);
   }
   // row `row`, channels {32 ks + 4g + r, 32 ks + 16 + 4g + r}
   __device__ __forceinline__ In row_frag(int row, int ks, int g) const {
@@ -143,12 +197,13 @@ constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ Buffer buffer(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
 }
-__device__ __forceinline__ bf16x8 buffer_row8(Buffer b, uint32_t at, uint16_t) {
-  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
+// 8 values at `at` (of a lane) + `more` (of the wavefront)
+__device__ __forceinline__ bf16x8 buffer_row8(Buffer b, uint32_t at, uint32_t more, uint16_t) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, (int)more, 0));
 }
-__device__ __forceinline__ float8v buffer_row8(Buffer b, uint32_t at, float) {
-  const floatx4 lo = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
-  const floatx4 hi = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 16, 0));
+__device__ __forceinline__ float8v buffer_row8(Buffer b, uint32_t at, uint32_t more, float) {
+  const floatx4 lo = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, (int)more, 0));
+  const floatx4 hi = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, (int)more + 16, 0));
   return float8v{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 __device__ __forceinline__ uint16_t buffer_one(Buffer b, uint32_t at, uint16_t) { return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, (int)at, 0, 0); }
@@ -165,38 +220,49 @@ template <typename T, int D, int THREADS> struct Rows8 {
   In v[kLoads];
   // chunk row `row` is memory row `row`, or have - 1 - row backwards; rows `have` and more are zeros
   __device__ __forceinline__ void load(Buffer b, uint32_t stride, int have, int reverse, int tid) {
+    const int r = tid / kPieces, c = tid % kPieces * 8 * (int)sizeof(T);
+    if (have == kC) {   // whole: one address a lane, the rest is the wavefront's
+      const uint32_t at = (uint32_t)(reverse ? kStep - 1 - r : r) * stride + c;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = i * kStep + tid / kPieces;
-      const uint32_t at = (uint32_t)(reverse ? have - 1 - row : row) * stride + (tid % kPieces) * 8 * (uint32_t)sizeof(T);
-      v[i] = buffer_row8(b, row < have ? at : kNowhere, T{});
+      for (int i = 0; i < kLoads; ++i) v[i] = buffer_row8(b, at, (uint32_t)(reverse ? kC - (i + 1) * kStep : i * kStep) * stride, T{});
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = i * kStep + r;
+        v[i] = buffer_row8(b, row < have ? (uint32_t)(reverse ? have - 1 - row : row) * stride + c : kNowhere, 0u, T{});
+      }
     }
   }
-  __device__ __forceinline__ void leave(Tile<T, D>& t, int tid) {
+  template <bool PAIRED = false> __device__ __forceinline__ void leave(Tile<T, D>& t, int tid) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) t.put8(i * kStep + tid / kPieces, tid % kPieces * 8, v[i]);
+    for (int i = 0; i < kLoads; ++i) {
+      if constexpr (PAIRED) t.put8_paired(i * kStep + tid / kPieces, tid % kPieces * 8, v[i]);
+      else t.put8(i * kStep + tid / kPieces, tid % kPieces * 8, v[i]);
+    }
   }
 };
 
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end); returns their sum.
+// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end), prefixes in units of ln 2;
+// returns their sum.
 __device__ __forceinline__ double put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale) {
-  double p = g;
+  const double own = (double)g * 1.4426950408889634074;
+  double p = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const double up = __shfl_up(p, d);
     p += lane >= d ? up : 0.0;
   }
   const double tot = __shfl(p, 63);
-  p -= reverse ? (double)g : 0.0;
+  p -= reverse ? own : 0.0;
   const float hi = (float)p, lo = (float)(p - (double)hi);
   const int place = key_place(lane);
   out.hi[place] = hi;
   out.lo[place] = lo;
-  out.oc[place] = exp_fast(hi) * out_scale;
-  out.uc[place] = exp_fast((float)(tot - p)) * in_scale;
-  out.tot = exp_fast((float)tot);
+  out.oc[place] = exp2_fast(hi) * out_scale;
+  out.uc[place] = exp2_fast((float)(tot - p)) * in_scale;
+  out.tot = exp2_fast((float)tot);
   return tot;
 }
 
@@ -309,15 +375,13 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     for (int i = 0; i < 4; ++i) {
       const int row = 16 * i + li;
       const uint32_t at = (uint32_t)(reverse ? have - 1 - row : row) * ((uint32_t)wk.sdot.t * E) + (32 * wave + 8 * g) * E;
-      dots[i] = buffer_row8(b, wk.dot && row < have ? at : kNowhere, T{});
+      dots[i] = buffer_row8(b, wk.dot && row < have ? at : kNowhere, 0u, T{});
     }
   };
   const auto row_dots = [&](const floatx4 (&acc)[4][2], Dot* out) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float8v d;
-      if constexpr (sizeof(T) == 2) d = __builtin_convertvector(__builtin_bit_cast(bf16x8v, dots[i]), float8v);
-      else d = dots[i];
+      const float8v d = widen(dots[i], T{});
       Dot s = 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) s += (Dot)acc[i][0][r] * (Dot)d[r] + (Dot)acc[i][1][r] * (Dot)d[4 + r];
@@ -330,7 +394,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   if (n_chunks > 0) {
     total += put_gates(lds.gates[0][wave], gate_of(wave, asked), lane, reverse, wk.out_scale, wk.in_scale);
     asked = gate_ask(NW + wave);
-    if constexpr (OUT) rx.leave(lds.o.x, tid);
+    if constexpr (OUT) rx.template leave<true>(lds.o.x, tid);
     ry.leave(lds.y, tid);
     rz.leave(lds.z, tid);
   }
@@ -344,56 +408,91 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       total += put_gates(lds.gates[(c + 1) / NW & 1][wave], gate_of(mine, asked), lane, reverse, wk.out_scale, wk.in_scale);
       asked = gate_ask(mine + NW);
     }
-    fetch(c + 1 < n_chunks ? c + 1 : c);   // the last chunk asks for its own rows again
-
     if constexpr (OUT) {
       // this wavefront's row tiles of the decayed X Y^T, transposed: column li is token 16 i + li
 #pragma unroll
       for (int ii = 0; ii < 4 / NW; ++ii) {
         const int i = wave + ii * NW;
-        const float qh = gt.hi[16 * i + key_place(li)], ql = gt.lo[16 * i + key_place(li)];
         floatx4 t[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) t[j] = floatx4{};
+        In xf[2], yf[2][4];
+        const auto ask = [&](int ks) {
+          xf[ks & 1] = lds.o.x.row_pair(16 * i + li, ks, g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) yf[ks & 1][j] = lds.y.row_frag(16 * j + sigma(li), ks, g);
+        };
+        ask(0);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const In xf = lds.o.x.row_frag(16 * i + li, ks, g);
+          if (ks + 1 < KS) ask(ks + 1);
+          in_order();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t[j] = mac(lds.y.row_frag(16 * j + sigma(li), ks, g), xf, t[j]);
+          for (int j = 0; j < 4; ++j) t[j] = mac(yf[ks & 1][j], xf[ks & 1], t[j]);
+          in_order();
         }
+        const float qh = gt.hi[16 * i + key_place(li)], ql = gt.lo[16 * i + key_place(li)];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          // exponents of later keys are put where the exponential is 0: selecting the product would put it behind a branch
+          // log2 of the decays; those of later keys are put where the exponential is 0: selecting the product would put it behind a branch
           const floatx4 kh = *reinterpret_cast<const floatx4*>(gt.hi + 16 * j + 4 * g), kl = *reinterpret_cast<const floatx4*>(gt.lo + 16 * j + 4 * g);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float e = (qh - kh[r]) + (ql - kl[r]);
-            t[j][r] *= exp_fast(16 * j + sigma(4 * g + r) <= 16 * i + li ? e : -1e30f) * (wk.out_scale * wk.in_scale);
+            t[j][r] *= exp2_fast(16 * j + sigma(4 * g + r) <= 16 * i + li ? e : -1e30f) * (wk.out_scale * wk.in_scale);
           }
         }
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           const float8v f = {t[2 * ks][0], t[2 * ks][1], t[2 * ks][2], t[2 * ks][3], t[2 * ks + 1][0], t[2 * ks + 1][1], t[2 * ks + 1][2], t[2 * ks + 1][3]};
-          store_frag(lds.o.p[i][ks], lane, make_op<PL>(f, T{}));
+          store_frag(lds.o.p[i][ks], lane, planes_of<PL>(f, T{}));
         }
       }
     }
+
     if constexpr (DOTS) ask_dots(c);
     floatx4 acc[4][2];
     if constexpr (OUT) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = floatx4{};
+      In xf[2][4];
+      const auto ask = [&](int ks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xf[ks & 1][i] = lds.o.x.row_pair(16 * i + li, ks, g);
+      };
+      ask(0);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
+        if (ks + 1 < KS) ask(ks + 1);
+        in_order();
         typename Frags<T>::template Op<PL> sp[2];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const floatx4 a = S[2 * ks][cc], b = S[2 * ks + 1][cc];
-          sp[cc] = make_op<PL>(float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, T{});
+          sp[cc] = planes_of<PL>(float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, T{});
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mac2(sp, lds.o.x.row_frag(16 * i + li, ks, g), acc[i]);
+        for (int i = 0; i < 4; ++i) mac2(sp, xf[ks & 1][i], acc[i]);
+        in_order();
       }
+    }
+
+    // The next chunk's rows (the last chunk asks for its own again): from here on there are registers for them
+    fetch(c + 1 < n_chunks ? c + 1 : c);
+
+    // the new state, and the rest of the outputs: both take the columns of Z
+    In zf[2];
+    const auto ask_z = [&](int ks) {
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
+    };
+    ask_z(0);
+    const float tot = gt.tot;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) S[m][cc] *= tot;
+    if constexpr (OUT) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float oc = gt.oc[16 * i + key_place(li)];
@@ -401,43 +500,52 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         acc[i][1] *= oc;
       }
       if constexpr (DOTS) row_dots(acc, lds.dots[0][wave]);
-      block_barrier();   // the tiles of X Y^T are there
     }
-
-    // state and the rest of the outputs
-    const float tot = gt.tot;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) S[m][cc] *= tot;
+    // the steps' columns of Y, asked for two products ahead
+    In yf[3];
+    const auto ask_y = [&](int n) {
+      if (n < 2 * MT) yf[n % 3] = lds.y.template columns<1>(16 * (n % MT), n / MT, lane);
+    };
+    ask_y(0);
+    ask_y(1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      In zf[2];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
-      if constexpr (OUT) {
-#pragma unroll
-        for (int i = 2 * ks; i < 4; ++i) mac2(zf, load_frag<typename Frags<T>::template Op<PL>>(lds.o.p[i][ks], lane), acc[i]);
-      }
-      typename Frags<T>::template Op<UP> zu[2];
       const floatx4 u0 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 4 * g), u1 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 16 + 4 * g);
       const float8v u = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+      typename Frags<T>::template Op<UP> zu[2];
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        float8v f;
-        if constexpr (sizeof(T) == 2) f = __builtin_convertvector(__builtin_bit_cast(bf16x8v, zf[cc]), float8v);
-        else f = zf[cc];
-        zu[cc] = make_op<UP>(f * u, T{});
+        float8v f = widen(zf[cc], T{});
+#pragma unroll
+        for (int r = 0; r < 8; ++r) f[r] *= u[r];
+        zu[cc] = planes_of<UP>(f, T{});
       }
+      if (OUT || ks == 0) ask_z(1 - ks);
+      in_order();
 #pragma unroll
-      for (int m = 0; m < MT; ++m) mac2(lds.y.template columns<1>(16 * m, ks, lane), zu, S[m]);
+      for (int m = 0; m < MT; ++m) {
+        ask_y(ks * MT + m + 2);
+        in_order();
+        mac2(yf[(ks * MT + m) % 3], zu, S[m]);
+        in_order();
+      }
     }
-
     if constexpr (OUT) {
+      block_barrier();   // the tiles of X Y^T are there
+      typename Frags<T>::template Op<PL> pf[2];
+      const auto ask = [&](int n) {   // tiles (0..3, 0), (2..3, 1)
+        const int i = n < 4 ? n : n - 2, ks = n < 4 ? 0 : 1;
+        if (n < 6) pf[n & 1] = load_frag<typename Frags<T>::template Op<PL>>(lds.o.p[i][ks], lane);
+      };
+      ask(0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) settle(acc[i][cc]);
+      for (int n = 0; n < 6; ++n) {
+        ask(n + 1);
+        in_order();
+        mac2(zf, pf[n & 1], acc[n < 4 ? n : n - 2]);
+        if (n == 3) ask_z(1);
+        in_order();
+      }
       if constexpr (DOTS) row_dots(acc, lds.dots[1][wave]);
       const int64_t out_row = sg.row * wk.so.b + h * wk.so.h + chunk_at(c) * wk.so.t;
       const bool wide = MODE == kParts && wk.out_f32;
@@ -447,7 +555,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       for (int i = 0; i < 4; ++i) {
         const int row = 16 * i + li;
         const uint32_t at = row < have ? (uint32_t)(reverse ? have - 1 - row : row) * ostep + (32 * wave + 8 * g) * esz : kNowhere;
-        if constexpr (sizeof(T) == 2) buffer_put16(ob, wide ? kNowhere : at, pack2(acc[i][0], acc[i][1]));
+        if constexpr (sizeof(T) == 2) buffer_put16(ob, wide ? kNowhere : at, round8(acc[i][0], acc[i][1]));
         if constexpr (sizeof(T) == 4 || MODE == kParts) {
           buffer_put16(ob, sizeof(T) == 4 || wide ? at : kNowhere, acc[i][0]);
           buffer_put16(ob, sizeof(T) == 4 || wide ? at : kNowhere, acc[i][1], 16);
@@ -455,7 +563,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       }
     }
     block_barrier();   // nobody reads this chunk's rows any more
-    if constexpr (OUT) rx.leave(lds.o.x, tid);
+    if constexpr (OUT) rx.template leave<true>(lds.o.x, tid);
     ry.leave(lds.y, tid);
     rz.leave(lds.z, tid);
     if constexpr (DOTS) {
@@ -479,7 +587,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     if (tid == 0) {
 #pragma unroll
       for (int w = 1; w < NW; ++w) total += lds.total[w];
-      wk.decay[slot * p.Hv + h] = exp_fast((float)total);
+      wk.decay[slot * p.Hv + h] = exp2_fast((float)total);
     }
   }
   if (wk.leaving && (wk.leave_slot || end)) {
