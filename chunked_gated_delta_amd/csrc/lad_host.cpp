@@ -188,10 +188,10 @@ int kda_lad_chunk_fwd(const void* q, const void* k, const void* v, const void* w
     k0.leaving = floats(ws.s);
     k0.leave_slot = 1;
     k0.decay = floats(ws.s_decay);
-    k0.skip_end = 1;
+    k0.skip_end = !S_final;
     if ((rc = done(launch_lad_states(p, desc->dtype, (int)dk, (int)dv, s))) != KDA_OK) return rc;
     LadScan sc{};
-    sc.s = floats(ws.s); sc.s_decay = floats(ws.s_decay); sc.S0 = S0; sc.seq_start = seq_start;
+    sc.s = floats(ws.s); sc.s_decay = floats(ws.s_decay); sc.S0 = S0; sc.S_final = S_final; sc.seq_start = seq_start;
     sc.T = T; sc.L = pl.L; sc.n_seq = pl.n_seq; sc.Hv = (int)Hv; sc.size = (int)(dk * dv); sc.dirs = 1;
     if ((rc = done(launch_lad_scan(sc, s))) != KDA_OK) return rc;
   }
@@ -201,7 +201,7 @@ int kda_lad_chunk_fwd(const void* q, const void* k, const void* v, const void* w
   k0.out_scale = desc->scale;
   k0.entering = need > 0 ? floats(ws.s) : S0;
   k0.by_slot = need > 0;
-  k0.leaving = S_final;
+  k0.leaving = need > 0 ? nullptr : S_final;
   return done(launch_lad_fwd(p, desc->dtype, (int)dk, (int)dv, s));
 }
 

@@ -32,6 +32,12 @@ __device__ __forceinline__ int zcol(int c, int m) { return 8 * (m >> 2) + 4 * c 
 __device__ __forceinline__ floatx4 mac(bf16x8 a, bf16x8 b, floatx4 c) { return mfma(a, b, c); }
 __device__ __forceinline__ floatx4 mac(const float8v& a, const float8v& b, floatx4 c) { return mma(a, b, c); }
 
+// A value that the compiler may not carry over from before: addresses made from it are formed where they are used and do not
+// keep registers through the loop.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 // The compiler's schedule puts an LDS read right in front of its use, whose latency a wavefront then waits for (45 times a
 // chunk): reads are asked for a step ahead, and nothing crosses this.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
@@ -170,6 +176,7 @@ struct Gates {
   float hi[kC], lo[kC];     // the prefix as a sum of two floats: differences stay exact beside a reset
   float oc[kC], uc[kC];     // e^{P} out_scale,  e^{Ptot - P} in_scale
   float tot;                // e^{Ptot}
+  double tot2;              // Ptot, in units of ln 2
 };
 
 template <typename T, int DX, int DZ, int PL, int MODE> struct Lds {
@@ -178,7 +185,6 @@ template <typename T, int DX, int DZ, int PL, int MODE> struct Lds {
   Tile<T, DX> y;
   Tile<T, DZ> z;
   Gates gates[2][kWaves];
-  double total[kWaves];
   struct Outs {
     Tile<T, DX> x;
     char p[4][2][op_frag<T, PL>()];
@@ -220,20 +226,21 @@ template <typename T, int D, int THREADS> struct Rows8 {
   In v[kLoads];
   // chunk row `row` is memory row `row`, or have - 1 - row backwards; rows `have` and more are zeros
   __device__ __forceinline__ void load(Buffer b, uint32_t stride, int have, int reverse, int tid) {
-    const int r = tid / kPieces, c = tid % kPieces * 8 * (int)sizeof(T);
+    const int id = fresh(tid), r = id / kPieces, c = id % kPieces * 8 * (int)sizeof(T), rs = reverse ? -1 : 1;
     if (have == kC) {   // whole: one address a lane, the rest is the wavefront's
-      const uint32_t at = (uint32_t)(reverse ? kStep - 1 - r : r) * stride + c;
+      const uint32_t at = (uint32_t)((reverse ? kStep - 1 : 0) + rs * r) * stride + c;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) v[i] = buffer_row8(b, at, (uint32_t)(reverse ? kC - (i + 1) * kStep : i * kStep) * stride, T{});
     } else {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int row = i * kStep + r;
-        v[i] = buffer_row8(b, row < have ? (uint32_t)(reverse ? have - 1 - row : row) * stride + c : kNowhere, 0u, T{});
+        v[i] = buffer_row8(b, row < have ? (uint32_t)((reverse ? have - 1 : 0) + rs * row) * stride + c : kNowhere, 0u, T{});
       }
     }
   }
-  template <bool PAIRED = false> __device__ __forceinline__ void leave(Tile<T, D>& t, int tid) {
+  template <bool PAIRED = false> __device__ __forceinline__ void leave(Tile<T, D>& t, int id) {
+    const int tid = fresh(id);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if constexpr (PAIRED) t.put8_paired(i * kStep + tid / kPieces, tid % kPieces * 8, v[i]);
@@ -244,9 +251,8 @@ template <typename T, int D, int THREADS> struct Rows8 {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end), prefixes in units of ln 2;
-// returns their sum.
-__device__ __forceinline__ double put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale) {
+// One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end), prefixes in units of ln 2.
+__device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale) {
   const double own = (double)g * 1.4426950408889634074;
   double p = own;
 #pragma unroll
@@ -263,7 +269,7 @@ __device__ __forceinline__ double put_gates(Gates& out, float g, int lane, int r
   out.oc[place] = exp2_fast(hi) * out_scale;
   out.uc[place] = exp2_fast((float)(tot - p)) * in_scale;
   out.tot = exp2_fast((float)tot);
-  return tot;
+  out.tot2 = tot;
 }
 
 }  // namespace lad
@@ -298,10 +304,12 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   if (wk.skip_end && end) return;
 
   // chunk c of the walk: its first token in memory, and its tokens.  Backwards the chunks are the same ones.
+  // Without outputs the chunks are taken from the end: the state is a sum in which each has the decay behind it.
   const int64_t n_chunks = (len + kC - 1) / kC;
-  const auto chunk_at = [&](int64_t c) { return sg.t0 + first + kC * (reverse ? n_chunks - 1 - c : c); };
+  const bool down = (reverse != 0) == OUT;
+  const auto chunk_at = [&](int64_t c) { return sg.t0 + first + kC * (down ? n_chunks - 1 - c : c); };
   const auto chunk_have = [&](int64_t c) {
-    const int64_t left = len - kC * (reverse ? n_chunks - 1 - c : c);
+    const int64_t left = len - kC * (down ? n_chunks - 1 - c : c);
     return (int)(left < kC ? left : kC);
   };
   // the first token of the sequence's part of a tensor; a chunk's rows from there
@@ -327,7 +335,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   const auto gate_ask = [&](int64_t c) {
     const int have = c < n_chunks ? chunk_have(c) : 0;
     const int64_t t = c < n_chunks ? chunk_at(c) : 0;
-    const uint32_t at = (uint32_t)(reverse ? have - 1 - lane : lane) * ((uint32_t)p.sw.t * E);
+    const uint32_t at = (uint32_t)((reverse ? have - 1 : 0) + (reverse ? -1 : 1) * lane) * ((uint32_t)p.sw.t * E);
     return buffer_one(buffer(wb + (p.w_per_head ? 0 : t * p.sw.t)), p.w_per_head || lane >= have ? kNowhere : at, T{});
   };
   const auto gate_of = [&](int64_t c, T asked) {
@@ -338,7 +346,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     return c < n_chunks && lane < chunk_have(c) ? g : 0.f;
   };
 
-  double total = 0.0;
+  double behind = 0.0;   // without outputs: the decay behind the chunk, in units of ln 2
   T asked{};
   if (n_chunks > 0) {
     asked = gate_ask(wave);
@@ -368,13 +376,15 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   // this wavefront's part of out . dot for every token of the chunk
   using Dot = typename Lds<T, DX, DZ, PL, MODE>::Dot;
   In dots[DOTS ? 4 : 1];
+  // row of a chunk in memory = r0 + rs row
+  const int rs = reverse ? -1 : 1;
   const auto ask_dots = [&](int64_t c) {
-    const int have = chunk_have(c);
+    const int have = chunk_have(c), r0 = reverse ? have - 1 : 0, ln = fresh(lane), li = ln & 15, g = ln >> 4;
     const Buffer b = buffer(rows_of(wk.dot, wk.sdot, wk.grp_dot) + chunk_at(c) * wk.sdot.t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 16 * i + li;
-      const uint32_t at = (uint32_t)(reverse ? have - 1 - row : row) * ((uint32_t)wk.sdot.t * E) + (32 * wave + 8 * g) * E;
+      const uint32_t at = (uint32_t)(r0 + rs * row) * ((uint32_t)wk.sdot.t * E) + (32 * wave + 8 * g) * E;
       dots[i] = buffer_row8(b, wk.dot && row < have ? at : kNowhere, 0u, T{});
     }
   };
@@ -392,7 +402,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   };
 
   if (n_chunks > 0) {
-    total += put_gates(lds.gates[0][wave], gate_of(wave, asked), lane, reverse, wk.out_scale, wk.in_scale);
+    put_gates(lds.gates[0][wave], gate_of(wave, asked), lane, reverse, wk.out_scale, wk.in_scale);
     asked = gate_ask(NW + wave);
     if constexpr (OUT) rx.template leave<true>(lds.o.x, tid);
     ry.leave(lds.y, tid);
@@ -405,52 +415,55 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     const Gates& gt = lds.gates[c / NW & 1][c % NW];
     if (c % NW == NW - 1) {   // the gates of the next NW chunks
       const int64_t mine = c + 1 + wave;
-      total += put_gates(lds.gates[(c + 1) / NW & 1][wave], gate_of(mine, asked), lane, reverse, wk.out_scale, wk.in_scale);
+      put_gates(lds.gates[(c + 1) / NW & 1][wave], gate_of(mine, asked), lane, reverse, wk.out_scale, wk.in_scale);
       asked = gate_ask(mine + NW);
     }
     if constexpr (OUT) {
-      // this wavefront's row tiles of the decayed X Y^T, transposed: column li is token 16 i + li
+      // this wavefront's row tiles of the decayed X Y^T, transposed: column li is token 16 i + li.  Two key tiles at a
+      // time, the later two only where a row comes behind them.
 #pragma unroll
       for (int ii = 0; ii < 4 / NW; ++ii) {
-        const int i = wave + ii * NW;
-        floatx4 t[4];
+        const int i = wave + ii * NW, ln = fresh(lane), li = ln & 15, g = ln >> 4;
+        const auto key_tiles = [&](int half) {
+          floatx4 t[2] = {};
+          In xf[2], yf[2][2];
+          const auto ask = [&](int ks) {
+            xf[ks & 1] = lds.o.x.row_pair(16 * i + li, ks, g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t[j] = floatx4{};
-        In xf[2], yf[2][4];
-        const auto ask = [&](int ks) {
-          xf[ks & 1] = lds.o.x.row_pair(16 * i + li, ks, g);
+            for (int j = 0; j < 2; ++j) yf[ks & 1][j] = lds.y.row_frag(32 * half + 16 * j + sigma(li), ks, g);
+          };
+          ask(0);
+          const float qh = gt.hi[16 * i + key_place(li)], ql = gt.lo[16 * i + key_place(li)];
+          floatx4 kh[2], kl[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) yf[ks & 1][j] = lds.y.row_frag(16 * j + sigma(li), ks, g);
-        };
-        ask(0);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          if (ks + 1 < KS) ask(ks + 1);
-          in_order();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) t[j] = mac(yf[ks & 1][j], xf[ks & 1], t[j]);
-          in_order();
-        }
-        const float qh = gt.hi[16 * i + key_place(li)], ql = gt.lo[16 * i + key_place(li)];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // log2 of the decays; those of later keys are put where the exponential is 0: selecting the product would put it behind a branch
-          const floatx4 kh = *reinterpret_cast<const floatx4*>(gt.hi + 16 * j + 4 * g), kl = *reinterpret_cast<const floatx4*>(gt.lo + 16 * j + 4 * g);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float e = (qh - kh[r]) + (ql - kl[r]);
-            t[j][r] *= exp2_fast(16 * j + sigma(4 * g + r) <= 16 * i + li ? e : -1e30f) * (wk.out_scale * wk.in_scale);
+          for (int j = 0; j < 2; ++j) {
+            kh[j] = *reinterpret_cast<const floatx4*>(gt.hi + 32 * half + 16 * j + 4 * g);
+            kl[j] = *reinterpret_cast<const floatx4*>(gt.lo + 32 * half + 16 * j + 4 * g);
           }
-        }
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const float8v f = {t[2 * ks][0], t[2 * ks][1], t[2 * ks][2], t[2 * ks][3], t[2 * ks + 1][0], t[2 * ks + 1][1], t[2 * ks + 1][2], t[2 * ks + 1][3]};
-          store_frag(lds.o.p[i][ks], lane, planes_of<PL>(f, T{}));
-        }
+          for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 1 < KS) ask(ks + 1);
+            in_order();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) t[j] = mac(yf[ks & 1][j], xf[ks & 1], t[j]);
+            in_order();
+          }
+          // log2 of the decays; those of later keys are put where the exponential is 0: selecting the product would put it behind a branch
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float e = (qh - kh[j][r]) + (ql - kl[j][r]);
+              t[j][r] *= exp2_fast(32 * half + 16 * j + sigma(4 * g + r) <= 16 * i + li ? e : -1e30f) * (wk.out_scale * wk.in_scale);
+            }
+          const float8v f = {t[0][0], t[0][1], t[0][2], t[0][3], t[1][0], t[1][1], t[1][2], t[1][3]};
+          store_frag(lds.o.p[i][half], ln, planes_of<PL>(f, T{}));
+        };
+        key_tiles(0);
+        if (i >= 2) key_tiles(1);
       }
     }
 
-    if constexpr (DOTS) ask_dots(c);
     floatx4 acc[4][2];
     if constexpr (OUT) {
 #pragma unroll
@@ -487,19 +500,20 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
     };
     ask_z(0);
-    const float tot = gt.tot;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) S[m][cc] *= tot;
+    const float before = OUT ? 1.f : exp2_fast((float)behind);
+    behind += gt.tot2;
     if constexpr (OUT) {
+      const float tot = gt.tot;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) S[m][cc] *= tot;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float oc = gt.oc[16 * i + key_place(li)];
         acc[i][0] *= oc;
         acc[i][1] *= oc;
       }
-      if constexpr (DOTS) row_dots(acc, lds.dots[0][wave]);
     }
     // the steps' columns of Y, asked for two products ahead
     In yf[3];
@@ -511,7 +525,11 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const floatx4 u0 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 4 * g), u1 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 16 + 4 * g);
-      const float8v u = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+      float8v u = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+      if constexpr (!OUT) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) u[r] *= before;
+      }
       typename Frags<T>::template Op<UP> zu[2];
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
@@ -521,6 +539,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         zu[cc] = planes_of<UP>(f, T{});
       }
       if (OUT || ks == 0) ask_z(1 - ks);
+      if (DOTS && ks == 1) ask_dots(c);
       in_order();
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -531,6 +550,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       }
     }
     if constexpr (OUT) {
+      if constexpr (DOTS) row_dots(acc, lds.dots[0][wave]);
       block_barrier();   // the tiles of X Y^T are there
       typename Frags<T>::template Op<PL> pf[2];
       const auto ask = [&](int n) {   // tiles (0..3, 0), (2..3, 1)
@@ -551,10 +571,11 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       const bool wide = MODE == kParts && wk.out_f32;
       const uint32_t esz = wide ? 4 : E, ostep = (uint32_t)wk.so.t * esz;
       const Buffer ob = buffer(static_cast<char*>(wk.out) + out_row * esz);
+      const int r0 = reverse ? have - 1 : 0, ln = fresh(lane), li = ln & 15, g = ln >> 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = 16 * i + li;
-        const uint32_t at = row < have ? (uint32_t)(reverse ? have - 1 - row : row) * ostep + (32 * wave + 8 * g) * esz : kNowhere;
+        const uint32_t at = row < have ? (uint32_t)(r0 + rs * row) * ostep + (32 * wave + 8 * g) * esz : kNowhere;
         if constexpr (sizeof(T) == 2) buffer_put16(ob, wide ? kNowhere : at, round8(acc[i][0], acc[i][1]));
         if constexpr (sizeof(T) == 4 || MODE == kParts) {
           buffer_put16(ob, sizeof(T) == 4 || wide ? at : kNowhere, acc[i][0]);
@@ -562,6 +583,8 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         }
       }
     }
+    // a state that forgets: what lies further from its end has a factor of 0
+    if (!OUT && exp2_fast((float)behind) == 0.f) break;
     block_barrier();   // nobody reads this chunk's rows any more
     if constexpr (OUT) rx.template leave<true>(lds.o.x, tid);
     ry.leave(lds.y, tid);
@@ -581,15 +604,7 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     block_barrier();
   }
 
-  if (wk.decay) {
-    lds.total[wave] = total;
-    block_barrier();
-    if (tid == 0) {
-#pragma unroll
-      for (int w = 1; w < NW; ++w) total += lds.total[w];
-      wk.decay[slot * p.Hv + h] = exp2_fast((float)total);
-    }
-  }
+  if (!OUT && wk.decay && tid == 0) wk.decay[slot * p.Hv + h] = exp2_fast((float)behind);
   if (wk.leaving && (wk.leave_slot || end)) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
