@@ -42,6 +42,36 @@ __device__ __forceinline__ int fresh(int x) {
 // chunk): reads are asked for a step ahead, and nothing crosses this.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
+// Vector work on x stays behind this, and what made x before it: in its place between the matrix instructions.
+__device__ __forceinline__ void from_here(float& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void from_here(bf16x8& x, int i) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w = __builtin_bit_cast(u32x4, x);
+  uint32_t v = w[i];
+  asm volatile("" : "+v"(v));
+  w[i] = v;
+  x = __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ void from_here(float8v& x, int i) {
+  float a = x[2 * i], b = x[2 * i + 1];
+  asm volatile("" : "+v"(a), "+v"(b));
+  x[2 * i] = a;
+  x[2 * i + 1] = b;
+}
+template <int N> __device__ __forceinline__ void until_here(Planes<N>& x, int i) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) from_here(x.p[n], i);
+}
+__device__ __forceinline__ void until_here(float8v& x, int i) { from_here(x, i); }
+// N matrix instructions with V vector ones behind each, which run while it does.
+template <int N, int V> __device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+  }
+}
+
 // c[i] += a[i] b over planes of one side; the accumulators in turn, so that no product waits for the one before
 template <int N> __device__ __forceinline__ void mac2(const Planes<N> (&a)[2], bf16x8 b, floatx4 (&c)[2]) {
 #pragma unroll
@@ -74,29 +104,39 @@ __device__ __forceinline__ void mac2(const float8v& a, const float8v (&b)[2], fl
     for (int i = 0; i < 2; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[i][e], c[i], 0, 0, 0);
 }
 
-// Values as planes of bf16, two at a time: a wider conversion compiles to one instruction a value.
-template <int N> __device__ __forceinline__ Planes<N> planes_of(const float8v& x, uint16_t) {
+// Values as planes of bf16, two at a time: a wider conversion compiles to one instruction a value.  Pair i of 8 values.
+template <int N> __device__ __forceinline__ void planes_pair(Planes<N>& out, int i, float a, float b) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  u32x4 p[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = x[2 * i], b = x[2 * i + 1];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const uint32_t h = pk_bf16(a, b);
-      p[n][i] = h;
-      if (n + 1 < N) {
-        a -= lo_bf16(h);
-        b -= hi_bf16(h);
-      }
+  for (int n = 0; n < N; ++n) {
+    u32x4 p = __builtin_bit_cast(u32x4, out.p[n]);
+    const uint32_t h = pk_bf16(a, b);
+    p[i] = h;
+    out.p[n] = __builtin_bit_cast(bf16x8, p);
+    if (n + 1 < N) {
+      a -= lo_bf16(h);
+      b -= hi_bf16(h);
     }
   }
+}
+template <int> __device__ __forceinline__ void planes_pair(float8v& out, int i, float a, float b) {
+  out[2 * i] = a;
+  out[2 * i + 1] = b;
+}
+template <int N> __device__ __forceinline__ Planes<N> planes_of(const float8v& x, uint16_t) {
   Planes<N> r;
 #pragma unroll
-  for (int n = 0; n < N; ++n) r.p[n] = __builtin_bit_cast(bf16x8, p[n]);
+  for (int i = 0; i < 4; ++i) planes_pair<N>(r, i, x[2 * i], x[2 * i + 1]);
   return r;
 }
 template <int N> __device__ __forceinline__ float8v planes_of(const float8v& x, float) { return x; }
+// pair i of 8 values of a row
+__device__ __forceinline__ float2v widen2(bf16x8 f, int i) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const uint32_t w = __builtin_bit_cast(u32x4, f)[i];
+  return float2v{lo_bf16(w), hi_bf16(w)};
+}
+__device__ __forceinline__ float2v widen2(const float8v& f, int i) { return float2v{f[2 * i], f[2 * i + 1]}; }
 __device__ __forceinline__ bf16x8 round8(floatx4 a, floatx4 b) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   return __builtin_bit_cast(bf16x8, u32x4{pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(b[0], b[1]), pk_bf16(b[2], b[3])});
@@ -224,20 +264,14 @@ template <typename T, int D, int THREADS> struct Rows8 {
   static_assert(THREADS % kPieces == 0 && kLoads * kStep == kC, "whole rows");
   using In = typename Frags<T>::In;
   In v[kLoads];
-  // chunk row `row` is memory row `row`, or have - 1 - row backwards; rows `have` and more are zeros
-  __device__ __forceinline__ void load(Buffer b, uint32_t stride, int have, int reverse, int tid) {
-    const int id = fresh(tid), r = id / kPieces, c = id % kPieces * 8 * (int)sizeof(T), rs = reverse ? -1 : 1;
-    if (have == kC) {   // whole: one address a lane, the rest is the wavefront's
-      const uint32_t at = (uint32_t)((reverse ? kStep - 1 : 0) + rs * r) * stride + c;
+  // Part `part` of four of a chunk's loads.  Chunk row `row` is memory row `row`, or have - 1 - row backwards; rows
+  // `have` and more are zeros.
+  __device__ __forceinline__ void load(int part, Buffer b, uint32_t stride, int have, int reverse, int tid) {
+    const int id = fresh(tid), r = id / kPieces, rs = reverse ? -1 : 1;
+    const uint32_t at = (uint32_t)((reverse ? have - 1 : 0) + rs * r) * stride + id % kPieces * 8 * (int)sizeof(T);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) v[i] = buffer_row8(b, at, (uint32_t)(reverse ? kC - (i + 1) * kStep : i * kStep) * stride, T{});
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int row = i * kStep + r;
-        v[i] = buffer_row8(b, row < have ? (uint32_t)((reverse ? have - 1 : 0) + rs * row) * stride + c : kNowhere, 0u, T{});
-      }
-    }
+    for (int i = part * kLoads / 4; i < (part + 1) * kLoads / 4; ++i)
+      v[i] = buffer_row8(b, r < have - i * kStep ? at + (uint32_t)(rs * i * kStep) * stride : kNowhere, 0u, T{});
   }
   template <bool PAIRED = false> __device__ __forceinline__ void leave(Tile<T, D>& t, int id) {
     const int tid = fresh(id);
@@ -321,13 +355,11 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
 
   Rows8<T, DX, THREADS> rx, ry;
   Rows8<T, DZ, THREADS> rz;
-  const auto fetch = [&](int64_t c) {
-    const int have = chunk_have(c);
-    const int64_t t = chunk_at(c);
-    if constexpr (OUT) rx.load(buffer(xb + t * xs), (uint32_t)xs * E, have, reverse, tid);
-    ry.load(buffer(yb + t * ys), (uint32_t)ys * E, have, reverse, tid);
-    rz.load(buffer(zb + t * zs), (uint32_t)zs * E, have, reverse, tid);
-  };
+  // Part `part` of four of a tensor's rows of chunk c.  Asked for all at once they would fill the queue of the address
+  // unit, and their wavefronts would wait there (a quarter of a chunk's time).
+  const auto fetch_x = [&](int64_t c, int part) { rx.load(part, buffer(xb + chunk_at(c) * xs), (uint32_t)xs * E, chunk_have(c), reverse, tid); };
+  const auto fetch_y = [&](int64_t c, int part) { ry.load(part, buffer(yb + chunk_at(c) * ys), (uint32_t)ys * E, chunk_have(c), reverse, tid); };
+  const auto fetch_z = [&](int64_t c, int part) { rz.load(part, buffer(zb + chunk_at(c) * zs), (uint32_t)zs * E, chunk_have(c), reverse, tid); };
   // Each wavefront forms the gates of one chunk in NW, all at the same time; their values of w are asked for as many
   // chunks before.
   const float head_w = p.w_per_head && p.w ? global_in<float>(p.w)[h] : 0.f;
@@ -350,7 +382,12 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   T asked{};
   if (n_chunks > 0) {
     asked = gate_ask(wave);
-    fetch(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (OUT) fetch_x(0, i);
+      fetch_y(0, i);
+      fetch_z(0, i);
+    }
   }
 
   floatx4 S[MT][2];
@@ -418,6 +455,8 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
       put_gates(lds.gates[(c + 1) / NW & 1][wave], gate_of(mine, asked), lane, reverse, wk.out_scale, wk.in_scale);
       asked = gate_ask(mine + NW);
     }
+    const int64_t next = c + 1 < n_chunks ? c + 1 : c;   // the last chunk asks for its own rows again
+
     if constexpr (OUT) {
       // this wavefront's row tiles of the decayed X Y^T, transposed: column li is token 16 i + li.  Two key tiles at a
       // time, the later two only where a row comes behind them.
@@ -469,45 +508,54 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = floatx4{};
       In xf[2][4];
+      typename Frags<T>::template Op<PL> sp[2][2];
       const auto ask = [&](int ks) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) xf[ks & 1][i] = lds.o.x.row_pair(16 * i + li, ks, g);
       };
+      const float tot = gt.tot;
+      // planes of the state, pairs 2 u and 2 u + 1 of its 8 in step ks; it is not needed as it was any more
+      const auto planes = [&](int ks, int u) {
+#pragma unroll
+        for (int k = 2 * u; k < 2 * u + 2; ++k) {
+          const int cc = k >> 2, i = k & 3;
+          floatx4& from = S[2 * ks + (i >> 1)][cc];
+          float a = from[2 * (i & 1)], b = from[2 * (i & 1) + 1];
+          from_here(a);
+          from_here(b);
+          planes_pair<PL>(sp[ks & 1][cc], i, a, b);
+          a *= tot;
+          b *= tot;
+          until_here(sp[ks & 1][cc], i);
+          from_here(a);
+          from_here(b);
+          from[2 * (i & 1)] = a;
+          from[2 * (i & 1) + 1] = b;
+        }
+      };
       ask(0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) planes(0, u);
+      in_order();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         if (ks + 1 < KS) ask(ks + 1);
-        in_order();
-        typename Frags<T>::template Op<PL> sp[2];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const floatx4 a = S[2 * ks][cc], b = S[2 * ks + 1][cc];
-          sp[cc] = planes_of<PL>(float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, T{});
+        for (int i = ks * 4 / KS; i < (ks + 1) * 4 / KS; ++i) {
+          fetch_x(next, i);
+          fetch_y(next, i);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mac2(sp, xf[ks & 1][i], acc[i]);
         in_order();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mac2(sp[ks & 1], xf[ks & 1][i], acc[i]);
+          if (ks + 1 < KS) {
+            planes(ks + 1, i);
+            interleave<2 * PL, 4>();
+          }
+          in_order();
+        }
       }
-    }
-
-    // The next chunk's rows (the last chunk asks for its own again): from here on there are registers for them
-    fetch(c + 1 < n_chunks ? c + 1 : c);
-
-    // the new state, and the rest of the outputs: both take the columns of Z
-    In zf[2];
-    const auto ask_z = [&](int ks) {
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
-    };
-    ask_z(0);
-    const float before = OUT ? 1.f : exp2_fast((float)behind);
-    behind += gt.tot2;
-    if constexpr (OUT) {
-      const float tot = gt.tot;
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) S[m][cc] *= tot;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float oc = gt.oc[16 * i + key_place(li)];
@@ -515,40 +563,68 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
         acc[i][1] *= oc;
       }
     }
+
+    // the new state, and the rest of the outputs: both take the columns of Z
+    In zf[2];
+    const auto ask_z = [&](int ks) {
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
+    };
+    const float before = OUT ? 1.f : exp2_fast((float)behind);
+    behind += gt.tot2;
+    typename Frags<T>::template Op<UP> zu[2][2];
+    float8v u;
+    const auto ask_u = [&](int ks) {
+      const floatx4 u0 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 4 * g), u1 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 16 + 4 * g);
+      u = float8v{u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+      if constexpr (!OUT) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) u[r] *= before;
+      }
+    };
+    const auto decayed = [&](int ks, int k) {   // pair k of the 8 of Z's columns
+      from_here(zf[k >> 2], k & 3);
+      const float2v f = widen2(zf[k >> 2], k & 3);
+      planes_pair<UP>(zu[ks][k >> 2], k & 3, f[0] * u[2 * (k & 3)], f[1] * u[2 * (k & 3) + 1]);
+      until_here(zu[ks][k >> 2], k & 3);
+    };
     // the steps' columns of Y, asked for two products ahead
     In yf[3];
     const auto ask_y = [&](int n) {
       if (n < 2 * MT) yf[n % 3] = lds.y.template columns<1>(16 * (n % MT), n / MT, lane);
     };
+    ask_z(0);
+    ask_u(0);
     ask_y(0);
     ask_y(1);
 #pragma unroll
+    for (int k = 0; k < 8; ++k) decayed(0, k);
+    ask_z(1);
+    ask_u(1);
+    in_order();
+#pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const floatx4 u0 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 4 * g), u1 = *reinterpret_cast<const floatx4*>(gt.uc + 32 * ks + 16 + 4 * g);
-      float8v u = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
-      if constexpr (!OUT) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) u[r] *= before;
-      }
-      typename Frags<T>::template Op<UP> zu[2];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        float8v f = widen(zf[cc], T{});
-#pragma unroll
-        for (int r = 0; r < 8; ++r) f[r] *= u[r];
-        zu[cc] = planes_of<UP>(f, T{});
-      }
-      if (OUT || ks == 0) ask_z(1 - ks);
       if (DOTS && ks == 1) ask_dots(c);
-      in_order();
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        ask_y(ks * MT + m + 2);
+        const int n = ks * MT + m;
+        ask_y(n + 2);
         in_order();
-        mac2(yf[(ks * MT + m) % 3], zu, S[m]);
+        mac2(yf[n % 3], zu[ks], S[m]);
+        if (ks == 0) {   // the next step's planes beside this one's products
+#pragma unroll
+          for (int k = m * 8 / MT; k < (m + 1) * 8 / MT; ++k) decayed(1, k);
+          interleave<2 * UP, 4>();
+        }
         in_order();
+        // a quarter of the rows that are still to be asked for, four times over the two steps
+        if (n % (MT / 2) == MT / 2 - 1) {
+          if constexpr (!OUT) fetch_y(next, n / (MT / 2));
+          fetch_z(next, n / (MT / 2));
+        }
       }
     }
+    if constexpr (OUT) ask_z(0);
     if constexpr (OUT) {
       if constexpr (DOTS) row_dots(acc, lds.dots[0][wave]);
       block_barrier();   // the tiles of X Y^T are there
