@@ -38,7 +38,7 @@ Plan plan_of(const kda_lad_t* d, bool packed, bool bwd) {
   Plan p;
   p.n_seq = packed ? d->n_seq : d->B;
   p.grp = (int)(d->Hv / d->Hk);
-  p.L = lad_segment(d->B, d->T, p.n_seq, (int)d->Hv, packed, bwd);
+  p.L = lad_segment(d, bwd);
   p.slots = lad_slots(d->B, d->T, p.n_seq, p.L, packed);
   return p;
 }
@@ -133,11 +133,29 @@ float* floats(char* p) { return reinterpret_cast<float*>(p); }
 
 namespace kda {
 
-int64_t lad_segment(int64_t B, int64_t T, int64_t n_seq, int Hv, bool packed, bool bwd) {
-  const int64_t least = bwd ? 256 : 512;
-  const double want = (double)B * (double)T * Hv / 512.0;   // tokens a workgroup, two of them a compute unit
-  int64_t L = (int64_t)((want + kGdrChunk - 1) / kGdrChunk) * kGdrChunk;
-  return L < least ? least : L;
+// Tokens of a segment.  Up to 3 chunks are not worth three launches.  Otherwise n segments and heads at a time:
+//  - as many as workgroups run at once: two a compute unit, one of fp32 with a side of 128; the gradients' three walks
+//    take a third each, or half where their workgroups are small or long (fp32);
+//  - a chunk of a segment is some a us of a walk and of its state's (less with more segments), a segment's state some b us of
+//    the memory's time: n^2 = a / b times the chunks.  Two sequences of 2048 tokens, 16 heads of 128 x 128, bf16: 350
+//    segments' forward 50 us, 512 56; gradients with 176 101 us, with 256 108, with 512 132.  9 packed prompts, 4099 tokens,
+//    16 heads: 30 segments a head 67 us, 21 81, 41 80;
+//  - the chain over a sequence's segments is serial: c chunks each at least, c^2 = T / 1250.
+int64_t lad_segment(const kda_lad_t* d, bool bwd) {
+  const int64_t T = d->T;
+  if (T <= 3 * kGdrChunk) return 3 * kGdrChunk;
+  const double chunks = (double)d->B * (double)T * (double)d->Hv / kGdrChunk, state = (double)(d->dk * d->dv) / 16384.0;
+  const bool f32 = d->dtype == KDA_DTYPE_F32, wide = d->dk == 128 || d->dv == 128;
+  const double capacity = bwd ? (wide && !f32 ? 170.0 : 256.0) : (wide && f32 ? 256.0 : 512.0);
+  const double fair = std::sqrt((bwd ? 70.0 : d->n_seq > 0 ? 200.0 : 120.0) * chunks / state);
+  const int64_t at_once = (int64_t)((fair < capacity ? fair : capacity) / (double)d->Hv);   // segments of a head
+  int64_t n;
+  if (d->n_seq > 0) n = at_once > d->n_seq ? at_once - d->n_seq / 2 : at_once / 2;   // their last ones are partly filled
+  else n = at_once / d->B;
+  int64_t L = n > 0 ? (T + n - 1) / n : T;
+  const int64_t least = kGdrChunk * (int64_t)(0.5 + std::sqrt((double)T / 1250.0));
+  if (L < least) L = least;
+  return (L + kGdrChunk - 1) / kGdrChunk * kGdrChunk;
 }
 
 int64_t lad_slots(int64_t B, int64_t T, int64_t n_seq, int64_t L, bool packed) {

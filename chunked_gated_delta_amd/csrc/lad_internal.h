@@ -105,7 +105,7 @@ struct QkNormParams {
 };
 
 // segment length, and the number of slots that segments of it need
-int64_t lad_segment(int64_t B, int64_t T, int64_t n_seq, int Hv, bool packed, bool bwd);
+int64_t lad_segment(const kda_lad_t* d, bool bwd);
 int64_t lad_slots(int64_t B, int64_t T, int64_t n_seq, int64_t L, bool packed);
 
 // the walks of p over every segment; states: only their states (no outputs)
