@@ -130,24 +130,26 @@ struct LadSeg {
 
 // A sequence of len tokens has max(1, ceil(len / L)) segments; packed ones keep them at slot floor(start / L) +
 // sequence, which leaves room for every sequence's last one without a prefix sum over the lengths.  Offsets are
-// clamped into [0, T], so that offsets out of order address nothing out of range.
+// clamped into [0, T], so that offsets out of order address nothing out of range.  T, L < 2^31 and slots < 2^24 (checked on
+// the host), so 32 bits divide them: a 64-bit division is 130 instructions in front of everything.
 __device__ __forceinline__ LadSeg lad_seq(const int32_t* seq_start, int64_t T, int64_t L, int64_t s) {
   LadSeg q;
   q.seq = s;
   q.seg = 0;
+  const uint32_t L_ = (uint32_t)L;
   if (!seq_start) {
     q.row = s;
     q.t0 = 0;
     q.len = T;
-    q.n_seg = T > L ? (T + L - 1) / L : 1;
+    q.n_seg = T > L ? ((uint32_t)T + L_ - 1) / L_ : 1;
     q.slot0 = s * q.n_seg;
   } else {
     const int64_t a = clamp_off(seq_start[s], 0, T), e = clamp_off(seq_start[s + 1], a, T);
     q.row = 0;
     q.t0 = a;
     q.len = e - a;
-    q.n_seg = q.len > L ? (q.len + L - 1) / L : 1;
-    q.slot0 = a / L + s;
+    q.n_seg = q.len > L ? ((uint32_t)q.len + L_ - 1) / L_ : 1;
+    q.slot0 = (uint32_t)a / L_ + s;
   }
   return q;
 }
@@ -155,13 +157,14 @@ __device__ __forceinline__ LadSeg lad_seq(const int32_t* seq_start, int64_t T, i
 // the segment at this slot; false where the slot holds none
 __device__ __forceinline__ bool lad_find(const int32_t* seq_start, int64_t T, int64_t L, int64_t n_seq, int64_t slot, LadSeg* out) {
   int64_t lo = 0;
+  const uint32_t L_ = (uint32_t)L;
   if (!seq_start) {
-    lo = slot / (T > L ? (T + L - 1) / L : 1);
+    lo = (uint32_t)slot / (T > L ? ((uint32_t)T + L_ - 1) / L_ : 1u);
   } else {
     int64_t hi = n_seq - 1;   // the last sequence whose first slot is not behind this one
     while (lo < hi) {
       const int64_t mid = (lo + hi + 1) / 2;
-      if (clamp_off(seq_start[mid], 0, T) / L + mid <= slot) lo = mid; else hi = mid - 1;
+      if ((uint32_t)clamp_off(seq_start[mid], 0, T) / L_ + mid <= slot) lo = mid; else hi = mid - 1;
     }
   }
   *out = lad_seq(seq_start, T, L, lo);

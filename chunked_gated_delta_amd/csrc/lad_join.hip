@@ -7,12 +7,13 @@ namespace kda {
 namespace {
 
 // S entering segment i + 1 = e^{decay of i} S entering i + segment i's own state, and its adjoint from the last segment
-// down; in place.  Every thread holds 4 values of a state and asks for 4 segments at a time; bound by HBM.
+// down; in place.  Every thread holds 4 values of a state and asks for 8 segments at a time; bound by HBM, or by
+// the trips to memory of the longest sequence.
 __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
   const int per = (p.size + 1023) / 1024;
-  const int64_t unit = blockIdx.x / per;
-  const int dir = p.first + (int)(unit % p.dirs), h = (int)(unit / p.dirs % p.Hv);
-  const int64_t seq = unit / p.dirs / p.Hv;
+  const uint32_t unit = blockIdx.x / (uint32_t)per, dirs = (uint32_t)p.dirs;
+  const int dir = p.first + (int)(unit % dirs), h = (int)(unit / dirs % (uint32_t)p.Hv);
+  const int64_t seq = unit / dirs / (uint32_t)p.Hv;
   const int64_t at = (blockIdx.x % per) * 1024 + 4 * threadIdx.x;
   if (at >= p.size) return;
   const LadSeg sg = lad_seq(p.seq_start, p.T, p.L, seq);
@@ -27,18 +28,18 @@ __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
   const auto slot = [&](int64_t i) { return (sg.slot0 + (dir ? n - 1 - i : i)) * p.Hv + h; };
   // the last one's own state counts only where something leaves it
   const int64_t own = out ? n : n - 1;
-  for (int64_t i = 0; i < n; i += 4) {
-    floatx4 add[4];
-    float a[4];
+  for (int64_t i = 0; i < n; i += 8) {
+    floatx4 add[8];
+    float a[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int64_t s = slot(i + j < own ? i + j : 0);
       const bool live = i + j < own;
       add[j] = live ? ld4f(base + s * p.size + at) : floatx4{};
       a[j] = live ? decay[s] : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (i + j < n) {
         *repoint<floatx4>(base + slot(i + j) * p.size + at) = x;
         x = a[j] * x + add[j];
@@ -58,8 +59,8 @@ template <typename T>
 __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
   __shared__ double part[4];
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
-  const int64_t slot = blockIdx.x / p.Hv;
-  const int h = (int)(blockIdx.x % p.Hv);
+  const int64_t slot = blockIdx.x / (uint32_t)p.Hv;
+  const int h = (int)(blockIdx.x % (uint32_t)p.Hv);
   LadSeg sg;
   if (!lad_find(p.seq_start, p.T, p.L, p.n_seq, slot, &sg)) {
     if (p.w_per_head && tid == 0) p.partial[slot * p.Hv + h] = 0.0;

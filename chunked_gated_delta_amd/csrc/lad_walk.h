@@ -285,16 +285,27 @@ template <typename T, int D, int THREADS> struct Rows8 {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A value of a lane before (DPP control CTRL, into the rows of ROWS), 0 where there is none
+template <int CTRL, int ROWS> __device__ __forceinline__ double behind_lane(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)lo | ((uint64_t)(uint32_t)hi << 32));
+}
+
 // One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end), prefixes in units of ln 2.
 __device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale) {
   const double own = (double)g * 1.4426950408889634074;
   double p = own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double up = __shfl_up(p, d);
-    p += lane >= d ? up : 0.0;
-  }
-  const double tot = __shfl(p, 63);
+  p += behind_lane<0x111, 0xf>(p);   // 1, 2, 4, 8 lanes before, in rows of 16
+  p += behind_lane<0x112, 0xf>(p);
+  p += behind_lane<0x114, 0xf>(p);
+  p += behind_lane<0x118, 0xf>(p);
+  p += behind_lane<0x142, 0xa>(p);   // the last lane of rows 0 and 2 to rows 1 and 3
+  p += behind_lane<0x143, 0xc>(p);   // lane 31 to rows 2 and 3
+  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+  const double tot = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)bits, 63) |
+                                                    ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), 63) << 32));
   p -= reverse ? own : 0.0;
   const float hi = (float)p, lo = (float)(p - (double)hi);
   const int place = key_place(lane);
@@ -322,13 +333,13 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   auto& lds = *reinterpret_cast<Lds<T, DX, DZ, PL, MODE>*>(raw);
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, li = lane & 15, g = lane >> 4;
 
-  int64_t unit;
-  int part;
-  const int n_kh = p.Hv / p.grp;
-  if (!gdr_block(blockIdx.x, p.slots * n_kh, p.n_walks * p.grp, &unit, &part)) return;
-  const LadWalk& wk = p.walk[part / p.grp];
+  // Workgroups of one (segment, query/key head) read the same rows: they get blocks of one XCD (block b runs on XCD b mod 8)
+  const uint32_t n_kh = (uint32_t)(p.Hv / p.grp), parts = (uint32_t)(p.n_walks * p.grp), round = blockIdx.x >> 3;
+  const uint32_t unit = (blockIdx.x & 7) + 8 * (round / parts), part = round % parts;
+  if (unit >= (uint32_t)p.slots * n_kh) return;
+  const LadWalk& wk = p.walk[part / (uint32_t)p.grp];
   const int64_t slot = unit / n_kh;
-  const int h = (int)(unit % n_kh) * p.grp + part % p.grp;
+  const int h = (int)(unit % n_kh * (uint32_t)p.grp + part % (uint32_t)p.grp);
   LadSeg sg;
   if (!lad_find(p.seq_start, p.T, p.L, p.n_seq, slot, &sg)) return;
   const int reverse = wk.reverse;
@@ -395,19 +406,20 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
     const int64_t at = wk.by_slot ? slot * p.Hv + h : sg.seq * p.Hv + h;
     const auto src = global_in<float>(wk.entering) + at * (DX * DZ);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) S[m][0] = S[m][1] = floatx4{};
+    if (wk.entering && wk.transposed) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int z = 32 * wave + zcol(c, li), x = 16 * m + 4 * g;
-        S[m][c] = floatx4{};
-        if (wk.entering) {
-          if (wk.transposed) S[m][c] = ld4f(src + z * DX + x);
-          else {
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[m][c][r] = src[(x + r) * DZ + z];
-          }
-        }
-      }
+        for (int c = 0; c < 2; ++c) S[m][c] = ld4f(src + (32 * wave + zcol(c, li)) * DX + 16 * m + 4 * g);
+    } else if (wk.entering) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[m][c][r] = src[(16 * m + 4 * g + r) * DZ + 32 * wave + zcol(c, li)];
+    }
   }
 
   // this wavefront's part of out . dot for every token of the chunk
