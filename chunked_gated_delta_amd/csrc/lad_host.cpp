@@ -307,13 +307,8 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     p.walk[0] = a;
     p.walk[1] = b;
     p.walk[2] = c;
-    p.n_walks = dk == dv ? 3 : 2;
+    p.n_walks = 3;
     if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, per_head && grads->dw, s))) != KDA_OK) return rc;
-    if (dk != dv) {
-      p.walk[0] = c;
-      p.n_walks = 1;
-      if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dk, (int)dv, false, s))) != KDA_OK) return rc;
-    }
     if (shared) {
       LadSum sm{};
       sm.seq_start = seq_start; sm.B = B; sm.T = T; sm.n_seq = pl.n_seq; sm.Hk = (int)Hk; sm.grp = pl.grp; sm.D = (int)dk; sm.dtype = desc->dtype;

@@ -110,7 +110,7 @@ int64_t lad_slots(int64_t B, int64_t T, int64_t n_seq, int64_t L, bool packed);
 
 // the walks of p over every segment; states: only their states (no outputs)
 hipError_t launch_lad_fwd(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
-// exact: with fp32's accuracy up to the results' own rounding
+// three walks: dq, dk (over dx, dz) and dv (over dz, dx); exact: with fp32's accuracy up to the results' own rounding
 hipError_t launch_lad_bwd(const LadParams& p, int dtype, int dx, int dz, bool exact, hipStream_t s);
 hipError_t launch_lad_bwd_exact(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);
 hipError_t launch_lad_states(const LadParams& p, int dtype, int dx, int dz, hipStream_t s);

@@ -84,6 +84,7 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
   }
   double dot = 0.0;
   if (S)
+#pragma unroll 8   // eight trips to memory at once
     for (int i = 4 * tid; i < p.size; i += 1024) {
       const floatx4 a = ld4f(global_in<float>(S) + i), b = ld4f(global_in<float>(R) + i);
 #pragma unroll

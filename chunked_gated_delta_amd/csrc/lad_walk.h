@@ -323,20 +323,16 @@ __device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int rev
 // in bf16 are taken from them, three (fp32's accuracy) for states and decays' gradients in fp32.
 // MODE: what a walk leaves behind.  kStates: the segment's state from zero and nothing else; kOuts: outputs of type T;
 // kDots: also their products with rows of another tensor; kParts: the same with outputs that may be in fp32.
-template <typename T, int DX, int DZ, int UP, int PL, int MODE, int OCC>
-__global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
+template <typename T, int DX, int DZ, int UP, int PL, int MODE>
+__device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t unit, uint32_t part) {
   using namespace lad;
   constexpr bool OUT = MODE != kStates, DOTS = MODE >= kDots;
   constexpr int THREADS = 2 * DZ, NW = DZ / 32, MT = DX / 16, KS = DX / 32;
   using In = typename Frags<T>::In;
-  extern __shared__ __attribute__((aligned(16))) char raw[];
   auto& lds = *reinterpret_cast<Lds<T, DX, DZ, PL, MODE>*>(raw);
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, li = lane & 15, g = lane >> 4;
 
-  // Workgroups of one (segment, query/key head) read the same rows: they get blocks of one XCD (block b runs on XCD b mod 8)
-  const uint32_t n_kh = (uint32_t)(p.Hv / p.grp), parts = (uint32_t)(p.n_walks * p.grp), round = blockIdx.x >> 3;
-  const uint32_t unit = (blockIdx.x & 7) + 8 * (round / parts), part = round % parts;
-  if (unit >= (uint32_t)p.slots * n_kh) return;
+  const uint32_t n_kh = (uint32_t)(p.Hv / p.grp);
   const LadWalk& wk = p.walk[part / (uint32_t)p.grp];
   const int64_t slot = unit / n_kh;
   const int h = (int)(unit % n_kh * (uint32_t)p.grp + part % (uint32_t)p.grp);
@@ -714,17 +710,52 @@ __global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
   }
 }
 
+// Workgroups of one (segment, query/key head) read the same rows: they get blocks of one XCD (block b runs on XCD b mod
+// 8).  False for a block without work.
+__device__ __forceinline__ bool lad_block(const LadParams& p, uint32_t* unit, uint32_t* part) {
+  const uint32_t parts = (uint32_t)(p.n_walks * p.grp), round = blockIdx.x >> 3;
+  *unit = (blockIdx.x & 7) + 8 * (round / parts);
+  *part = round % parts;
+  return *unit < (uint32_t)p.slots * (uint32_t)(p.Hv / p.grp);
+}
+
+template <typename T, int DX, int DZ, int UP, int PL, int MODE, int OCC>
+__global__ __launch_bounds__(2 * DZ, OCC) void lad_walk_kernel(LadParams p) {
+  extern __shared__ __attribute__((aligned(16))) char raw[];
+  uint32_t unit, part;
+  if (lad_block(p, &unit, &part)) lad_walk<T, DX, DZ, UP, PL, MODE>(p, raw, unit, part);
+}
+
+// The three walks of the gradients where dk and dv differ: the first two have DX = dv, the third DX = dk.  A launch of its own
+// for the third would run behind them (dk = 64, dv = 128 in fp32, 5 sequences of up to 447 tokens: 24 + 17 us).
+template <typename T, int DX, int DZ, int UP, int PL, int MODE, int OCC>
+__global__ __launch_bounds__(2 * (DX > DZ ? DX : DZ), OCC) void lad_walks_kernel(LadParams p) {
+  extern __shared__ __attribute__((aligned(16))) char raw[];
+  uint32_t unit, part;
+  if (!lad_block(p, &unit, &part)) return;
+  if (part < 2 * (uint32_t)p.grp) {
+    if (threadIdx.x < 2 * DZ) lad_walk<T, DX, DZ, UP, PL, MODE>(p, raw, unit, part);
+  } else {
+    if (threadIdx.x < 2 * DX) lad_walk<T, DZ, DX, UP, PL, MODE>(p, raw, unit, part);
+  }
+}
+
 template <typename T, int DX, int DZ, int UP, int PL, int MODE>
 hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
-  constexpr int kLdsBytes = (int)sizeof(lad::Lds<T, DX, DZ, PL, MODE>);
-  // two workgroups a compute unit where registers and LDS allow it
-  constexpr int OCC = sizeof(T) == 2 && DZ == 128 && PL == 2 ? 2 : 1;
-  const auto kernel = lad_walk_kernel<T, DX, DZ, UP, PL, MODE, OCC>;
+  constexpr int kOne = (int)sizeof(lad::Lds<T, DX, DZ, PL, MODE>), kOther = (int)sizeof(lad::Lds<T, DZ, DX, PL, MODE>);
+  constexpr bool kBoth = MODE >= lad::kDots && DX != DZ;
+  constexpr int kLdsBytes = kBoth && kOther > kOne ? kOther : kOne, kSide = kBoth && DX > DZ ? DX : DZ;
+  // Two workgroups a compute unit where registers and LDS allow it; a single wavefront's 32 columns beside 128 need more than
+  // half of a SIMD's registers for the rows under way.
+  constexpr int OCC = sizeof(T) == 2 && kSide == 128 && PL == 2 && !(kBoth && DX + DZ == 160) ? 2 : 1;
+  void (*kernel)(LadParams);
+  if constexpr (kBoth) kernel = lad_walks_kernel<T, DX, DZ, UP, PL, MODE, OCC>;
+  else kernel = lad_walk_kernel<T, DX, DZ, UP, PL, MODE, OCC>;
   static std::atomic<uint64_t> done;
   const hipError_t set = set_dyn_lds(reinterpret_cast<const void*>(kernel), kLdsBytes, done);
   if (set != hipSuccess) return set;
   const int64_t grid = gdr_blocks(p.slots * (p.Hv / p.grp), p.n_walks * p.grp);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(2 * DZ), kLdsBytes, s, p);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(2 * kSide), kLdsBytes, s, p);
   return hipGetLastError();
 }
 
