@@ -20,6 +20,27 @@ _NONE = KdaStride(0, 0, 0)
 _NO_SIZE = ctypes.c_size_t(-1).value
 
 
+def _stream(dev):
+    """The handle of the device's current stream; the Stream object around it costs a microsecond."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _out(given, like, name, dev):
+    """The output and its strides: the one given, checked, or a new one in the input's order of dimensions."""
+    if given is not None:
+        return given, _view(given, name, like.shape, like.dtype, dev)
+    t = _like(like)
+    st = t.stride()
+    return t, KdaStride(st[0], st[1], st[2])
+
+
+def _rows(q, name):
+    st = q.stride()
+    if st[3] != 1 and q.shape[3] > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return KdaStride(st[0], st[1], st[2])
+
+
 def _describe(q, k, v, w, g_min, scale, log_decay, n_seq):
     """Checks the inputs; their descriptor."""
     dev = _gpu(q, "q")
@@ -31,7 +52,7 @@ def _describe(q, k, v, w, g_min, scale, log_decay, n_seq):
     Hv, dv = v.shape[1], v.shape[3]
     dt = q.dtype
     code = _dtype_code(q)
-    sq = _view(q, "q", q.shape, dt, dev)
+    sq = _rows(q, "q")
     sk = _view(k, "k", q.shape, dt, dev)
     sv = _view(v, "v", (B, Hv, T, dv), dt, dev)
     per_head = isinstance(w, torch.Tensor) and w.dim() == 1
@@ -82,18 +103,15 @@ def lad_chunk_fwd(q, k, v, w, S0=None, g_min: float = -5.0, *, scale: float = 1.
     states = (n_seq or desc.B, desc.Hv, desc.dk, desc.dv)
     if S0 is not None:
         _dense(S0, "S0", states, torch.float32, dev)
-    if out is None:
-        out = _like(v)
-    so = _view(out, "out", v.shape, v.dtype, dev)
+    out, so = _out(out, v, "out", dev)
     if S_final is None:
         S_final = torch.empty(states, dtype=torch.float32, device=dev)
     else:
         _dense(S_final, "S_final", states, torch.float32, dev)
     need = _need(desc, False)
     workspace = _workspace(workspace, need, dev)
-    stream = torch.cuda.current_stream(dev.index)
     _call("kda_lad_chunk_fwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(out), ctypes.byref(so),
-                                     _at(S_final), _at(workspace), need, stream.cuda_stream))
+                                     _at(S_final), _at(workspace), need, _stream(dev)))
     return out, S_final
 
 
@@ -120,11 +138,10 @@ def lad_chunk_bwd(q, k, v, w, dO, S0=None, dS_final=None, g_min: float = -5.0, *
     dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
     need = _need(desc, True)
     workspace = _workspace(workspace, need, dev)
-    stream = torch.cuda.current_stream(dev.index)
     at = lambda t: _NONE if t is None or t.dim() == 1 else KdaStride(*t.stride()[:3])  # noqa: E731
     grads = KdaLadGrads(_at(dq), _at(dk), _at(dv), _at(dw), _at(dS0), at(dq), at(dk), at(dv), at(dw))
     _call("kda_lad_chunk_bwd", dev, (_at(q), _at(k), _at(v), _at(w), _at(S0), _at(cu_seqlens), ctypes.byref(desc), _at(dO), ctypes.byref(sdo),
-                                     _at(dS_final), ctypes.byref(grads), _at(workspace), need, stream.cuda_stream))
+                                     _at(dS_final), ctypes.byref(grads), _at(workspace), need, _stream(dev)))
     return dq, dk, dv, dw, dS0
 
 
@@ -145,12 +162,9 @@ def lad_decode(q, k, v, w, S, slots=None, g_min: float = -5.0, *, scale: float =
         _dense(slots, "slots", (desc.B,), torch.int32, dev)
     elif S.shape[0] < desc.B:
         raise ValueError(f"S has {S.shape[0]} states for {desc.B} rows")
-    if out is None:
-        out = _like(v)
-    so = _view(out, "out", v.shape, v.dtype, dev)
-    stream = torch.cuda.current_stream(dev.index)
+    out, so = _out(out, v, "out", dev)
     _call("kda_lad_decode", dev, (_at(q), _at(k), _at(v), _at(w), _at(S), S.shape[0], _at(slots), ctypes.byref(desc), _at(out), ctypes.byref(so),
-                                  stream.cuda_stream))
+                                  _stream(dev)))
     return out
 
 
@@ -163,7 +177,7 @@ def _qk_describe(q, k, q_weight, k_weight, positions, inv_freq, norm, interleave
         raise ValueError("q must be [B,Hq,T,D]")
     B, Hq, T, D = q.shape
     code = _dtype_code(q)
-    sq, sk, Hk = _view(q, "q", q.shape, q.dtype, dev), _NONE, 0
+    sq, sk, Hk = _rows(q, "q"), _NONE, 0
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be a [B,Hk,T,D] tensor")
@@ -222,18 +236,10 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
                        k_scale=k_scale, eps=eps, q_out=q_out, k_out=k_out)
         return _on_stream(stream, call, q, k, q_weight, k_weight, positions, inv_freq)
     desc, dev = _qk_describe(q, k, q_weight, k_weight, positions, inv_freq, norm, interleaved, q_scale, k_scale, eps)
-    if q_out is None:
-        q_out = _like(q)
-    sq, sk = _view(q_out, "q_out", q.shape, q.dtype, dev), _NONE
-    if k is None:
-        k_out = None
-    else:
-        if k_out is None:
-            k_out = _like(k)
-        sk = _view(k_out, "k_out", k.shape, k.dtype, dev)
-    stream = torch.cuda.current_stream(dev.index)
+    q_out, sq = _out(q_out, q, "q_out", dev)
+    k_out, sk = _out(k_out, k, "k_out", dev) if k is not None else (None, _NONE)
     _call("kda_qk_norm_fwd", dev, (_at(q), _at(k), _at(q_weight), _at(k_weight), _at(positions), _at(inv_freq), ctypes.byref(desc), _at(q_out),
-                                   ctypes.byref(sq), _at(k_out), ctypes.byref(sk), stream.cuda_stream))
+                                   ctypes.byref(sq), _at(k_out), ctypes.byref(sk), _stream(dev)))
     return q_out, k_out
 
 
@@ -258,9 +264,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positio
     need = _lib.load().kda_qk_norm_bwd_workspace_bytes(ctypes.byref(desc)) if dqw is not None or dkw is not None else 0
     need = 0 if need == _NO_SIZE else need
     workspace = _workspace(workspace, need, dev)
-    stream = torch.cuda.current_stream(dev.index)
     at = lambda t: _NONE if t is None else KdaStride(*t.stride()[:3])  # noqa: E731
     grads = KdaQkNormGrads(_at(dq), _at(dk), _at(dqw), _at(dkw), at(dq), at(dk))
     _call("kda_qk_norm_bwd", dev, (_at(q), _at(k), _at(q_weight), _at(k_weight), _at(positions), _at(inv_freq), ctypes.byref(desc), _at(dq_out),
-                                   ctypes.byref(sdq), _at(dk_out), ctypes.byref(sdk), ctypes.byref(grads), _at(workspace), need, stream.cuda_stream))
+                                   ctypes.byref(sdq), _at(dk_out), ctypes.byref(sdk), ctypes.byref(grads), _at(workspace), need, _stream(dev)))
     return dq, dk, dqw, dkw
