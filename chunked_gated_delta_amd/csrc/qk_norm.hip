@@ -17,36 +17,65 @@ namespace {
 
 constexpr int kMaxBlocks = 512;   // workgroups a tensor of the gradient: rows of partial sums
 
-template <int NT, bool NEAR, bool VEC> struct Pairs {
+// How a lane's 8 pairs lie in a row.  kWhole: consecutive, moved in 16-byte pieces at whatever place they lie (this
+// hardware's vector accesses need no more than the type's alignment); the pairs that turn and those that do not (one kind
+// where they are neighbours) come in whole groups of 8.  kOver: the same, the last group of a kind reaching back over pairs
+// of the one before, which both write alike and only the first counts; each kind has none or at least 8.  kSingle: pairs NT
+// apart, one value at a time.
+enum { kSingle, kWhole, kOver };
+template <int NT, bool NEAR, int FORM> struct Pairs {
   int t, D, R;
-  __device__ __forceinline__ int pair(int j) const { return VEC ? 8 * t + j : j * NT + t; }
-  __device__ __forceinline__ bool has(int j) const { return pair(VEC ? 0 : j) < D / 2; }
+  int a0, b0, twice, turn;   // first values of the run (a, b), pairs of it that count elsewhere, its first frequency
+  bool live;                 // the lane has pairs
+  __device__ __forceinline__ Pairs(int t_, int D_, int R_) : t(t_), D(D_), R(R_), a0(0), b0(0), twice(0), turn(0), live(true) {
+    if constexpr (FORM != kSingle) {
+      const int turning = NEAR ? D / 2 : R / 2, groups = (turning + 7) / 8;
+      const bool turns = t < groups;
+      const int kind = turns ? turning : D / 2 - turning, first = 8 * (turns ? t : t - groups);
+      live = first < kind;
+      const int s = !live ? 0 : FORM == kWhole || first + 8 <= kind ? first : kind - 8;
+      twice = live ? first - s : 0;
+      turn = turns || !live ? s : R / 2;
+      a0 = NEAR ? 2 * s : turns || !live ? s : R + s;
+      b0 = NEAR ? 2 * s + 1 : turns || !live ? s + R / 2 : R + s + kind;
+      if (!live && R == 0 && !NEAR) b0 = D / 2;
+    }
+  }
+  __device__ __forceinline__ bool has(int j) const { return FORM == kSingle ? j * NT + t < D / 2 : live; }
+  __device__ __forceinline__ bool counts(int j) const { return FORM == kSingle ? j * NT + t < D / 2 : FORM == kWhole ? live : live && j >= twice; }
+  __device__ __forceinline__ int frequency(int j) const { return FORM == kSingle ? j * NT + t : turn + j; }   // R / 2 and more: none
   // places of the pair's two values
   __device__ __forceinline__ int a(int j) const {
-    const int p = pair(j);
+    if constexpr (FORM != kSingle) return a0 + (NEAR ? 2 * j : j);
+    const int p = j * NT + t;
     return NEAR ? 2 * p : p < R / 2 ? p : R / 2 + p;
   }
   __device__ __forceinline__ int b(int j) const {
-    const int p = pair(j);
+    if constexpr (FORM != kSingle) return b0 + (NEAR ? 2 * j : j);
+    const int p = j * NT + t;
     return NEAR ? 2 * p + 1 : p < R / 2 ? p + R / 2 : p + D / 2;
   }
 };
 
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ bf16x8 load_any8(GlobalPtr<const uint16_t> p) { return __builtin_bit_cast(bf16x8, *repoint<u32x4_at2>(p)); }
+__device__ __forceinline__ float8v load_any8(GlobalPtr<const float> p) {
+  const floatx4 a = __builtin_bit_cast(floatx4, *repoint<u32x4_at4>(p)), b = __builtin_bit_cast(floatx4, *repoint<u32x4_at4>(p + 4));
+  return float8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
 __device__ __forceinline__ float8v widen(bf16x8 f) { return __builtin_convertvector(__builtin_bit_cast(bf16x8v, f), float8v); }
 __device__ __forceinline__ float8v widen(const float8v& f) { return f; }
 
-template <typename T, int NT, bool NEAR, bool VEC>
-__device__ __forceinline__ void load_pairs(GlobalPtr<const T> row, Pairs<NT, NEAR, VEC> m, float (&a)[8], float (&b)[8]) {
-  if constexpr (VEC) {
-    const int at = m.has(0) ? m.t : 0;   // a lane behind the row reads its first values and drops them
-    const Pairs<NT, NEAR, VEC> in{at, m.D, m.R};
-    const int lo = in.a(0), hi = NEAR ? lo + 8 : in.b(0);
-    const float8v x = widen(load_row8(row + lo)), y = widen(load_row8(row + hi));
+template <typename T, int NT, bool NEAR, int FORM>
+__device__ __forceinline__ void load_pairs(GlobalPtr<const T> row, const Pairs<NT, NEAR, FORM>& m, float (&a)[8], float (&b)[8]) {
+  if constexpr (FORM != kSingle) {   // a lane without pairs reads the row's first values and drops them
+    const float8v x = widen(load_any8(row + m.a0)), y = widen(load_any8(row + (NEAR ? m.a0 + 8 : m.b0)));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       a[j] = NEAR ? (j < 4 ? x[2 * (j & 3)] : y[2 * (j & 3)]) : x[j];
       b[j] = NEAR ? (j < 4 ? x[2 * (j & 3) + 1] : y[2 * (j & 3) + 1]) : y[j];
-      if (!m.has(0)) a[j] = b[j] = 0.f;
+      if (!m.live) a[j] = b[j] = 0.f;
     }
   } else {
 #pragma unroll
@@ -61,24 +90,24 @@ __device__ __forceinline__ void load_pairs(GlobalPtr<const T> row, Pairs<NT, NEA
 }
 
 __device__ __forceinline__ void store8(GlobalPtr<uint16_t> p, const float (&x)[8]) {
-  *repoint<bf16x8>(p) = pack2(floatx4{x[0], x[1], x[2], x[3]}, floatx4{x[4], x[5], x[6], x[7]});
+  *repoint<u32x4_at2>(p) = u32x4_at2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])};
 }
 __device__ __forceinline__ void store8(GlobalPtr<float> p, const float (&x)[8]) {
-  store_row4(p, floatx4{x[0], x[1], x[2], x[3]});
-  store_row4(p + 4, floatx4{x[4], x[5], x[6], x[7]});
+  *repoint<u32x4_at4>(p) = __builtin_bit_cast(u32x4_at4, floatx4{x[0], x[1], x[2], x[3]});
+  *repoint<u32x4_at4>(p + 4) = __builtin_bit_cast(u32x4_at4, floatx4{x[4], x[5], x[6], x[7]});
 }
 
-template <typename T, int NT, bool NEAR, bool VEC>
-__device__ __forceinline__ void store_pairs(GlobalPtr<T> row, Pairs<NT, NEAR, VEC> m, const float (&a)[8], const float (&b)[8]) {
-  if constexpr (VEC) {
-    if (!m.has(0)) return;
+template <typename T, int NT, bool NEAR, int FORM>
+__device__ __forceinline__ void store_pairs(GlobalPtr<T> row, const Pairs<NT, NEAR, FORM>& m, const float (&a)[8], const float (&b)[8]) {
+  if constexpr (FORM != kSingle) {
+    if (!m.live) return;
     if constexpr (NEAR) {
       const float x[8] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]}, y[8] = {a[4], b[4], a[5], b[5], a[6], b[6], a[7], b[7]};
-      store8(row + m.a(0), x);
-      store8(row + m.a(0) + 8, y);
+      store8(row + m.a0, x);
+      store8(row + m.a0 + 8, y);
     } else {
-      store8(row + m.a(0), a);
-      store8(row + m.b(0), b);
+      store8(row + m.a0, a);
+      store8(row + m.b0, b);
     }
   } else {
 #pragma unroll
@@ -91,8 +120,8 @@ __device__ __forceinline__ void store_pairs(GlobalPtr<T> row, Pairs<NT, NEAR, VE
 }
 
 // cosines and sines of a token's angles; 1 and 0 for pairs that do not turn
-template <int NT, bool NEAR, bool VEC>
-__device__ __forceinline__ void angles(const QkNormParams& p, int64_t b, int64_t t, Pairs<NT, NEAR, VEC> m, float (&c)[8], float (&s)[8]) {
+template <int NT, bool NEAR, int FORM>
+__device__ __forceinline__ void angles(const QkNormParams& p, int64_t b, int64_t t, const Pairs<NT, NEAR, FORM>& m, float (&c)[8], float (&s)[8]) {
   double pos = 0.0;
   if (p.R > 0) {
     const int64_t at = b * p.pos_b + t * p.pos_t;
@@ -100,7 +129,7 @@ __device__ __forceinline__ void angles(const QkNormParams& p, int64_t b, int64_t
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = m.pair(j);
+    const int i = m.frequency(j);
     c[j] = 1.f;
     s[j] = 0.f;
     if (i < p.R / 2) {
@@ -116,8 +145,8 @@ template <int NT> __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-template <int NT, bool NEAR, bool VEC>
-__device__ __forceinline__ void load_weight(const void* w, int wdtype, Pairs<NT, NEAR, VEC> m, float (&a)[8], float (&b)[8]) {
+template <int NT, bool NEAR, int FORM>
+__device__ __forceinline__ void load_weight(const void* w, int wdtype, const Pairs<NT, NEAR, FORM>& m, float (&a)[8], float (&b)[8]) {
   if (!w) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = b[j] = 1.f;
@@ -130,7 +159,7 @@ template <typename T> __device__ __forceinline__ GlobalPtr<T> row_of(const void*
 }
 
 // One workgroup: 256 / NT tokens and up to `heads` heads of one tensor.  Blocks of the queries come first.
-template <typename T, int NT, bool NEAR, bool VEC>
+template <typename T, int NT, bool NEAR, int FORM>
 __global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkNormParams p, int heads, int parts_q, int parts) {
   constexpr int TOK = 256 / NT;
   const int part = blockIdx.x % parts, which = part >= parts_q;
@@ -138,7 +167,7 @@ __global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkNormParams p, int he
   const uint32_t row = (blockIdx.x / parts) * TOK + threadIdx.x / NT, T_ = (uint32_t)p.T;
   if (row >= (uint32_t)(p.B * p.T)) return;
   const int64_t b = row / T_, t = row - b * T_;
-  const Pairs<NT, NEAR, VEC> m{(int)(threadIdx.x % NT), p.D, p.R};
+  const Pairs<NT, NEAR, FORM> m((int)(threadIdx.x % NT), p.D, p.R);
   float wa[8], wb[8], c[8], s[8];
   load_weight(p.weight[which], p.wdtype, m, wa, wb);
   angles(p, b, t, m, c, s);
@@ -149,7 +178,7 @@ __global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkNormParams p, int he
     if (p.norm) {
       float q = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q += x[j] * x[j] + y[j] * y[j];
+      for (int j = 0; j < 8; ++j) q += m.counts(j) ? x[j] * x[j] + y[j] * y[j] : 0.f;
       r *= rsqrtf(row_sum<NT>(q) / (float)p.D + p.eps);
     }
 #pragma unroll
@@ -162,14 +191,15 @@ __global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkNormParams p, int he
   }
 }
 
-// blocks_q workgroups walk the queries' (tokens, heads) items, the others the keys'
-template <typename T, int NT, bool NEAR, bool VEC>
-__global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkNormParams p, int heads, int blocks_q) {
+// blocks_q workgroups walk the queries' (tokens, heads) items, the others the keys'.  Registers for four wavefronts a SIMD:
+// with two more a lane there were three, and 16384 + 16384 rows' heads took 59 us in place of 49.
+template <typename T, int NT, bool NEAR, int FORM>
+__global__ __launch_bounds__(256, FORM != kSingle ? 4 : 1) void qk_norm_bwd_kernel(QkNormParams p, int heads, int blocks_q) {
   constexpr int TOK = 256 / NT;
   __shared__ float acc[4][NT * 16];
   const int which = (int)blockIdx.x >= blocks_q;
   const int block = which ? blockIdx.x - blocks_q : blockIdx.x, blocks = which ? gridDim.x - blocks_q : blocks_q;
-  const Pairs<NT, NEAR, VEC> m{(int)(threadIdx.x % NT), p.D, p.R};
+  const Pairs<NT, NEAR, FORM> m((int)(threadIdx.x % NT), p.D, p.R);
   const uint32_t rows = (uint32_t)(p.B * p.T), T_ = (uint32_t)p.T;
   const int parts = (p.H[which] + heads - 1) / heads;
   const int64_t items = (int64_t)((rows + TOK - 1) / TOK) * parts;
@@ -192,7 +222,7 @@ __global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkNormParams p, int he
       if (p.norm) {
         float q = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q += x[j] * x[j] + y[j] * y[j];
+        for (int j = 0; j < 8; ++j) q += m.counts(j) ? x[j] * x[j] + y[j] * y[j] : 0.f;
         r = rsqrtf(row_sum<NT>(q) / (float)p.D + p.eps);
       }
       float dot = 0.f;
@@ -207,7 +237,7 @@ __global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkNormParams p, int he
         db[j] += v[j] * y[j];
         u[j] *= wa[j];
         v[j] *= wb[j];
-        dot += u[j] * x[j] + v[j] * y[j];
+        dot += m.counts(j) ? u[j] * x[j] + v[j] * y[j] : 0.f;
       }
       if (p.norm) {
         dot = row_sum<NT>(dot) / (float)p.D;
@@ -242,7 +272,7 @@ __global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkNormParams p, int he
     const auto out = as_global(p.partial) + ((int64_t)which * kMaxBlocks + block) * p.D;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (!m.has(j)) continue;
+      if (!m.counts(j)) continue;
       float a = 0.f, b = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -277,7 +307,7 @@ __global__ __launch_bounds__(1024) void qk_norm_weight_kernel(QkNormParams p, in
   }
 }
 
-template <typename T, int NT, bool NEAR, bool VEC>
+template <typename T, int NT, bool NEAR, int FORM>
 hipError_t launch_one(const QkNormParams& p, hipStream_t s, bool bwd) {
   constexpr int TOK = 256 / NT;
   const int64_t groups = (p.B * p.T + TOK - 1) / TOK;
@@ -288,42 +318,40 @@ hipError_t launch_one(const QkNormParams& p, hipStream_t s, bool bwd) {
   if (!bwd) {
     const int64_t grid = groups * (parts_q + parts_k);
     if (grid > 0)
-      hipLaunchKernelGGL((qk_norm_fwd_kernel<T, NT, NEAR, VEC>), dim3((unsigned)grid), dim3(256), 0, s, p, heads, (int)parts_q, (int)(parts_q + parts_k));
+      hipLaunchKernelGGL((qk_norm_fwd_kernel<T, NT, NEAR, FORM>), dim3((unsigned)grid), dim3(256), 0, s, p, heads, (int)parts_q, (int)(parts_q + parts_k));
     return hipGetLastError();
   }
   const auto blocks = [&](int64_t items) { return (int)(items < kMaxBlocks ? items : kMaxBlocks); };
   const int blocks_q = blocks(groups * parts_q), blocks_k = blocks(groups * parts_k);
   if (blocks_q + blocks_k > 0)
-    hipLaunchKernelGGL((qk_norm_bwd_kernel<T, NT, NEAR, VEC>), dim3(blocks_q + blocks_k), dim3(256), 0, s, p, heads, blocks_q);
+    hipLaunchKernelGGL((qk_norm_bwd_kernel<T, NT, NEAR, FORM>), dim3(blocks_q + blocks_k), dim3(256), 0, s, p, heads, blocks_q);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.dweight[0] && !p.dweight[1])) return e;
   hipLaunchKernelGGL(qk_norm_weight_kernel, dim3((unsigned)((p.D + 15) / 16), 2), dim3(1024), 0, s, p, blocks_q, blocks_k);
   return hipGetLastError();
 }
 
-template <typename T, bool NEAR, bool VEC>
+// lanes along a row
+template <typename T, bool NEAR, int FORM>
 hipError_t launch_d(const QkNormParams& p, hipStream_t s, bool bwd) {
-  if (p.D <= 64) return launch_one<T, 4, NEAR, VEC>(p, s, bwd);
-  if (p.D <= 128) return launch_one<T, 8, NEAR, VEC>(p, s, bwd);
-  if (p.D <= 256) return launch_one<T, 16, NEAR, VEC>(p, s, bwd);
-  return launch_one<T, 64, NEAR, VEC>(p, s, bwd);
+  const int turning = NEAR ? p.D / 2 : p.R / 2, lanes = (turning + 7) / 8 + (p.D / 2 - turning + 7) / 8;
+  if (lanes <= 4) return launch_one<T, 4, NEAR, FORM>(p, s, bwd);
+  if (lanes <= 8) return launch_one<T, 8, NEAR, FORM>(p, s, bwd);
+  if (lanes <= 16) return launch_one<T, 16, NEAR, FORM>(p, s, bwd);
+  if (lanes <= 32) return launch_one<T, 32, NEAR, FORM>(p, s, bwd);
+  return launch_one<T, 64, NEAR, FORM>(p, s, bwd);
 }
 
-bool rows16(const void* ptr, kda_stride_t s, int esz) {
-  if (!ptr) return true;
-  const int64_t per = 16 / esz;
-  return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0 && s.b % per == 0 && s.h % per == 0 && s.t % per == 0;
+template <typename T, bool NEAR> hipError_t launch_form(const QkNormParams& p, hipStream_t s, bool bwd) {
+  const int turning = NEAR ? p.D / 2 : p.R / 2, rest = p.D / 2 - turning;
+  if (turning % 8 == 0 && rest % 8 == 0) return launch_d<T, NEAR, kWhole>(p, s, bwd);
+  // 65 groups do not fit a wavefront
+  const bool over = (turning == 0 || turning >= 8) && (rest == 0 || rest >= 8) && (turning + 7) / 8 + (rest + 7) / 8 <= 64;
+  return over ? launch_d<T, NEAR, kOver>(p, s, bwd) : launch_d<T, NEAR, kSingle>(p, s, bwd);
 }
 
 template <typename T> hipError_t launch_t(const QkNormParams& p, hipStream_t s, bool bwd) {
-  const kda_stride_t none = {0, 0, 0};
-  // whole 16-byte pieces: a lane's 8 pairs are all turned or all not, unless they are neighbours
-  bool vec = p.D % 16 == 0 && (p.interleaved || (p.R % 16 == 0));
-  for (int i = 0; i < 2; ++i)
-    vec = vec && rows16(p.x[i], p.sx[i], sizeof(T)) && rows16(p.y[i], p.sy[i], sizeof(T)) && rows16(p.dy[i], p.sdy[i], sizeof(T)) &&
-          rows16(p.dx[i], p.sdx[i], sizeof(T)) && rows16(p.weight[i], none, 4);
-  if (p.interleaved) return vec ? launch_d<T, true, true>(p, s, bwd) : launch_d<T, true, false>(p, s, bwd);
-  return vec ? launch_d<T, false, true>(p, s, bwd) : launch_d<T, false, false>(p, s, bwd);
+  return p.interleaved ? launch_form<T, true>(p, s, bwd) : launch_form<T, false>(p, s, bwd);
 }
 
 }  // namespace

@@ -15,12 +15,11 @@ int check_desc(const kda_qk_norm_t* d) {
   if (d->D % 2 != 0 || d->R % 2 != 0 || d->R > d->D) return KDA_ERR_SHAPE;
   if (d->D > KDA_QK_NORM_MAX_D) return KDA_ERR_UNSUPPORTED;
   if (d->Hq > 65535 || d->Hk > 65535 || (double)d->B * (double)d->T >= 2147483648.0) return KDA_ERR_SHAPE;
-  // a grid holds fewer than 2^24 workgroups of 256 threads; at most one for 4 tokens and a head
-  if ((double)d->B * (double)d->T * (double)(d->Hq + d->Hk) >= (double)(1 << 25)) {
-    const double tok = 256.0 / (d->D <= 64 ? 4 : d->D <= 128 ? 8 : d->D <= 256 ? 16 : 64);
-    const double heads = (double)(d->Hq > d->Hk ? d->Hq : d->Hk);
-    if ((double)d->B * (double)d->T / tok * (double)(d->Hq + d->Hk) / heads >= (double)(1 << 22)) return KDA_ERR_SHAPE;
-  }
+  // A grid holds fewer than 2^24 workgroups of 256 threads: where there are many, one takes all heads of queries or of keys
+  // of its tokens, 256 / NT of them with NT lanes a row.
+  const int64_t turning = (d->interleaved ? d->D : d->R) / 2, lanes = (turning + 7) / 8 + (d->D / 2 - turning + 7) / 8;
+  const double tokens = lanes <= 4 ? 64 : lanes <= 8 ? 32 : lanes <= 16 ? 16 : lanes <= 32 ? 8 : 4;
+  if ((double)d->B * (double)d->T / tokens >= (double)(1 << 22)) return KDA_ERR_SHAPE;
   if (d->dtype != KDA_DTYPE_F32 && d->dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
   if (d->wdtype != KDA_DTYPE_F32 && d->wdtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
   for (int32_t x : {d->norm, d->interleaved, d->wide_positions})

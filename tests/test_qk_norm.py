@@ -42,6 +42,13 @@ CASES = [  # B, T, Hq, Hk, D, R, norm, weight type ("": none), interleaved, posi
     (2, 21, 3, 3, 32, 32, False, "", False, "each", "fused"),
     (1, 3000, 4, 4, 64, 64, True, F32, False, "row", "token"),
     (1, 77, 3, 0, 128, 128, True, F32, False, "row", "token"),
+    (2, 40, 2, 1, 128, 52, True, BF16, False, "each", "odd"),
+    (1, 33, 3, 1, 96, 24, True, F32, False, "row", "token"),
+    (1, 33, 2, 1, 100, 36, True, F32, True, "row", "odd"),
+    (1, 70, 1, 1, 128, 122, True, F32, False, "row", "head"),
+    (1, 30, 1, 1, 48, 16, True, F32, False, "row", "fused"),
+    (1, 30, 2, 1, 1024, 514, True, F32, False, "row", "token"),
+    (1, 20, 1, 1, 384, 100, True, "", False, "row", "token"),
 ]
 
 
