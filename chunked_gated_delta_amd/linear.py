@@ -236,6 +236,8 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
                        k_scale=k_scale, eps=eps, q_out=q_out, k_out=k_out)
         return _on_stream(stream, call, q, k, q_weight, k_weight, positions, inv_freq)
     desc, dev = _qk_describe(q, k, q_weight, k_weight, positions, inv_freq, norm, interleaved, q_scale, k_scale, eps)
+    if k is None and k_out is not None:
+        raise ValueError("k_out is given without k")
     q_out, sq = _out(q_out, q, "q_out", dev)
     k_out, sk = _out(k_out, k, "k_out", dev) if k is not None else (None, _NONE)
     _call("kda_qk_norm_fwd", dev, (_at(q), _at(k), _at(q_weight), _at(k_weight), _at(positions), _at(inv_freq), ctypes.byref(desc), _at(q_out),
