@@ -258,44 +258,44 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   LadParams p = params(desc, pl, w, seq_start);
   const Tensor rq{q, desc->q, pl.grp}, rk{k, desc->k, pl.grp}, rv{v, desc->v, 1}, rdo{dO, sdo, 1};
+  // Sequences of several segments have their states formed and chained first.  A single segment's walks take the entering
+  // states as they are given and leave S behind the last token and dS0 themselves, in three planes, for two launches less.
   const bool segments = T > pl.L;
   const bool want_end = dS_final && grads->dw;               // <S, R> behind the last token
-  const bool forwards = segments || want_end, backwards = segments || grads->dS0;
-  if (forwards || backwards) {
-    p.n_walks = 0;
-    if (forwards) {
-      LadWalk& a = p.walk[p.n_walks++];
-      a = walk_over({nullptr, {}, 1}, rk, rv);
-      a.leaving = floats(ws.s); a.leave_slot = 1; a.decay = floats(ws.s_decay); a.skip_end = !want_end;
-    }
-    if (backwards) {
-      LadWalk& a = p.walk[p.n_walks++];
-      a = walk_over({nullptr, {}, 1}, rq, rdo);
-      a.leaving = floats(ws.r); a.leave_slot = 1; a.decay = floats(ws.r_decay); a.skip_end = !grads->dS0;
-      a.reverse = 1;
-      a.in_scale = desc->scale;
-    }
+  if (segments) {
+    p.n_walks = 2;
+    LadWalk &f = p.walk[0], &r = p.walk[1];
+    f = walk_over({nullptr, {}, 1}, rk, rv);
+    f.leaving = floats(ws.s); f.leave_slot = 1; f.decay = floats(ws.s_decay); f.skip_end = !want_end;
+    r = walk_over({nullptr, {}, 1}, rq, rdo);
+    r.leaving = floats(ws.r); r.leave_slot = 1; r.decay = floats(ws.r_decay); r.skip_end = !grads->dS0;
+    r.reverse = 1;
+    r.in_scale = desc->scale;
     if ((rc = done(launch_lad_states(p, desc->dtype, (int)dk, (int)dv, s))) != KDA_OK) return rc;
     LadScan sc{};
     sc.s = floats(ws.s); sc.s_decay = floats(ws.s_decay); sc.S0 = S0; sc.S_final = want_end ? floats(ws.s_final) : nullptr;
     sc.r = floats(ws.r); sc.r_decay = floats(ws.r_decay); sc.dSf = dS_final; sc.dS0 = grads->dS0;
-    sc.first = forwards ? 0 : 1; sc.dirs = (int)forwards + (int)backwards;
+    sc.dirs = 2;
     sc.seq_start = seq_start; sc.T = T; sc.L = pl.L; sc.n_seq = pl.n_seq; sc.Hv = (int)Hv; sc.size = (int)(dk * dv);
     if ((rc = done(launch_lad_scan(sc, s))) != KDA_OK) return rc;
   }
-  if (T > 0) {
+  if (T > 0 || grads->dS0) {
     const bool shared = pl.grp > 1;
     const kda_stride_t part{Hv * T * dk, T * dk, dk};
     LadWalk a = walk_over(rdo, rv, rk), b = walk_over(rv, rdo, rq), c = walk_over(rk, rq, rdo);
     a.out = shared ? ws.dq : grads->dq; a.so = shared ? part : grads->sq; a.out_f32 = shared; a.transposed = 1;
     a.out_scale = desc->scale;
-    a.entering = forwards ? floats(ws.s) : S0; a.by_slot = forwards;
+    a.entering = segments ? floats(ws.s) : S0; a.by_slot = segments;
     b.out = shared ? ws.dk : grads->dk; b.so = shared ? part : grads->sk; b.out_f32 = shared; b.transposed = 1;
     c.out = grads->dv; c.so = grads->sv;
     b.reverse = c.reverse = 1;
     b.in_scale = c.in_scale = desc->scale;
-    b.entering = c.entering = backwards ? floats(ws.r) : dS_final;
-    b.by_slot = c.by_slot = backwards;
+    b.entering = c.entering = segments ? floats(ws.r) : dS_final;
+    b.by_slot = c.by_slot = segments;
+    if (!segments) {
+      a.leaving = want_end ? floats(ws.s_final) : nullptr;
+      c.leaving = grads->dS0;
+    }
     const auto set_dots = [&](LadWalk& x, char* at) {
       x.dots[0] = reinterpret_cast<double*>(at);
       x.dots[1] = x.dots[0] + B * Hv * T;
@@ -308,8 +308,8 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     p.walk[1] = b;
     p.walk[2] = c;
     p.n_walks = 3;
-    if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, per_head && grads->dw, s))) != KDA_OK) return rc;
-    if (shared) {
+    if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, (per_head && grads->dw) || a.leaving || c.leaving, s))) != KDA_OK) return rc;
+    if (shared && T > 0) {
       LadSum sm{};
       sm.seq_start = seq_start; sm.B = B; sm.T = T; sm.n_seq = pl.n_seq; sm.Hk = (int)Hk; sm.grp = pl.grp; sm.D = (int)dk; sm.dtype = desc->dtype;
       sm.part[0] = floats(ws.dq); sm.out[0] = grads->dq; sm.so[0] = grads->sq;

@@ -52,7 +52,7 @@ struct LadScan {
   float *S_final, *dS0;                     // per (sequence, head); nullable
   const int32_t* seq_start;
   int64_t T, L, n_seq;
-  int Hv, size, first, dirs;                // size = dk dv; directions first .. first + dirs - 1 (0 forwards, 1 its adjoint)
+  int Hv, size, dirs;                       // size = dk dv; 1: forwards, 2: its adjoint too
 };
 
 // the log-decay's gradient from dots of q.dq and k.dk

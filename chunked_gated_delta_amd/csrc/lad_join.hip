@@ -12,7 +12,7 @@ namespace {
 __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
   const int per = (p.size + 1023) / 1024;
   const uint32_t unit = blockIdx.x / (uint32_t)per, dirs = (uint32_t)p.dirs;
-  const int dir = p.first + (int)(unit % dirs), h = (int)(unit / dirs % (uint32_t)p.Hv);
+  const int dir = (int)(unit % dirs), h = (int)(unit / dirs % (uint32_t)p.Hv);
   const int64_t seq = unit / dirs / (uint32_t)p.Hv;
   const int64_t at = (blockIdx.x % per) * 1024 + 4 * threadIdx.x;
   if (at >= p.size) return;

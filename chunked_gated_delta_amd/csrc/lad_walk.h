@@ -596,6 +596,13 @@ __device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t
       planes_pair<UP>(zu[ks][k >> 2], k & 3, f[0] * u[2 * (k & 3)], f[1] * u[2 * (k & 3) + 1]);
       until_here(zu[ks][k >> 2], k & 3);
     };
+    if constexpr (!OUT) {   // nothing else lies before it: all at once
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        fetch_y(next, i);
+        fetch_z(next, i);
+      }
+    }
     // the steps' columns of Y, asked for two products ahead
     In yf[3];
     const auto ask_y = [&](int n) {
@@ -627,8 +634,7 @@ __device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t
         in_order();
         // a quarter of the rows that are still to be asked for, four times over the two steps
         if (n % (MT / 2) == MT / 2 - 1) {
-          if constexpr (!OUT) fetch_y(next, n / (MT / 2));
-          fetch_z(next, n / (MT / 2));
+          if constexpr (OUT) fetch_z(next, n / (MT / 2));
         }
       }
     }

@@ -129,11 +129,12 @@ def test_backward_packed(case, dtype):
 
 
 @pytest.mark.parametrize("want_dw,want_dS0,dSf", [(False, False, True), (False, True, False), (True, False, True), (True, True, False), (True, False, False)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T", [90, 700])
-def test_backward_in_part(T, want_dw, want_dS0, dSf):
+def test_backward_in_part(T, dtype, want_dw, want_dS0, dSf):
     """What is not wanted is left out, and the rest is what it was."""
-    say(f"[case] lad backward in part {T} {want_dw} {want_dS0} {dSf}")
-    d = make(1, T, 1, 2, 64, 64, F32, seed=5, states=1)
+    say(f"[case] lad backward in part {T} {dtype} {want_dw} {want_dS0} {dSf}")
+    d = make(1, T, 1, 2, 64, 32, dtype, seed=5, states=1)
     if not dSf:
         d["dS_final"] = None
     got = run_bwd(d, want_dw=want_dw, want_dS0=want_dS0)
@@ -142,7 +143,7 @@ def test_backward_in_part(T, want_dw, want_dS0, dSf):
         if (n == "dw" and not want_dw) or (n == "dS0" and not want_dS0):
             assert x is None
         else:
-            check(n, x, ref[n], tol(n, F32))
+            check(n, x, ref[n], tol(n, dtype))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -206,9 +207,9 @@ def test_bf16_results_are_rounded_once(case):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T", [500, 1100])
+@pytest.mark.parametrize("T", [130, 500, 1100])
 def test_states_keep_fp32s_accuracy(T, dtype):
-    """Final states and dS0 of 8 and 18 chunks: sums in fp32 of two parts a chunk, each off by half a step of what has come
+    """Final states and dS0 of 3, 8 and 18 chunks: sums in fp32 of two parts a chunk, each off by half a step of what has come
     together, 2 sqrt(36) half steps = 7.2e-7 at most; two bf16 planes in place of three are off by 2e-6 and more."""
     say(f"[case] lad states {T} {dtype}")
     d = make(1, T, 2, 2, 128, 128, dtype, "log", per_head=True, seed=8, states=1)
@@ -269,6 +270,24 @@ def test_offsets_out_of_order_stay_inside():
         lad_chunk_bwd(*(t[n] for n in NAMES), t["dO"], cu_seqlens=c)
         torch.cuda.synchronize()
         assert (pad[:, :, T:] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_nan_stays_in_its_sequence(dtype):
+    """A NaN and an infinity in the tokens of one sequence leave the others as they are, forwards and in the gradients."""
+    say(f"[case] lad with a NaN {dtype}")
+    lens = [70, 300, 129]
+    d = make(1, sum(lens), 1, 2, 64, 64, dtype, seed=19, states=3)
+    clean = run_fwd(d, lens) + run_bwd(d, lens)
+    for n, i in (("k", 75), ("v", 90), ("q", 200), ("w", 150)):
+        d[n][:, :, i] = float("nan") if n != "v" else float("inf")
+    got = run_fwd(d, lens) + run_bwd(d, lens)
+    for x, y in zip(got, clean):
+        if x.shape[0] == 3:
+            assert torch.equal(x[[0, 2]], y[[0, 2]])
+        else:
+            assert torch.equal(x[:, :, :70], y[:, :, :70]) and torch.equal(x[:, :, 370:], y[:, :, 370:])
+    assert not torch.isfinite(got[0][:, :, 70:370]).all()
 
 
 def test_runs_are_equal():
