@@ -324,9 +324,10 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     g.kdk[i] = reinterpret_cast<const double*>(ws.kdk) + i * B * Hv * T;
   }
   g.s = floats(ws.s); g.r = floats(ws.r);
-  g.S_final = floats(ws.s_final); g.dSf = dS_final; g.w = w; g.sw = desc->w; g.dw = grads->dw; g.sdw = grads->sw;
+  g.S0 = S0; g.S_final = floats(ws.s_final); g.dSf = dS_final; g.dS0 = grads->dS0; g.w = w; g.sw = desc->w; g.dw = grads->dw; g.sdw = grads->sw;
   g.partial = reinterpret_cast<double*>(ws.partial); g.seq_start = seq_start;
   g.T = T; g.L = pl.L; g.n_seq = pl.n_seq; g.slots = pl.slots; g.Hv = (int)Hv; g.size = (int)(dk * dv);
+  g.exact = per_head || desc->dtype == KDA_DTYPE_F32;
   g.w_per_head = per_head; g.gate = desc->gate; g.dtype = desc->dtype; g.g_min = desc->g_min;
   return done(launch_lad_decay_grad(g, s));
 }

@@ -58,15 +58,15 @@ struct LadScan {
 // the log-decay's gradient from dots of q.dq and k.dk
 struct LadDecayGrad {
   const double *qdq[2], *kdk[2];            // [B, Hv, T]: from other chunks, and all
-  const float *s, *r;                       // entering states of the segments (null: one segment a sequence)
-  const float *S_final, *dSf;               // per (sequence, head); dSf nullable
+  const float *s, *r;                       // entering states of the segments, where sequences have several
+  const float *S0, *S_final, *dSf, *dS0;    // per (sequence, head); S0, dSf, dS0 nullable, S_final with dSf
   const void* w;
   kda_stride_t sw, sdw;
   void* dw;
   double* partial;                          // per (slot, head), of w per head
   const int32_t* seq_start;
   int64_t T, L, n_seq, slots;
-  int Hv, size, w_per_head, gate, dtype;
+  int Hv, size, w_per_head, gate, dtype, exact;
   float g_min;
 };
 

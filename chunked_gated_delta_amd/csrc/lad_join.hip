@@ -48,16 +48,19 @@ __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
   if (out) *repoint<floatx4>(as_global(out) + whole) = x;
 }
 
-// The log-decay's gradient is a sum over pairs of tokens, dg_t = sum of c_ij over i >= t > j; with B_c the sum over the
-// pairs on both sides of chunk c's start (= <S, R> there), and the dots d_i = q_i . dq_i = sum of c_ij over j <= i,
-// e_j = k_j . dk_j = sum of c_ij over i >= j, each also without its chunk's own pairs (d', e'):
-//     dg_t = B_{c+1} + sum over t' >= t of the chunk (d - e),   B_c = B_{c+1} + sum over the chunk (d' - e')
-// A chunk's own pairs cancel in its d and e; left out of B they leave no rounding there, which would come from as many
-// tokens as the segment has and be large beside the gradient of a head that soon forgets.  B at the segment's end is the product
-// of states.  All in double; a wavefront takes a chunk, from the last one down.
+// The log-decay's gradient is a sum over pairs of tokens, dg_t = sum of c_ij over i >= t > j.  With the dots d_i = q_i . dq_i
+// = sum of c_ij over j <= i and e_j = k_j . dk_j = sum over i >= j, their parts d', e' across chunks, and A_c the sum over the
+// pairs with j before chunk c and i behind it,
+//     dg_t = A_c + sum over t' >= t of the chunk (d - (e - e')) + sum over t' < t of the chunk e'
+// where a chunk's own pairs cancel as the values that they are.  A_c = B_{c+1} - sum of the chunk's e' = B_c - sum of its
+// d' with B_c, the sum over the pairs on both sides of the chunk's start, = <S, R> there.  B is known at both ends of a segment;
+// the chunks are walked from the end where it is smaller, since its rounding goes with them to where everything may be small
+// (a state that the first tokens forget).  A segment of one chunk has A = e^{decay} <S entering, R from behind>, without any
+// difference.  exact: dw is a result in fp32; otherwise the walk is from the last chunk down.  All in double; a
+// wavefront takes a chunk.
 template <typename T>
 __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
-  __shared__ double part[4];
+  __shared__ double part[2][4];
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   const int64_t slot = blockIdx.x / (uint32_t)p.Hv;
   const int h = (int)(blockIdx.x % (uint32_t)p.Hv);
@@ -67,61 +70,87 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
     return;
   }
   const int64_t first = sg.seg * p.L, len = sg.len - first < p.L ? sg.len - first : p.L;
+  const int64_t n_chunks = (len + kGdrChunk - 1) / kGdrChunk;
   const auto wave_sum = [](double x) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
     return x;
   };
-  // <S, R> where the segment ends
-  const bool last = sg.seg == sg.n_seg - 1;
-  const float *S = nullptr, *R = nullptr;
-  if (!last) {
-    S = p.s + ((slot + 1) * p.Hv + h) * p.size;
-    R = p.r + (slot * p.Hv + h) * p.size;
-  } else if (p.dSf) {
-    S = p.S_final + (sg.seq * p.Hv + h) * p.size;
-    R = p.dSf + (sg.seq * p.Hv + h) * p.size;
-  }
-  double dot = 0.0;
-  if (S)
+  const auto block_sum = [&](double x, double (&at)[4]) {
+    x = wave_sum(x);
+    if (lane == 0) at[wave] = x;
+    __syncthreads();
+    return at[0] + at[1] + at[2] + at[3];
+  };
+  const auto product = [&](const float* a, const float* b) {   // this thread's part
+    double dot = 0.0;
+    if (a && b)
 #pragma unroll 8   // eight trips to memory at once
-    for (int i = 4 * tid; i < p.size; i += 1024) {
-      const floatx4 a = ld4f(global_in<float>(S) + i), b = ld4f(global_in<float>(R) + i);
+      for (int i = 4 * tid; i < p.size; i += 1024) {
+        const floatx4 x = ld4f(global_in<float>(a) + i), y = ld4f(global_in<float>(b) + i);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dot += (double)a[r] * (double)b[r];
+        for (int r = 0; r < 4; ++r) dot += (double)x[r] * (double)y[r];
+      }
+    return dot;
+  };
+  // states at the segment's ends: of the chain, or as the call has them
+  const bool chained = p.T > p.L, opens = sg.seg == 0, closes = sg.seg == sg.n_seg - 1;
+  const auto of_slot = [&](const float* t, int64_t i) { return t + ((slot + i) * p.Hv + h) * p.size; };
+  const auto of_seq = [&](const float* t) { return t ? t + (sg.seq * p.Hv + h) * p.size : nullptr; };
+  const float *S_in = chained ? of_slot(p.s, 0) : of_seq(p.S0), *R_out = chained ? of_slot(p.r, 0) : of_seq(p.dSf);
+  const float* S_out = closes ? (p.dSf ? of_seq(p.S_final) : nullptr) : of_slot(p.s, 1);
+  const float* R_in = opens ? of_seq(p.dS0) : of_slot(p.r, -1);
+  const bool one = p.exact && n_chunks == 1;
+  bool down = true;
+  double B;     // the sum at the end that the walk starts from
+  if (one) {
+    double g = 0.0;
+    if (wave == 0 && lane < len)
+      g = lad_decay<T>(p.w, p.w_per_head, p.sw, sg.row, h, sg.t0 + first + lane, p.gate, p.g_min);
+    const double dot = block_sum(product(S_in, R_out), part[0]), total = block_sum(g, part[1]);
+    B = S_in && R_out ? exp(total) * dot : 0.0;
+  } else {
+    B = block_sum(product(S_out, R_out), part[0]);
+    if (p.exact && (!S_in || R_in)) {   // what enters is there, or nothing enters
+      const double at_start = block_sum(product(S_in, R_in), part[1]);
+      if (fabs(at_start) < fabs(B)) {
+        down = false;
+        B = at_start;
+      }
     }
-  dot = wave_sum(dot);
-  if (lane == 0) part[wave] = dot;
-  __syncthreads();
-  double B = part[0] + part[1] + part[2] + part[3];   // behind the chunks taken so far
+  }
   const int64_t at = (sg.row * p.Hv + h) * p.T + sg.t0 + first;
-  const int64_t n_chunks = (len + kGdrChunk - 1) / kGdrChunk;
   double total = 0.0;
   for (int64_t done = 0; done < n_chunks; done += 4) {
-    const int64_t c = n_chunks - 1 - done - wave, t = kGdrChunk * c + lane;
+    const int64_t c = down ? n_chunks - 1 - done - wave : done + wave, t = kGdrChunk * c + lane;
     const bool live = c >= 0 && t < len;
-    double own = 0.0, across = 0.0;
+    double d_in = 0.0, e_in = 0.0, own = 0.0;
     if (live) {
-      own = p.qdq[1][at + t] - p.kdk[1][at + t];
-      across = p.qdq[0][at + t] - p.kdk[0][at + t];
+      d_in = p.qdq[0][at + t];
+      e_in = p.kdk[0][at + t];
+      own = p.qdq[1][at + t] - (p.kdk[1][at + t] - e_in);
     }
+    double before = e_in;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const double more = __shfl_down(own, d);
+      const double more = __shfl_down(own, d), less = __shfl_up(before, d);
       if (lane + d < 64) own += more;
+      if (lane >= d) before += less;
     }
-    across = wave_sum(across);
+    const double e_sum = __shfl(before, 63), d_sum = wave_sum(d_in);
+    before -= e_in;
     __syncthreads();   // the values of the turn before have been read
-    if (lane == 0) part[wave] = across;
+    if (lane == 0) part[0][wave] = down ? d_sum - e_sum : e_sum - d_sum;
     __syncthreads();
     double mine = B;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      if (w < wave) mine += part[w];
-      B += part[w];
+      if (w < wave) mine += part[0][w];
+      B += part[0][w];
     }
+    if (!one) mine -= down ? e_sum : d_sum;
     if (!live) continue;
-    const double dg = mine + own;
+    const double dg = mine + own + before;
     if (p.w_per_head) total += dg;
     else {
       const int64_t tok = sg.t0 + first + t;
@@ -130,11 +159,9 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
     }
   }
   if (!p.w_per_head) return;
-  total = wave_sum(total);
   __syncthreads();
-  if (lane == 0) part[wave] = total;
-  __syncthreads();
-  if (tid == 0) p.partial[slot * p.Hv + h] = part[0] + part[1] + part[2] + part[3];
+  total = block_sum(total, part[1]);
+  if (tid == 0) p.partial[slot * p.Hv + h] = total;
 }
 
 // dw of a w per head: the segments' sums, in a fixed order

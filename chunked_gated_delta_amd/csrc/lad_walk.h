@@ -284,6 +284,12 @@ template <typename T, int D, int THREADS> struct Rows8 {
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// 2^(hi + lo), lo a rounding's size beside hi: an exponent of -20 as one float would be off by 6e-7 of the power
+__device__ __forceinline__ float exp2_two(float hi, float lo) { return exp2_fast(hi) * (1.f + lo * kLn2); }
+__device__ __forceinline__ float exp2_of(double x) {
+  const float hi = (float)x;
+  return exp2_two(hi, (float)(x - (double)hi));
+}
 
 // A value of a lane before (DPP control CTRL, into the rows of ROWS), 0 where there is none
 template <int CTRL, int ROWS> __device__ __forceinline__ double behind_lane(double x) {
@@ -311,9 +317,9 @@ __device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int rev
   const int place = key_place(lane);
   out.hi[place] = hi;
   out.lo[place] = lo;
-  out.oc[place] = exp2_fast(hi) * out_scale;
-  out.uc[place] = exp2_fast((float)(tot - p)) * in_scale;
-  out.tot = exp2_fast((float)tot);
+  out.oc[place] = exp2_two(hi, lo) * out_scale;
+  out.uc[place] = exp2_of(tot - p) * in_scale;
+  out.tot = exp2_of(tot);
   out.tot2 = tot;
 }
 
@@ -500,8 +506,15 @@ __device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float e = (qh - kh[j][r]) + (ql - kl[j][r]);
-              t[j][r] *= exp2_fast(32 * half + 16 * j + sigma(4 * g + r) <= 16 * i + li ? e : -1e30f) * (wk.out_scale * wk.in_scale);
+              const bool before = 32 * half + 16 * j + sigma(4 * g + r) <= 16 * i + li;
+              float e;
+              if constexpr (sizeof(T) == 4 || PL == 3) {   // |qh| >= |kh| there, so what their difference loses is found exactly
+                const float d = qh - kh[j][r];
+                e = exp2_two(before ? d : -1e30f, ((qh - d) - kh[j][r]) + (ql - kl[j][r]));
+              } else {
+                e = exp2_fast(before ? (qh - kh[j][r]) + (ql - kl[j][r]) : -1e30f);
+              }
+              t[j][r] *= e * (wk.out_scale * wk.in_scale);
             }
           const float8v f = {t[0][0], t[0][1], t[0][2], t[0][3], t[1][0], t[1][1], t[1][2], t[1][3]};
           store_frag(lds.o.p[i][half], ln, planes_of<PL>(f, T{}));
@@ -578,7 +591,7 @@ __device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) zf[cc] = lds.z.template columns<2>(32 * wave + 4 * cc, ks, lane);
     };
-    const float before = OUT ? 1.f : exp2_fast((float)behind);
+    const float before = OUT ? 1.f : exp2_of(behind);
     behind += gt.tot2;
     typename Frags<T>::template Op<UP> zu[2][2];
     float8v u;
@@ -694,7 +707,7 @@ __device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t
     block_barrier();
   }
 
-  if (!OUT && wk.decay && tid == 0) wk.decay[slot * p.Hv + h] = exp2_fast((float)behind);
+  if (!OUT && wk.decay && tid == 0) wk.decay[slot * p.Hv + h] = exp2_of(behind);
   if (wk.leaving && (wk.leave_slot || end)) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
