@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
 // d' with B_c, the sum over the pairs on both sides of the chunk's start, = <S, R> there.  B is known at both ends of a segment;
 // the chunks are walked from the end where it is smaller, since its rounding goes with them to where everything may be small
 // (a state that the first tokens forget).  A segment of one chunk has A = e^{decay} <S entering, R from behind>, without any
-// difference.  exact: dw is a result in fp32; otherwise the walk is from the last chunk down.  All in double; a
+// difference; A is 0 where nothing enters or nothing lies behind.  exact: dw is a result in fp32; otherwise the walk is from the last chunk down.  All in double; a
 // wavefront takes a chunk.
 template <typename T>
 __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
@@ -149,6 +149,7 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
       B += part[0][w];
     }
     if (!one) mine -= down ? e_sum : d_sum;
+    if ((c == 0 && opens && !p.S0) || (c == n_chunks - 1 && closes && !p.dSf)) mine = 0.0;   // nothing enters, or nothing is behind
     if (!live) continue;
     const double dg = mine + own + before;
     if (p.w_per_head) total += dg;
