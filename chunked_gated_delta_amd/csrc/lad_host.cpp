@@ -137,9 +137,10 @@ namespace kda {
 //  - as many as workgroups run at once: two a compute unit, one of fp32 with a side of 128; the gradients' three walks
 //    take a third each, or half where their workgroups are small or long (fp32);
 //  - a chunk of a segment is some a us of a walk and of its state's (less with more segments), a segment's state some b us of
-//    the memory's time: n^2 = a / b times the chunks.  Two sequences of 2048 tokens, 16 heads of 128 x 128, bf16: 350
-//    segments' forward 50 us, 512 56; gradients with 176 101 us, with 256 108, with 512 132.  9 packed prompts, 4099 tokens,
-//    16 heads: 30 segments a head 67 us, 21 81, 41 80;
+//    the memory's time: n^2 = a / b times the chunks.  Two sequences of 2048 tokens, 16 heads of 128 x 128, bf16: 8, 11 (this
+//    rule) and 32 segments a head's forward 53, 56 and 81 us; of 4096 tokens 79, 79 (16) and 102; 64K tokens of one with 32
+//    422, with 16 470; gradients of 2 x 4096 with 5 177 us, with 4 191, with 11 194.  9 packed prompts, 4099 tokens, 16 heads: 30
+//    segments a head 63 us, 21 69, 41 75.  Within 5 % of the best of each sweep;
 //  - the chain over a sequence's segments is serial: c chunks each at least, c^2 = T / 1250.
 int64_t lad_segment(const kda_lad_t* d, bool bwd) {
   const int64_t T = d->T;
