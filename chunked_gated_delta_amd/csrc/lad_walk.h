@@ -514,9 +514,12 @@ __device__ __forceinline__ void lad_walk(const LadParams& p, char* raw, uint32_t
             for (int r = 0; r < 4; ++r) {
               const bool before = 32 * half + 16 * j + sigma(4 * g + r) <= 16 * i + li;
               float e;
-              if constexpr (sizeof(T) == 4 || PL == 3) {   // |qh| >= |kh| there, so what their difference loses is found exactly
-                const float d = qh - kh[j][r];
-                e = exp2_two(before ? d : -1e30f, ((qh - d) - kh[j][r]) + (ql - kl[j][r]));
+              if constexpr (sizeof(T) == 4 || PL == 3) {
+                // |qh| >= |kh| there, so what their difference loses is found exactly.  It is of the prefixes' rounding, which
+                // behind many resets is far more than that of their difference (32 resets: 0.03), so the two are summed first
+                // and what that sum loses is left (without it a reset every second token put outputs off by 2.3e-5).
+                const float d = qh - kh[j][r], l = ((qh - d) - kh[j][r]) + (ql - kl[j][r]), sum = d + l;
+                e = exp2_two(before ? sum : -1e30f, l - (sum - d));
               } else {
                 e = exp2_fast(before ? (qh - kh[j][r]) + (ql - kl[j][r]) : -1e30f);
               }
