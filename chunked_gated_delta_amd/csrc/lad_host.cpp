@@ -72,7 +72,7 @@ Span w_span(const kda_lad_t* d, const void* w) {
 
 // workspace sections
 struct Work {
-  char *s, *r, *s_decay, *r_decay, *s_final;   // the chain over the segments
+  char *s, *r, *s_decay, *r_decay, *s_final, *r_start;   // the chain over the segments, and what leaves it
   char *qdq, *kdk, *partial;                   // of the decay's gradient; qdq and kdk twice [B, Hv, T]
   char *dq, *dk;                               // gradients by value head, where heads share q and k
 };
@@ -93,6 +93,7 @@ size_t layout(Work& w, void* base, const kda_lad_t* d, const Plan& p, bool bwd) 
   take(w.r, per_slot * size);
   take(w.r_decay, per_slot * 4);
   take(w.s_final, (double)p.n_seq * d->Hv * size);
+  take(w.r_start, (double)p.n_seq * d->Hv * size);
   take(w.qdq, rows * 4);   // two of doubles
   take(w.kdk, rows * 4);
   take(w.partial, per_slot * 8);
@@ -142,6 +143,11 @@ namespace kda {
 //    422, with 16 470; gradients of 2 x 4096 with 5 177 us, with 4 191, with 11 194.  9 packed prompts, 4099 tokens, 16 heads: 30
 //    segments a head 63 us, 21 69, 41 75.  Within 5 % of the best of each sweep;
 //  - the chain over a sequence's segments is serial: c chunks each at least, c^2 = T / 1250.
+// The gradients' segments have at most 16 chunks where the chain allows it, also where fewer would fill the machine: the
+// decay's gradient starts from <S, R> at their ends, and carried over more than that it takes rounding from far away
+// (lad_decay_grad_kernel).  16 x 4096 tokens, 16 heads of 128 x 128, bf16, in one segment a row and in four: 928 and 973 us where
+// decays forget, 934 and 1178 where they keep everything; with dS0, which a single segment's walks leave in three planes, 1501
+// and 971.
 int64_t lad_segment(const kda_lad_t* d, bool bwd) {
   const int64_t T = d->T;
   if (T <= 3 * kGdrChunk) return 3 * kGdrChunk;
@@ -154,7 +160,10 @@ int64_t lad_segment(const kda_lad_t* d, bool bwd) {
   if (d->n_seq > 0) n = at_once > d->n_seq ? at_once - d->n_seq / 2 : at_once / 2;   // their last ones are partly filled
   else n = at_once / d->B;
   int64_t L = n > 0 ? (T + n - 1) / n : T;
-  const int64_t least = kGdrChunk * (int64_t)(0.5 + std::sqrt((double)T / 1250.0));
+  int64_t least = kGdrChunk * (int64_t)(0.5 + std::sqrt((double)T / 1250.0));
+  if (bwd && least > kGdrChunk * kLadMaxChunks) least = kGdrChunk * kLadMaxChunks;
+  const int64_t most = kGdrChunk * 16;
+  if (bwd && L > most) L = most;
   if (L < least) L = least;
   return (L + kGdrChunk - 1) / kGdrChunk * kGdrChunk;
 }
@@ -262,20 +271,22 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
   // Sequences of several segments have their states formed and chained first.  A single segment's walks take the entering
   // states as they are given and leave S behind the last token and dS0 themselves, in three planes, for two launches less.
   const bool segments = T > pl.L;
-  const bool want_end = dS_final && grads->dw;               // <S, R> behind the last token
+  // <S, R> behind the last token and in front of the first
+  const bool want_end = dS_final && grads->dw, want_start = S0 && grads->dw;
+  float* const r_start = grads->dS0 ? grads->dS0 : want_start ? floats(ws.r_start) : nullptr;
   if (segments) {
     p.n_walks = 2;
     LadWalk &f = p.walk[0], &r = p.walk[1];
     f = walk_over({nullptr, {}, 1}, rk, rv);
     f.leaving = floats(ws.s); f.leave_slot = 1; f.decay = floats(ws.s_decay); f.skip_end = !want_end;
     r = walk_over({nullptr, {}, 1}, rq, rdo);
-    r.leaving = floats(ws.r); r.leave_slot = 1; r.decay = floats(ws.r_decay); r.skip_end = !grads->dS0;
+    r.leaving = floats(ws.r); r.leave_slot = 1; r.decay = floats(ws.r_decay); r.skip_end = !r_start;
     r.reverse = 1;
     r.in_scale = desc->scale;
     if ((rc = done(launch_lad_states(p, desc->dtype, (int)dk, (int)dv, s))) != KDA_OK) return rc;
     LadScan sc{};
     sc.s = floats(ws.s); sc.s_decay = floats(ws.s_decay); sc.S0 = S0; sc.S_final = want_end ? floats(ws.s_final) : nullptr;
-    sc.r = floats(ws.r); sc.r_decay = floats(ws.r_decay); sc.dSf = dS_final; sc.dS0 = grads->dS0;
+    sc.r = floats(ws.r); sc.r_decay = floats(ws.r_decay); sc.dSf = dS_final; sc.dS0 = r_start;
     sc.dirs = 2;
     sc.seq_start = seq_start; sc.T = T; sc.L = pl.L; sc.n_seq = pl.n_seq; sc.Hv = (int)Hv; sc.size = (int)(dk * dv);
     if ((rc = done(launch_lad_scan(sc, s))) != KDA_OK) return rc;
@@ -295,7 +306,7 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     b.by_slot = c.by_slot = segments;
     if (!segments) {
       a.leaving = want_end ? floats(ws.s_final) : nullptr;
-      c.leaving = grads->dS0;
+      c.leaving = r_start;
     }
     const auto set_dots = [&](LadWalk& x, char* at) {
       x.dots[0] = reinterpret_cast<double*>(at);
@@ -309,7 +320,8 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     p.walk[1] = b;
     p.walk[2] = c;
     p.n_walks = 3;
-    if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, (per_head && grads->dw) || a.leaving || c.leaving, s))) != KDA_OK) return rc;
+    const bool exact = (per_head && grads->dw) || a.leaving || (c.leaving && grads->dS0);
+    if ((rc = done(launch_lad_bwd(p, desc->dtype, (int)dv, (int)dk, exact, s))) != KDA_OK) return rc;
     if (shared && T > 0) {
       LadSum sm{};
       sm.seq_start = seq_start; sm.B = B; sm.T = T; sm.n_seq = pl.n_seq; sm.Hk = (int)Hk; sm.grp = pl.grp; sm.D = (int)dk; sm.dtype = desc->dtype;
@@ -325,10 +337,9 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
     g.kdk[i] = reinterpret_cast<const double*>(ws.kdk) + i * B * Hv * T;
   }
   g.s = floats(ws.s); g.r = floats(ws.r);
-  g.S0 = S0; g.S_final = floats(ws.s_final); g.dSf = dS_final; g.dS0 = grads->dS0; g.w = w; g.sw = desc->w; g.dw = grads->dw; g.sdw = grads->sw;
+  g.S0 = S0; g.S_final = floats(ws.s_final); g.dSf = dS_final; g.dS0 = r_start; g.w = w; g.sw = desc->w; g.dw = grads->dw; g.sdw = grads->sw;
   g.partial = reinterpret_cast<double*>(ws.partial); g.seq_start = seq_start;
   g.T = T; g.L = pl.L; g.n_seq = pl.n_seq; g.slots = pl.slots; g.Hv = (int)Hv; g.size = (int)(dk * dv);
-  g.exact = per_head || desc->dtype == KDA_DTYPE_F32;
   g.w_per_head = per_head; g.gate = desc->gate; g.dtype = desc->dtype; g.g_min = desc->g_min;
   return done(launch_lad_decay_grad(g, s));
 }

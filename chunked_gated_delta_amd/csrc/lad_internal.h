@@ -59,14 +59,14 @@ struct LadScan {
 struct LadDecayGrad {
   const double *qdq[2], *kdk[2];            // [B, Hv, T]: from other chunks, and all
   const float *s, *r;                       // entering states of the segments, where sequences have several
-  const float *S0, *S_final, *dSf, *dS0;    // per (sequence, head); S0, dSf, dS0 nullable, S_final with dSf
+  const float *S0, *S_final, *dSf, *dS0;    // per (sequence, head); S0, dSf nullable; S_final with dSf, dS0 with S0
   const void* w;
   kda_stride_t sw, sdw;
   void* dw;
   double* partial;                          // per (slot, head), of w per head
   const int32_t* seq_start;
   int64_t T, L, n_seq, slots;
-  int Hv, size, w_per_head, gate, dtype, exact;
+  int Hv, size, w_per_head, gate, dtype;
   float g_min;
 };
 
@@ -104,6 +104,8 @@ struct QkNormParams {
   float* partial;
 };
 
+// chunks of a segment at most: what launch_lad_decay_grad keeps of them fits LDS
+constexpr int64_t kLadMaxChunks = 1024;
 // segment length, and the number of slots that segments of it need
 int64_t lad_segment(const kda_lad_t* d, bool bwd);
 int64_t lad_slots(int64_t B, int64_t T, int64_t n_seq, int64_t L, bool packed);
@@ -178,5 +180,36 @@ __device__ __forceinline__ float lad_decay(const void* w, int per_head, kda_stri
   const float x = per_head ? global_in<float>(w)[h] : get(global_in<T>(w) + row * sw.b + h * sw.h + t * sw.t);
   return gdr_gate(x, gate, g_min);
 }
+
+// ---------------------------------------------------------------- sums over a wavefront
+
+// A value of a lane before (DPP control CTRL, into the rows of ROWS), 0 where there is none
+template <int CTRL, int ROWS> __device__ __forceinline__ float behind_lane(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ double behind_lane(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)lo | ((uint64_t)(uint32_t)hi << 32));
+}
+// sum over the lanes up to this one
+template <typename F> __device__ __forceinline__ F lane_prefix(F p) {
+  p += behind_lane<0x111, 0xf>(p);   // 1, 2, 4, 8 lanes before, in rows of 16
+  p += behind_lane<0x112, 0xf>(p);
+  p += behind_lane<0x114, 0xf>(p);
+  p += behind_lane<0x118, 0xf>(p);
+  p += behind_lane<0x142, 0xa>(p);   // the last lane of rows 0 and 2 to rows 1 and 3
+  p += behind_lane<0x143, 0xc>(p);   // lane 31 to rows 2 and 3
+  return p;
+}
+// the last lane's value
+__device__ __forceinline__ float last_lane(float x) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63)); }
+__device__ __forceinline__ double last_lane(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63) |
+                                        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32));
+}
+template <typename F> __device__ __forceinline__ F lane_sum(F x) { return last_lane(lane_prefix(x)); }
 
 }  // namespace kda

@@ -52,16 +52,19 @@ __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
 // = sum of c_ij over j <= i and e_j = k_j . dk_j = sum over i >= j, their parts d', e' across chunks, and A_c the sum over the
 // pairs with j before chunk c and i behind it,
 //     dg_t = A_c + sum over t' >= t of the chunk (d - (e - e')) + sum over t' < t of the chunk e'
-// where a chunk's own pairs cancel as the values that they are.  A_c = B_{c+1} - sum of the chunk's e' = B_c - sum of its
-// d' with B_c, the sum over the pairs on both sides of the chunk's start, = <S, R> there.  B is known at both ends of a segment;
-// the chunks are walked from the end where it is smaller, since its rounding goes with them to where everything may be small
-// (a state that the first tokens forget).  A segment of one chunk has A = e^{decay} <S entering, R from behind>, without any
-// difference; A is 0 where nothing enters or nothing lies behind.  exact: dw is a result in fp32; otherwise the walk is from
-// the last chunk down.  All in double; a wavefront takes a chunk.  Bound by the states' trip from memory (2 x 4096 tokens, 160
-// segments of 128 x 128: 12.7 us).
-template <typename T>
-__global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
-  __shared__ double part[2][4];
+// where a chunk's own pairs cancel as the values that they are.  With B_c, the sum over the pairs on both sides of the
+// chunk's start, A_c = B_c - sum of its d' = B_{c+1} - sum of its e'.  B = <S, R> is known at both ends of a segment (0 where
+// nothing enters or nothing lies behind), so A is carried from either end.  Every sum that goes into it leaves its rounding
+// there, also where the head has forgotten what made it large, so each chunk takes the end whose values on the way were smaller.
+// And A_c has the chunk's whole decay as a factor: where 0 is nearer to it than the rounding of what is carried (a
+// reset, a decay of more than a half a token), it is 0 and both ways start anew.  Between a part that forgets and one that remembers
+// (2048 tokens, decays of 2 and 1/2048 a token, fp32) the first one's gradients were off by 1.7e-3 where A came from the far end.
+// A segment of one chunk has A = e^{decay} <S entering, R from behind>, without any difference.  All in double; a wavefront
+// takes a chunk.  Bound by the states' trip from memory (2 x 4096 tokens, 160 segments of 128 x 128, four states each: 12.9 us).
+template <typename T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void lad_decay_grad_kernel(LadDecayGrad p) {
+  extern __shared__ __attribute__((aligned(16))) char raw[];
+  __shared__ double part[4][WAVES];
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   const int64_t slot = blockIdx.x / (uint32_t)p.Hv;
   const int h = (int)(blockIdx.x % (uint32_t)p.Hv);
@@ -71,88 +74,125 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
     return;
   }
   const int64_t first = sg.seg * p.L, len = sg.len - first < p.L ? sg.len - first : p.L;
-  const int64_t n_chunks = (len + kGdrChunk - 1) / kGdrChunk;
-  const auto wave_sum = [](double x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-    return x;
-  };
-  const auto block_sum = [&](double x, double (&at)[4]) {
-    x = wave_sum(x);
-    if (lane == 0) at[wave] = x;
-    __syncthreads();
-    return at[0] + at[1] + at[2] + at[3];
-  };
-  const auto product = [&](const float* a, const float* b) {   // this thread's part
-    double dot = 0.0;
-    if (a && b)
-#pragma unroll 8   // eight trips to memory at once
-      for (int i = 4 * tid; i < p.size; i += 1024) {
-        const floatx4 x = ld4f(global_in<float>(a) + i), y = ld4f(global_in<float>(b) + i);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dot += (double)x[r] * (double)y[r];
-      }
-    return dot;
-  };
+  const int n_chunks = (int)((len + kGdrChunk - 1) / kGdrChunk), most = (int)(p.L / kGdrChunk);
+  // by chunk: sums of d' and e' and their sizes, e^{decay}; A from the start and from the end, and the size of what it was taken from
+  double* const d_sum = reinterpret_cast<double*>(raw);
+  double *const e_sum = d_sum + most, *const A_up = e_sum + most, *const A_down = A_up + most;
+  float* const d_size = reinterpret_cast<float*>(A_down + most);
+  float *const e_size = d_size + most, *const kept = e_size + most, *const size_up = kept + most, *const size_down = size_up + most;
+  const int64_t at = (sg.row * p.Hv + h) * p.T + sg.t0 + first;
   // states at the segment's ends: of the chain, or as the call has them
   const bool chained = p.T > p.L, opens = sg.seg == 0, closes = sg.seg == sg.n_seg - 1;
   const auto of_slot = [&](const float* t, int64_t i) { return t + ((slot + i) * p.Hv + h) * p.size; };
   const auto of_seq = [&](const float* t) { return t ? t + (sg.seq * p.Hv + h) * p.size : nullptr; };
   const float *S_in = chained ? of_slot(p.s, 0) : of_seq(p.S0), *R_out = chained ? of_slot(p.r, 0) : of_seq(p.dSf);
-  const float* S_out = closes ? (p.dSf ? of_seq(p.S_final) : nullptr) : of_slot(p.s, 1);
-  const float* R_in = opens ? of_seq(p.dS0) : of_slot(p.r, -1);
-  const bool one = p.exact && n_chunks == 1;
-  bool down = true;
-  double B;     // the sum at the end that the walk starts from
-  if (one) {
-    double g = 0.0;
-    if (wave == 0 && lane < len)
-      g = lad_decay<T>(p.w, p.w_per_head, p.sw, sg.row, h, sg.t0 + first + lane, p.gate, p.g_min);
-    const double dot = block_sum(product(S_in, R_out), part[0]), total = block_sum(g, part[1]);
-    B = S_in && R_out ? exp(total) * dot : 0.0;
-  } else {
-    B = block_sum(product(S_out, R_out), part[0]);
-    if (p.exact && (!S_in || R_in)) {   // what enters is there, or nothing enters
-      const double at_start = block_sum(product(S_in, R_in), part[1]);
-      if (fabs(at_start) < fabs(B)) {
-        down = false;
-        B = at_start;
+  const float *S_out = closes ? (p.dSf ? of_seq(p.S_final) : nullptr) : of_slot(p.s, 1);
+  const float *R_in = opens ? (p.S0 ? of_seq(p.dS0) : nullptr) : of_slot(p.r, -1);
+  // their product, and the size of its terms, as sums of the wavefronts' parts
+  const auto product = [&](const float* a, const float* b, double* sum, double* size) {
+    double dot = 0.0, sq = 0.0;
+    if (a && b)
+#pragma unroll 4   // eight trips to memory at once
+      for (int i = 4 * tid; i < p.size; i += 256 * WAVES) {
+        const floatx4 x = ld4f(global_in<float>(a) + i), y = ld4f(global_in<float>(b) + i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const double term = (double)x[r] * (double)y[r];
+          dot += term;
+          sq += term * term;
+        }
+      }
+    dot = lane_sum(dot);
+    sq = lane_sum(sq);
+    if (lane == 0) {
+      sum[wave] = dot;
+      size[wave] = sq;
+    }
+  };
+  const auto all = [](const double* x) {
+    double s = 0.0;
+    for (int w = 0; w < WAVES; ++w) s += x[w];
+    return s;
+  };
+  // a wavefront's first chunk is on its way beside the states
+  double d, e;
+  float g;
+  const auto ask = [&](int c) {
+    const int64_t t = kGdrChunk * (int64_t)c + lane;
+    const bool live = t < len;
+    d = live ? p.qdq[0][at + t] : 0.0;
+    e = live ? p.kdk[0][at + t] : 0.0;
+    g = live ? lad_decay<T>(p.w, p.w_per_head, p.sw, sg.row, h, sg.t0 + first + t, p.gate, p.g_min) : 0.f;
+  };
+  ask(wave);
+  if (n_chunks == 1) product(S_in, R_out, part[0], part[1]);
+  else if (n_chunks > 1) {
+    product(S_in, R_in, part[0], part[1]);
+    product(S_out, R_out, part[2], part[3]);
+  }
+  for (int c = wave; c < n_chunks; c += WAVES) {
+    if (c != wave) ask(c);
+    const double ds = lane_sum(d), es = lane_sum(e), decay = lane_sum((double)g);
+    const float dn = lane_sum((float)fabs(d)), en = lane_sum((float)fabs(e));
+    if (lane == 0) {
+      d_sum[c] = ds;
+      e_sum[c] = es;
+      d_size[c] = 0.125f * dn;   // of 64 values with signs of their own
+      e_size[c] = 0.125f * en;
+      kept[c] = (float)exp(decay);
+      if (n_chunks == 1) A_up[0] = exp(decay);
+    }
+  }
+  __syncthreads();
+  if (n_chunks == 1) {
+    if (tid == 0) {
+      A_up[0] = S_in && R_out ? A_up[0] * all(part[0]) : 0.0;
+      size_up[0] = size_down[0] = 0.f;
+    }
+  } else if (n_chunks > 1) {
+    if (lane == 0 && wave < 2) {
+      const bool down = wave == 1;
+      const float ends[2] = {(float)sqrt(all(part[1])), (float)sqrt(all(part[3]))};
+      float whole = ends[0] + ends[1];
+      for (int c = 0; c < n_chunks; ++c) whole += d_size[c] + e_size[c];
+      // A without its factor, a product of two states, is taken as at most 2^20 times the values' size; their rounding is 2^-22 of it
+      const float far = 0x1p42f * whole;
+      const double *const near_sum = down ? e_sum : d_sum, *const far_sum = down ? d_sum : e_sum;
+      const float *const near_size = down ? e_size : d_size, *const far_size = down ? d_size : e_size;
+      double* const A_out = down ? A_down : A_up;
+      float* const size_out = down ? size_down : size_up;
+      double B = all(down ? part[2] : part[0]);
+      float size = ends[down];
+      for (int i = 0; i < n_chunks; ++i) {
+        const int c = down ? n_chunks - 1 - i : i;
+        double A = B - near_sum[c];
+        size += near_size[c];
+        const float to_zero = kept[c] == 0.f ? 0.f : kept[c] * far;
+        if (to_zero < size) {
+          A = 0.0;
+          size = to_zero;
+        }
+        A_out[c] = A;
+        size_out[c] = size;
+        B = A + far_sum[c];
+        size += far_size[c];
       }
     }
   }
-  const int64_t at = (sg.row * p.Hv + h) * p.T + sg.t0 + first;
+  __syncthreads();
   double total = 0.0;
-  for (int64_t done = 0; done < n_chunks; done += 4) {
-    const int64_t c = down ? n_chunks - 1 - done - wave : done + wave, t = kGdrChunk * c + lane;
-    const bool live = c >= 0 && t < len;
-    double d_in = 0.0, e_in = 0.0, own = 0.0;
+  for (int c = wave; c < n_chunks; c += WAVES) {
+    const int64_t t = kGdrChunk * (int64_t)c + lane;
+    const bool live = t < len;
+    double e_in = 0.0, own = 0.0;
     if (live) {
-      d_in = p.qdq[0][at + t];
       e_in = p.kdk[0][at + t];
       own = p.qdq[1][at + t] - (p.kdk[1][at + t] - e_in);
     }
-    double before = e_in;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double more = __shfl_down(own, d), less = __shfl_up(before, d);
-      if (lane + d < 64) own += more;
-      if (lane >= d) before += less;
-    }
-    const double e_sum = __shfl(before, 63), d_sum = wave_sum(d_in);
-    before -= e_in;
-    __syncthreads();   // the values of the turn before have been read
-    if (lane == 0) part[0][wave] = down ? d_sum - e_sum : e_sum - d_sum;
-    __syncthreads();
-    double mine = B;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (w < wave) mine += part[0][w];
-      B += part[0][w];
-    }
-    if (!one) mine -= down ? e_sum : d_sum;
-    if ((c == 0 && opens && !p.S0) || (c == n_chunks - 1 && closes && !p.dSf)) mine = 0.0;   // nothing enters, or nothing is behind
+    const double before = lane_prefix(e_in) - e_in, upto = lane_prefix(own);
+    own += last_lane(upto) - upto;   // from this token on
     if (!live) continue;
-    const double dg = mine + own + before;
+    const double dg = (size_down[c] < size_up[c] ? A_down[c] : A_up[c]) + own + before;
     if (p.w_per_head) total += dg;
     else {
       const int64_t tok = sg.t0 + first + t;
@@ -161,9 +201,10 @@ __global__ __launch_bounds__(256) void lad_decay_grad_kernel(LadDecayGrad p) {
     }
   }
   if (!p.w_per_head) return;
+  total = lane_sum(total);
+  if (lane == 0) part[0][wave] = total;
   __syncthreads();
-  total = block_sum(total, part[1]);
-  if (tid == 0) p.partial[slot * p.Hv + h] = total;
+  if (tid == 0) p.partial[slot * p.Hv + h] = all(part[0]);
 }
 
 // dw of a w per head: the segments' sums, in a fixed order
@@ -207,8 +248,16 @@ hipError_t launch_lad_scan(const LadScan& p, hipStream_t s) {
 
 hipError_t launch_lad_decay_grad(const LadDecayGrad& p, hipStream_t s) {
   const dim3 grid((unsigned)(p.slots * p.Hv));
-  if (p.dtype == KDA_DTYPE_BF16) hipLaunchKernelGGL(lad_decay_grad_kernel<uint16_t>, grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL(lad_decay_grad_kernel<float>, grid, dim3(256), 0, s, p);
+  const unsigned lds = (unsigned)(p.L / kGdrChunk) * (4 * sizeof(double) + 5 * sizeof(float));   // at most kLadMaxChunks: 52 KiB
+  // Few workgroups wait for their states from memory, and 16 wavefronts have more of them under way than 4 (2 x 4096 tokens, 160 of
+  // them: 25 and 16 us when this was chosen); many hide it behind one another, and wavefronts without a chunk of their own are in the way.
+  if (p.slots * p.Hv <= 1024) {
+    if (p.dtype == KDA_DTYPE_BF16) hipLaunchKernelGGL((lad_decay_grad_kernel<uint16_t, 16>), grid, dim3(1024), lds, s, p);
+    else hipLaunchKernelGGL((lad_decay_grad_kernel<float, 16>), grid, dim3(1024), lds, s, p);
+  } else {
+    if (p.dtype == KDA_DTYPE_BF16) hipLaunchKernelGGL((lad_decay_grad_kernel<uint16_t, 4>), grid, dim3(256), lds, s, p);
+    else hipLaunchKernelGGL((lad_decay_grad_kernel<float, 4>), grid, dim3(256), lds, s, p);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.w_per_head) return e;
   hipLaunchKernelGGL(lad_head_grad_kernel, dim3((unsigned)p.Hv), dim3(256), 0, s, p);

@@ -297,27 +297,11 @@ __device__ __forceinline__ float exp2_of(double x) {
   return exp2_two(hi, (float)(x - (double)hi));
 }
 
-// A value of a lane before (DPP control CTRL, into the rows of ROWS), 0 where there is none
-template <int CTRL, int ROWS> __device__ __forceinline__ double behind_lane(double x) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, x);
-  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
-  const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, false);
-  return __builtin_bit_cast(double, (uint64_t)(uint32_t)lo | ((uint64_t)(uint32_t)hi << 32));
-}
-
 // One wavefront: the gates of a chunk from its lanes' log-decays (0 behind the end), prefixes in units of ln 2.
 __device__ __forceinline__ void put_gates(Gates& out, float g, int lane, int reverse, float out_scale, float in_scale) {
   const double own = (double)g * 1.4426950408889634074;
-  double p = own;
-  p += behind_lane<0x111, 0xf>(p);   // 1, 2, 4, 8 lanes before, in rows of 16
-  p += behind_lane<0x112, 0xf>(p);
-  p += behind_lane<0x114, 0xf>(p);
-  p += behind_lane<0x118, 0xf>(p);
-  p += behind_lane<0x142, 0xa>(p);   // the last lane of rows 0 and 2 to rows 1 and 3
-  p += behind_lane<0x143, 0xc>(p);   // lane 31 to rows 2 and 3
-  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
-  const double tot = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)bits, 63) |
-                                                    ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), 63) << 32));
+  double p = lane_prefix(own);
+  const double tot = last_lane(p);
   p -= reverse ? own : 0.0;
   const float hi = (float)p, lo = (float)(p - (double)hi);
   const int place = key_place(lane);
