@@ -5,8 +5,8 @@
 //
 // NT lanes hold a row as 8 pairs each; a group of NT lanes keeps one token and walks its heads, so the sines of a
 // token's angles are formed once for all of them (64 pairs cost more than a row's trip through memory would).
-// Angles are products of the position and the fp32 frequency in double, reduced to turns there: a float's product is off
-// by 0.03 radians at position 10^6.
+// Angles are products of the position and the fp32 frequency in double, reduced to a turn there (a float's product is off
+// by 0.03 radians at position 10^6) and rounded once to fp32 for the sine and cosine: off by at most 2^-25 of a half turn.
 //
 // The gradient recomputes the norm from the same row; the weights' gradients are summed in registers over the rows that a
 // workgroup takes, and a second kernel adds up the workgroups in a fixed order.
@@ -39,7 +39,6 @@ template <int NT, bool NEAR, int FORM> struct Pairs {
       turn = turns || !live ? s : R / 2;
       a0 = NEAR ? 2 * s : turns || !live ? s : R + s;
       b0 = NEAR ? 2 * s + 1 : turns || !live ? s + R / 2 : R + s + kind;
-      if (!live && R == 0 && !NEAR) b0 = D / 2;
     }
   }
   __device__ __forceinline__ bool has(int j) const { return FORM == kSingle ? j * NT + t < D / 2 : live; }
@@ -193,7 +192,8 @@ __global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkNormParams p, int he
 }
 
 // blocks_q workgroups walk the queries' (tokens, heads) items, the others the keys'.  Registers for four wavefronts a SIMD:
-// with two more a lane there were three, and 16384 + 16384 rows' heads took 59 us in place of 49.
+// with two more a lane there were three, and 16384 + 16384 rows' heads took 59 us in place of 49.  For it the 16-byte forms keep
+// two to five registers in scratch.
 template <typename T, int NT, bool NEAR, int FORM>
 __global__ __launch_bounds__(256, FORM != kSingle ? 4 : 1) void qk_norm_bwd_kernel(QkNormParams p, int heads, int blocks_q) {
   constexpr int TOK = 256 / NT;
