@@ -138,10 +138,11 @@ namespace kda {
 //  - as many as workgroups run at once: two a compute unit, one of fp32 with a side of 128; the gradients' three walks
 //    take a third each, or half where their workgroups are small or long (fp32);
 //  - a chunk of a segment is some a us of a walk and of its state's (less with more segments), a segment's state some b us of
-//    the memory's time: n^2 = a / b times the chunks.  Two sequences of 2048 tokens, 16 heads of 128 x 128, bf16: 8, 11 (this
-//    rule) and 32 segments a head's forward 53, 56 and 81 us; of 4096 tokens 79, 79 (16) and 102; 64K tokens of one with 32
-//    422, with 16 470; gradients of 2 x 4096 with 5 177 us, with 4 191, with 11 194.  9 packed prompts, 4099 tokens, 16 heads: 30
-//    segments a head 63 us, 21 69, 41 75.  Within 5 % of the best of each sweep;
+//    the memory's time: n^2 = a / b times the chunks.  With decays of at most 0.02 a token, so that no head forgets early, two
+//    sequences of 2048 tokens, 16 heads of 128 x 128, bf16: 8, 11 (this rule) and 32 segments a head's forward 53, 56 and 81 us; of
+//    4096 tokens 8, 16 (this rule) and 32 79, 77 and 102; 64K tokens of one with 32 (this rule) 409, with 16 461; gradients of
+//    2 x 4096 with 5 (this rule) 178 us, with 4 194, 8 173, 11 197.  9 packed prompts, 4099 tokens, 16 heads: 30 segments a head
+//    62 us, 21 69, 41 75.  Within 5 % of the best of each sweep;
 //  - the chain over a sequence's segments is serial: c chunks each at least, c^2 = T / 1250.
 // The gradients' segments have at most 16 chunks where the chain allows it, also where fewer would fill the machine: the
 // decay's gradient starts from <S, R> at their ends, and carried over more than that it takes rounding from far away
@@ -269,7 +270,9 @@ int kda_lad_chunk_bwd(const void* q, const void* k, const void* v, const void* w
   LadParams p = params(desc, pl, w, seq_start);
   const Tensor rq{q, desc->q, pl.grp}, rk{k, desc->k, pl.grp}, rv{v, desc->v, 1}, rdo{dO, sdo, 1};
   // Sequences of several segments have their states formed and chained first.  A single segment's walks take the entering
-  // states as they are given and leave S behind the last token and dS0 themselves, in three planes, for two launches less.
+  // states as they are given and leave S behind the last token and dS0 themselves, in three planes, for two launches less
+  // (64 tokens of 4 heads: 34 -> 25 us).  Many short rows pay for the planes: 16 heads of 128 x 128 in bf16, without dS0 and with
+  // it, 16 x 64 tokens 28 and 46 us, 64 x 192 tokens 184 and 339, 512 x 64 tokens 550 and 1115.
   const bool segments = T > pl.L;
   // <S, R> behind the last token and in front of the first
   const bool want_end = dS_final && grads->dw, want_start = S0 && grads->dw;

@@ -18,8 +18,8 @@
 // What bounds it, at 128 x 128 in bf16: chunks of one segment follow one another, 5 us each where a workgroup is alone (130
 // tokens of 4 heads: 21 us), 8.6 us with two workgroups on a compute unit.  64K tokens of 16 heads: outputs 276 us (4.1 TB/s, matrix
 // cores 30 % busy, the rest vector work on planes and trips to LDS), states 132 us, 4.1 a chunk; the gradients' three walks of
-// 2 x 4096 tokens 127 us.  Two workgroups a compute unit take each other's barriers and trips to memory behind their
-// products (with rows read without branches: 64K tokens' forward 540 -> 490 us).
+// 2 x 4096 tokens 127 us (in a trace, each kernel on an idle machine).  Two workgroups a compute unit take each other's barriers
+// and trips to memory behind their products (with rows read without branches: 64K tokens' forward 540 -> 490 us).
 #pragma once
 
 #include "lad_internal.h"
@@ -227,6 +227,8 @@ struct Gates {
 
 template <typename T, int DX, int DZ, int PL, int MODE> struct Lds {
   static constexpr int kWaves = DZ / 32;
+  // A wavefront's part of out . dot, 32 columns: in fp32 where the decay's gradient is rounded to bf16, whose step is far above
+  // what these sums lose; added up over the wavefronts and the tokens in double.
   using Dot = std::conditional_t<sizeof(T) == 4 || PL == 3, double, float>;
   Tile<T, DX> y;
   Tile<T, DZ> z;
@@ -758,7 +760,8 @@ hipError_t launch_walk_one(const LadParams& p, hipStream_t s) {
   constexpr bool kBoth = MODE >= lad::kDots && DX != DZ;
   constexpr int kLdsBytes = kBoth && kOther > kOne ? kOther : kOne, kSide = kBoth && DX > DZ ? DX : DZ;
   // Two workgroups a compute unit where registers and LDS allow it; a single wavefront's 32 columns beside 128 need more than
-  // half of a SIMD's registers for the rows under way.
+  // half of a SIMD's registers for the rows under way.  The gradients of 64 x 128 and 128 x 64 keep 4 and 7 registers in scratch for
+  // it (2 x 4096 tokens, 16 heads: 158 and 146 us, with one workgroup 203 and 193); those of 32 x 128 in fp32 do at any rate.
   constexpr int OCC = sizeof(T) == 2 && kSide == 128 && PL == 2 && !(kBoth && DX + DZ == 160) ? 2 : 1;
   void (*kernel)(LadParams);
   if constexpr (kBoth) kernel = lad_walks_kernel<T, DX, DZ, UP, PL, MODE, OCC>;

@@ -228,7 +228,7 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     q: [B,Hq,T,D]; k: [B,Hk,T,D] or None (bf16 or fp32, any strides with a contiguous last dimension; D even, up to
     1024).  norm False leaves out the division, a weight of None the product; weights [D], both bf16 or both fp32.
     positions: int32 or int64, [B,T] or [T]; inv_freq: fp32 [R/2], R <= D: pair i of a row is values i and i + R/2, or 2i
-    and 2i + 1 with `interleaved`; both None leave out the rotation.  Angles are formed in 64 bits.  Rows of unit
+    and 2i + 1 with `interleaved`; both None leave out the rotation.  Angles are formed in 64 bits and rounded once.  Rows of unit
     length, as a delta rule's keys, are those without a weight at a scale of D ** -0.5.  Outputs lie apart from every
     input (nothing is done in place).  Asynchronous on `stream`."""
     if stream is not None:

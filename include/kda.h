@@ -379,8 +379,8 @@ KDA_API size_t kda_norm_bwd_workspace_bytes(const kda_norm_t* desc);
  * Tensors, strides, packed sequences, aliasing and their limits are those of the head-gated rule above (there is no
  * beta).  Evaluated in chunks of 64 tokens, long sequences in segments side by side: a NaN or infinity in a token may
  * reach the other tokens of its chunk and segment and every later one (in the gradients every earlier one too), never
- * another sequence.  bf16: inputs are exact operands; what is computed is carried as a sum of two or three, so a result
- * is off by its own rounding and states are fp32's. */
+ * another sequence.  bf16: inputs are exact operands; what is computed is carried as a sum of two (off by 2^-17) where only
+ * results in bf16 are taken from it, else of three, so a result is off by its own rounding and states are fp32's. */
 typedef struct {
   int64_t B, Hk, Hv, T, dk, dv; /* Hk divides Hv; dk, dv in {32, 64, 128}; 0 <= T < 2^31 */
   int64_t n_seq;                /* packed sequences (0 without seq_start) */
@@ -429,7 +429,8 @@ KDA_API int kda_lad_decode(const void* q, const void* k, const void* v, const vo
  *     y = scale * (n, its first R values rotated in pairs by the angles p * inv_freq[i], i < R / 2)
  *     (a, b) -> (a cos - b sin, b cos + a sin);  rms(t) = sqrt(mean(t^2) + eps)
  * Pair i is values i and i + R/2, or 2i and 2i + 1 with desc->interleaved.  R = 0: no rotation (positions and
- * inv_freq are not read).  Angles are products in 64 bits, so far positions keep their accuracy.
+ * inv_freq are not read).  Angles are products in 64 bits, so far positions keep their accuracy, and are rounded to fp32
+ * once, as a part of a turn.
  * q, q_out [B,Hq,T,D], k, k_out [B,Hk,T,D]: of dtype, any strides with the last dimension contiguous (Hk may be
  * 0: no keys); weights dense [D] of wdtype; positions [B,T], int32 or int64 with strides in elements;
  * inv_freq dense fp32 [R/2].  D even, at most KDA_QK_NORM_MAX_D; R even, at most D.  An output may not hold
