@@ -57,7 +57,8 @@ __global__ __launch_bounds__(256) void lad_scan_kernel(LadScan p) {
 // nothing enters or nothing lies behind), so A is carried from either end.  Every sum that goes into it leaves its rounding
 // there, also where the head has forgotten what made it large, so each chunk takes the end whose values on the way were smaller.
 // And A_c has the chunk's whole decay as a factor: where 0 is nearer to it than the rounding of what is carried (a
-// reset, a decay of more than a half a token), it is 0 and both ways start anew.  Between a part that forgets and one that remembers
+// reset, a decay of more than a half a token), it is 0 and both ways start anew; unless what is carried stands out of its rounding
+// (masked tokens between two states: <S, R> is all there is).  Between a part that forgets and one that remembers
 // (2048 tokens, decays of 2 and 1/2048 a token, fp32) the first one's gradients were off by 1.7e-3 where A came from the far end.
 // A segment of one chunk has A = e^{decay} <S entering, R from behind>, without any difference.  All in double; a wavefront
 // takes a chunk.  Bound by the states' trip from memory (2 x 4096 tokens, 160 segments of 128 x 128, four states each: 12.9 us).
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(64 * WAVES) void lad_decay_grad_kernel(LadDecayGrad
         double A = B - near_sum[c];
         size += near_size[c];
         const float to_zero = kept[c] == 0.f ? 0.f : kept[c] * far;
-        if (to_zero < size) {
+        if (to_zero < size && fabs(A) <= 0x1p-12 * (double)size) {   // and what is carried does not say that it is more
           A = 0.0;
           size = to_zero;
         }

@@ -106,3 +106,22 @@ def test_packed_sequences_that_forget_and_remember(kind, dtype):
     one["w"] = one["w"].clamp(min=-1e4)
     _, _, ref = reference(one, lens, gate="log", grads=True)
     compare(got[3][:, :of], ref["dw"], bounds + [(1100, T)], dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [130, 1100])
+@pytest.mark.parametrize("empty", [("q", "k"), ("q",), ("k",)])
+def test_tokens_that_neither_read_nor_write(empty, T, dtype):
+    """Masked tokens (q or k zero, or both) between two states: dw is <S, R> alone, all of it behind a chunk that forgets nearly
+    everything (e^-45)."""
+    say(f"[case] lad dw of masked tokens {empty} {T} {dtype}")
+    d = make(2, T, 2, 2, 64, 64, dtype, "log", seed=52, states=2)
+    for n in empty:
+        d[n].zero_()
+    d["w"].fill_(-1.0 / 2048)
+    d["w"][:, :, :64] = -0.7
+    t = gpu(d)
+    got = lad_chunk_bwd(*(t[n] for n in ROWS), t["S0"], t["dS_final"], **gate_args("log"))
+    torch.cuda.synchronize()
+    _, _, ref = reference(d, gate="log", grads=True)
+    compare(got[3], ref["dw"], [(0, 64), (64, T)], dtype)
